@@ -60,6 +60,7 @@ enum {
 };
 
 enum { MOE_NN = 0, MOE_NT = 1 };
+enum { MOE_F32 = 0, MOE_BF16 = 1 }; /* element type of an argument that may be either */
 enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU = 1, MOE_EPI_SWIGLU_BWD = 2 };
 
 /* Text of a status code (static storage). */
@@ -313,6 +314,111 @@ int moe_route_bwd(const moe_shape_t* shape, const moe_bf16_t* x, const float* wr
                   const float* topk_w, const float* dtopk_w, const int32_t* sorted_slot,
                   const int32_t* group_offsets, float* dwr, float* dbias, moe_bf16_t* dx, void* ws, size_t ws_bytes,
                   moe_stream_t stream);
+
+/*
+ * moe_route_scored -- routing by scores: softmax or sigmoid of the logits, a
+ * balance bias that steers the choice only, choice among the best groups of
+ * experts, and weights that are the picked scores.
+ *  logits [T, E] fp32 or bf16 (logits_type); balance_bias [E] fp32 or NULL.
+ *  Scores s = softmax(logits[t]) or sigmoid(logits[t]); choice values
+ *  c = s + balance_bias. An expert whose logit or bias is -inf or NaN is
+ *  disabled: c = -inf, and its softmax score is 0 if the logit is the cause.
+ *  Groups: expert e belongs to group e / (E / n_group). With topk_group <
+ *  n_group a group's value is the sum of the group_top (1 or 2) largest c of
+ *  its enabled experts (of as many as there are; -inf if none), and the
+ *  topk_group groups of the largest value stay, ties going to the lower group.
+ *  Picks: the k enabled experts of the largest c in the groups that stay, in
+ *  descending order, ties to the lower id; where fewer are left, the lowest
+ *  other ids follow, with weight 0. The k picks of a token are distinct.
+ *  Weights: w = s at the picks; renorm: divided by their sum (0 where the sum
+ *  is 0); times scale.
+ * Choice values are compared in 64 bits, and without a bias experts (and
+ * groups with group_top 1) are compared by their logits; weights are rounded
+ * once to fp32 from more than 32 bits.
+ *  Needs E % n_group == 0, 1 <= topk_group <= n_group, group_top 1 or 2 and
+ *  at most E / n_group, k <= topk_group * (E / n_group), scale finite and > 0.
+ *
+ * moe_route_scored_bwd -- its gradient with the picks held fixed: dlogits
+ *  [T, E] (of the logits' type, every element written) from topk_idx, topk_w
+ *  of the forward and g = dtopk_w [T, k] fp32. A pick of weight 0 takes no
+ *  part. With q = w / scale and D = sum_j g_j q_j:
+ *   renorm, softmax: dl_j = w_j (g_j - D)       renorm, sigmoid: times (1 - s_j)
+ *   sigmoid:         dl_j = w_j (1 - s_j) g_j
+ *   softmax:         dl_e = [e picked] w_e g_e - s_e sum_j w_j g_j   (every e)
+ *  and 0 elsewhere. Only score, renorm and scale of the router are used. The
+ *  logits' own producer goes on from here (x^T dlogits, dlogits wr^T).
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+  int32_t score;      /* MOE_SCORE_* */
+  int32_t n_group;    /* groups of experts (1: no groups) */
+  int32_t topk_group; /* groups that stay */
+  int32_t group_top;  /* choice values summed into a group's value: 1 or 2 */
+  int32_t renorm;     /* nonzero: weights divided by their sum */
+  float scale;        /* factor of the weights */
+} moe_router_t;
+int moe_route_scored(const moe_shape_t* shape, const moe_router_t* router, const void* logits, int32_t logits_type,
+                     const float* balance_bias, int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+int moe_route_scored_bwd(const moe_shape_t* shape, const moe_router_t* router, const void* logits,
+                         int32_t logits_type, const int32_t* topk_idx, const float* topk_w, const float* dtopk_w,
+                         void* dlogits, moe_stream_t stream);
+
+/*
+ * 8-bit activation checkpoints, in the OCP microscaling format with INT8
+ * elements: 32 consecutive elements of a row share a power-of-two scale code
+ * c, an element is an integer code in [-127, 127] worth code * 2^(c-133).
+ * c = floor(log2(amax)) + 127 clamped to [1, 254]; the code is v / 2^(c-133)
+ * rounded to nearest, ties to even, saturating. So an element is off by at
+ * most half a step (one step where it saturates, past 127.5 steps). A block
+ * with a NaN or an infinity gets c = 255, codes 0, and reads back as NaN.
+ * Every finite value held is a bf16 number.
+ *  codes [rows, K] int8, scales [rows, K/32] bytes. K % 32 == 0.
+ *
+ * moe_ckpt_quantize -- rows src [M, K] fp32 or bf16 (src_type) to codes and
+ *  scales.
+ * moe_ckpt_dequantize -- back to dst [M, K] fp32 or bf16 (dst_type): row r is
+ *  source row row_index[r] / row_div, clamped into [0, src_rows), when
+ *  row_index [M] is given (sorted_slot with row_div = k gives the
+ *  expert-sorted rows of token checkpoints), else row r (src_rows must be M).
+ */
+int moe_ckpt_quantize(const void* src, int32_t src_type, int64_t M, int32_t K, int8_t* codes, uint8_t* scales,
+                      moe_stream_t stream);
+int moe_ckpt_dequantize(const int8_t* codes, const uint8_t* scales, int64_t src_rows, int32_t K,
+                        const int32_t* row_index, int32_t row_div, int64_t M, void* dst, int32_t dst_type,
+                        moe_stream_t stream);
+
+/*
+ * moe_swiglu_bwd_ckpt -- the SwiGLU backward from an 8-bit checkpoint of
+ *  h = [gate | up] (codes [M, 2*mlp], scales [M, 2*mlp/32]). For row r with
+ *  q = row_slot[r] (row_slot [M] a permutation of 0..M-1, or NULL: q = r),
+ *  w = slot_scale[q] (slot_scale [M] fp32, or NULL: 1), da [M, mlp] bf16 the
+ *  gradient of the unscaled SwiGLU output, and s = sigmoid(g):
+ *   a[r]  = g s u                                   [M, mlp] bf16 (NULL: not wanted)
+ *   dh[r] = [w da u s (1 + g (1 - s)) | w da g s]   [M, 2*mlp] bf16
+ *   dslot_scale[q] = sum_m da[m] (g s u)[m]         [M] fp32 (NULL: not wanted), unrounded a
+ *  A row whose row_slot lies outside [0, M) is taken with w = 0 and writes no
+ *  dslot_scale. mlp % 32 == 0, M < 2^31.
+ */
+int moe_swiglu_bwd_ckpt(int64_t M, int32_t mlp, const moe_bf16_t* da, const int8_t* h_codes, const uint8_t* h_scales,
+                        const int32_t* row_slot, const float* slot_scale, moe_bf16_t* dh, moe_bf16_t* a,
+                        float* dslot_scale, moe_stream_t stream);
+
+/*
+ * moe_grouped_gemm_wgrad_ckpt -- moe_grouped_gemm_wgrad with the left operand
+ *  held as an 8-bit checkpoint, read through a row mapping: for every expert
+ *  e, C[e] [P, Q] = sum over rows r of group e of X[row(r)]^T D[r], X being
+ *  A_codes [a_rows, P] with A_scales [a_rows, P/32] and row(r) =
+ *  row_slot[r] / slot_div clamped into [0, a_rows) (row_slot [M]; token rows
+ *  checkpointed once, read through sorted_slot with slot_div = k), or r
+ *  without row_slot (a_rows must be M). D [M, Q] bf16, C [E, P, Q] bf16,
+ *  fp32 accumulate; the values of X enter the products unrounded. An empty
+ *  group gives exact zeros. P % 32 == 0, Q % 8 == 0, a_rows * P < 2^31,
+ *  M < 2^31.
+ */
+int moe_grouped_gemm_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows,
+                                const int32_t* row_slot, int32_t slot_div, const moe_bf16_t* D,
+                                const int32_t* group_offsets, int32_t E, int64_t M, int32_t P, int32_t Q,
+                                moe_bf16_t* C, moe_stream_t stream);
 
 /*
  * MXFP8 ("[DRAFT][JAX] Optimize MoE block", Changes: MXFP8 quantization in

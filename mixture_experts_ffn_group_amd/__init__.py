@@ -7,6 +7,9 @@ the C ABI in include/moe_ffn.h:
 
     route, permute, grouped_gemm, grouped_gemm_wgrad, combine, combine_bwd,
     ffn_fwd, ffn_bwd
+    route_scored, route_scored_bwd: routing by scores, groups and a balance bias
+    ckpt_quantize, ckpt_dequantize, swiglu_bwd_ckpt, grouped_gemm_wgrad_ckpt:
+    activations kept in 8 bits between the passes
 
 Tensors: bf16 activations/weights, fp32 router weights/logits/top-k weights,
 int32 indices, all contiguous and on one CUDA (HIP) device.
@@ -22,7 +25,8 @@ from ._lib import (MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_BWD, MOE_NN, MOE
                    MoeGemmRows, MoeSaved, MoeShape)
 
 __all__ = ["route", "permute", "grouped_gemm", "grouped_gemm_wgrad", "combine", "combine_bwd", "ffn_fwd", "ffn_bwd",
-           "query_support", "workspace_bytes", "MoeError"]
+           "route_scored", "route_scored_bwd", "ckpt_quantize", "ckpt_dequantize", "swiglu_bwd_ckpt",
+           "grouped_gemm_wgrad_ckpt", "query_support", "workspace_bytes", "MoeError"]
 
 _EPI = {"none": MOE_EPI_NONE, "swiglu": MOE_EPI_SWIGLU, "swiglu_bwd": MOE_EPI_SWIGLU_BWD}
 _OP = {"nn": MOE_NN, "nt": MOE_NT}
@@ -415,3 +419,159 @@ def ffn_fwd_mx(x: torch.Tensor, wq: dict, k: int, wr: torch.Tensor | None = None
                                          _ptr(wq["wo_scales"]), _ptr(y), _ptr(ws), ws.numel(), _stream(dev)),
                "moe_ffn_fwd_mx")
     return y
+
+
+_SCORE = {"softmax": _lib.MOE_SCORE_SOFTMAX, "sigmoid": _lib.MOE_SCORE_SIGMOID}
+_TYPE = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16}
+
+
+def _need_like(t, name, shape, dtype, device):
+    """_need, with the shape checked too (the kernels index by the sizes they are given)."""
+    _need(t, name, dtype, device)
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_typed(t, name, ndim):
+    """A float32 or bfloat16 tensor of ndim dimensions; returns its MOE_* type."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPE:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    _need(t, name, t.dtype)
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    return _TYPE[t.dtype]
+
+
+def _router(score, n_group, topk_group, group_top, renorm, scale):
+    if score not in _SCORE:
+        raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
+    return _lib.MoeRouter(_SCORE[score], n_group, topk_group, group_top, int(bool(renorm)), scale)
+
+
+def route_scored(k: int, logits: torch.Tensor, balance_bias: torch.Tensor | None = None, score: str = "softmax",
+                 n_group: int = 1, topk_group: int = 1, group_top: int = 1, renorm: bool = True,
+                 scale: float = 1.0):
+    """Routing by scores (see moe_route_scored): (topk_idx [T, k] int32, topk_w [T, k] fp32) of logits [T, E]
+    fp32 or bf16. balance_bias [E] fp32 steers the choice and leaves the weights alone; with topk_group < n_group
+    the picks come from the topk_group groups of the largest sums of their group_top best choice values."""
+    ty = _need_typed(logits, "logits", 2)
+    dev = logits.device
+    T, E = logits.shape
+    _need_like(balance_bias, "balance_bias", (E,), torch.float32, dev)
+    r = _router(score, n_group, topk_group, group_top, renorm, scale)
+    s = _lib.shape(T, 64, 64, E, k)
+    with torch.cuda.device(dev):
+        idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+        _lib.check(_lib.lib().moe_route_scored(C.byref(s), C.byref(r), _ptr(logits), ty, _ptr(balance_bias),
+                                               _ptr(idx), _ptr(w), _stream(dev)), "moe_route_scored")
+    return idx, w
+
+
+def route_scored_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, dtopk_w: torch.Tensor,
+                     score: str = "softmax", renorm: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """dlogits [T, E], of the logits' type, from the gradient of route_scored's weights (moe_route_scored_bwd);
+    score, renorm and scale as in the forward."""
+    ty = _need_typed(logits, "logits", 2)
+    dev = logits.device
+    T, E = logits.shape
+    _need(topk_idx, "topk_idx", torch.int32, dev)
+    k = topk_idx.shape[1] if topk_idx.dim() == 2 else -1
+    _need_like(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+    _need_like(topk_w, "topk_w", (T, k), torch.float32, dev)
+    _need_like(dtopk_w, "dtopk_w", (T, k), torch.float32, dev)
+    r = _router(score, 1, 1, 1, renorm, scale)
+    s = _lib.shape(T, 64, 64, E, k)
+    with torch.cuda.device(dev):
+        d = torch.empty_like(logits)
+        _lib.check(_lib.lib().moe_route_scored_bwd(C.byref(s), C.byref(r), _ptr(logits), ty, _ptr(topk_idx),
+                                                   _ptr(topk_w), _ptr(dtopk_w), _ptr(d), _stream(dev)),
+                   "moe_route_scored_bwd")
+    return d
+
+
+def ckpt_quantize(src: torch.Tensor):
+    """8-bit checkpoint of rows src [M, K] fp32 or bf16 (see moe_ckpt_quantize): (codes [M, K] int8,
+    scales [M, K/32] uint8). K must be a multiple of 32."""
+    ty = _need_typed(src, "src", 2)
+    M, K = src.shape
+    with torch.cuda.device(src.device):
+        codes = torch.empty((M, K), dtype=torch.int8, device=src.device)
+        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=src.device)
+        _lib.check(_lib.lib().moe_ckpt_quantize(_ptr(src), ty, M, K, _ptr(codes), _ptr(scales),
+                                                _stream(src.device)), "moe_ckpt_quantize")
+    return codes, scales
+
+
+def _need_ckpt(codes, scales, name, dev):
+    _need(codes, f"{name}codes", torch.int8, dev)
+    if codes.dim() != 2:
+        raise ValueError(f"{name}codes must have 2 dimensions, got shape {tuple(codes.shape)}")
+    _need_like(scales, f"{name}scales", (codes.shape[0], codes.shape[1] // 32), torch.uint8, dev)
+
+
+def ckpt_dequantize(codes: torch.Tensor, scales: torch.Tensor, row_index: torch.Tensor | None = None,
+                    row_div: int = 1, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Values of an 8-bit checkpoint as rows [M, K] of dtype (bf16 holds them exactly); with row_index [M] int32,
+    row r is checkpoint row row_index[r] // row_div (see moe_ckpt_dequantize)."""
+    _need_ckpt(codes, scales, "", None)
+    dev = codes.device
+    if dtype not in _TYPE:
+        raise TypeError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+    R, K = codes.shape
+    _need(row_index, "row_index", torch.int32, dev)
+    M = R if row_index is None else row_index.numel()
+    with torch.cuda.device(dev):
+        dst = torch.empty((M, K), dtype=dtype, device=dev)
+        _lib.check(_lib.lib().moe_ckpt_dequantize(_ptr(codes), _ptr(scales), R, K, _ptr(row_index), row_div, M,
+                                                  _ptr(dst), _TYPE[dtype], _stream(dev)), "moe_ckpt_dequantize")
+    return dst
+
+
+def swiglu_bwd_ckpt(da: torch.Tensor, h_codes: torch.Tensor, h_scales: torch.Tensor,
+                    row_slot: torch.Tensor | None = None, slot_scale: torch.Tensor | None = None,
+                    want_a: bool = True, want_dscale: bool = True):
+    """SwiGLU backward from an 8-bit h (see moe_swiglu_bwd_ckpt): (dh [M, 2*mlp] bf16, a [M, mlp] bf16 or None,
+    dslot_scale [M] fp32 or None) from da [M, mlp] bf16; row_slot [M] int32 maps rows to entries of slot_scale [M]
+    and dslot_scale."""
+    _need(da, "da", torch.bfloat16)
+    dev = da.device
+    if da.dim() != 2:
+        raise ValueError(f"da must have 2 dimensions, got shape {tuple(da.shape)}")
+    M, mlp = da.shape
+    _need_ckpt(h_codes, h_scales, "h_", dev)
+    _need_like(h_codes, "h_codes", (M, 2 * mlp), torch.int8, dev)
+    _need_like(row_slot, "row_slot", (M,), torch.int32, dev)
+    _need_like(slot_scale, "slot_scale", (M,), torch.float32, dev)
+    with torch.cuda.device(dev):
+        dh = torch.empty((M, 2 * mlp), dtype=torch.bfloat16, device=dev)
+        a = torch.empty((M, mlp), dtype=torch.bfloat16, device=dev) if want_a else None
+        ds = torch.empty(M, dtype=torch.float32, device=dev) if want_dscale else None
+        _lib.check(_lib.lib().moe_swiglu_bwd_ckpt(M, mlp, _ptr(da), _ptr(h_codes), _ptr(h_scales), _ptr(row_slot),
+                                                  _ptr(slot_scale), _ptr(dh), _ptr(a), _ptr(ds), _stream(dev)),
+                   "moe_swiglu_bwd_ckpt")
+    return dh, a, ds
+
+
+def grouped_gemm_wgrad_ckpt(a_codes: torch.Tensor, a_scales: torch.Tensor, D: torch.Tensor,
+                            group_offsets: torch.Tensor, E: int, row_slot: torch.Tensor | None = None,
+                            slot_div: int = 1) -> torch.Tensor:
+    """C [E, P, Q] = per-group X^T D with X an 8-bit checkpoint [R, P] (see moe_grouped_gemm_wgrad_ckpt); with
+    row_slot [M] int32, row r of the product reads X row row_slot[r] // slot_div."""
+    _need_ckpt(a_codes, a_scales, "a_", None)
+    dev = a_codes.device
+    _need(D, "D", torch.bfloat16, dev)
+    if D.dim() != 2:
+        raise ValueError(f"D must have 2 dimensions, got shape {tuple(D.shape)}")
+    M, Q = D.shape
+    R, P = a_codes.shape
+    _need_like(row_slot, "row_slot", (M,), torch.int32, dev)
+    _need_like(group_offsets, "group_offsets", (E + 1,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        C_ = torch.empty((max(E, 0), P, Q), dtype=torch.bfloat16, device=dev)
+        _lib.check(_lib.lib().moe_grouped_gemm_wgrad_ckpt(_ptr(a_codes), _ptr(a_scales), R, _ptr(row_slot), slot_div,
+                                                          _ptr(D), _ptr(group_offsets), E, M, P, Q, _ptr(C_),
+                                                          _stream(dev)), "moe_grouped_gemm_wgrad_ckpt")
+    return C_

@@ -18,6 +18,8 @@ MOE_OK = 0
 MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP, MOE_ERR_ALIGN = 1, 2, 3, 4, 5, 6
 MOE_NN, MOE_NT = 0, 1
 MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_BWD = 0, 1, 2
+MOE_F32, MOE_BF16 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_SCHED_GEMM, MOE_SCHED_GEMM_SWIGLU, MOE_SCHED_WGRAD = 0, 1, 2
 
 # Every function the header declares, with its ctypes signature.
@@ -39,7 +41,13 @@ class MoeGemmRows(C.Structure):
                 ("slot_scale", C.c_void_p)]
 
 
+class MoeRouter(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("score", "n_group", "topk_group", "group_top", "renorm")] + \
+               [("scale", C.c_float)]
+
+
 _SHP = C.POINTER(MoeShape)
+_RTR = C.POINTER(MoeRouter)
 SIGNATURES = {
     "moe_status_str": ([C.c_int], C.c_char_p),
     "moe_last_error_detail": ([], C.c_char_p),
@@ -68,6 +76,12 @@ SIGNATURES = {
                             C.c_int),
     "moe_mx_quantize_rows": ([_p, _i64, _i32, _p, _i32, _i64, _p, _p, _p], C.c_int),
     "moe_mx_quantize_weight": ([_p, _i32, _i32, _i32, _p, _p, _p], C.c_int),
+    "moe_route_scored": ([_SHP, _RTR, _p, _i32, _p, _p, _p, _p], C.c_int),
+    "moe_route_scored_bwd": ([_SHP, _RTR, _p, _i32, _p, _p, _p, _p, _p], C.c_int),
+    "moe_ckpt_quantize": ([_p, _i32, _i64, _i32, _p, _p, _p], C.c_int),
+    "moe_ckpt_dequantize": ([_p, _p, _i64, _i32, _p, _i32, _i64, _p, _i32, _p], C.c_int),
+    "moe_swiglu_bwd_ckpt": ([_i64, _i32, _p, _p, _p, _p, _p, _p, _p, _p, _p], C.c_int),
+    "moe_grouped_gemm_wgrad_ckpt": ([_p, _p, _i64, _p, _i32, _p, _p, _i32, _i64, _i32, _i32, _p, _p], C.c_int),
     "moe_route_bwd": ([_SHP, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
 }
 

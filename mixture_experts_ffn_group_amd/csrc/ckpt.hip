@@ -1,0 +1,270 @@
+// Activation checkpoints in 8 bits, and the elementwise half of their use in
+// the layer's backward pass.
+//
+// Format (OCP microscaling, INT8 elements): 32 consecutive elements of a row
+// share a power-of-two scale held as E8M0 (code c is 2^(c-127)); an element is
+// an integer code in [-127, 127] worth code * 2^-6 * 2^(c-127). c is
+// floor(log2(amax)) + 127 clamped to [1, 254], the code is v / step rounded to
+// nearest (ties to even), step = 2^(c-133). An element is off by at most half
+// a step, 2^-7 of the block's largest power of two (one step for a magnitude
+// past 127.5 steps, which saturates). Integers rather than E4M3 elements: the
+// step is the same over a block, so a normal row comes back with about a third
+// of E4M3's error at the same 8.25 bits an element. Every value is a bf16
+// number (7 significant bits and a power of two), so reading back into bf16
+// rounds nothing. A block with a NaN or an infinity gets c = 255 and reads
+// back as NaN.
+//
+// Layout: codes [rows][K] int8, scales [rows][K/32] bytes, both as the row lies.
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+// 2^(c-133) of a scale code, NaN for 255: 2^(c-127) is the float with exponent field c.
+__device__ __forceinline__ float ckpt_step(uint32_t c) {
+  return __uint_as_float(c == 255 ? 0x7fc00000u : c << 23) * 0.015625f;
+}
+
+__device__ __forceinline__ int ckpt_scale_code(uint32_t amax_bits) {
+  const int c = (int)(amax_bits >> 23);  // floor(log2) + 127; 0 for zero and subnormals
+  return c < 1 ? 1 : c;                  // 255 where amax is inf or NaN
+}
+__device__ __forceinline__ int ckpt_code(float v, int ex) {
+  return (int)fminf(fmaxf(rintf(ldexpf(v, ex)), -127.0f), 127.0f);
+}
+
+// Eight consecutive elements of a row per thread; four threads share a block.
+template <bool BF16>
+__global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restrict__ src, int64_t n8,
+                                                            int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  // n8 is a multiple of 4, so a block's four threads are in or out together
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+    float x[8];
+    if (BF16) {
+      const u32x4_t v = ld16(static_cast<const uint16_t*>(src) + i * 8);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        x[2 * m] = bf16_lo(v[m]);
+        x[2 * m + 1] = bf16_hi(v[m]);
+      }
+    } else {
+      const f32x4_t* f = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(src) + i * 8);
+      const f32x4_t a = f[0], b = f[1];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        x[m] = a[m];
+        x[4 + m] = b[m];
+      }
+    }
+    uint32_t am = 0;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) am = max(am, __float_as_uint(x[m]) & 0x7fffffffu);
+    am = max(am, (uint32_t)__shfl_xor((int)am, 1));
+    am = max(am, (uint32_t)__shfl_xor((int)am, 2));
+    const int c = ckpt_scale_code(am);
+    u32x2_t o;
+    if (c == 255) {
+      o = u32x2_t{0u, 0u};
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) w |= ((uint32_t)ckpt_code(x[4 * h + m], 133 - c) & 0xffu) << (8 * m);
+        o[h] = w;
+      }
+    }
+    *reinterpret_cast<u32x2_t*>(codes + i * 8) = o;
+    if ((i & 3) == 0) scales[i >> 2] = (uint8_t)c;
+  }
+}
+
+// Eight elements per thread of destination row r, from source row row_index[r] / row_div (clamped) or r.
+template <bool BF16>
+__global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales, int64_t src_rows,
+                                                              int K, const int32_t* __restrict__ row_index,
+                                                              int row_div, int64_t M, void* __restrict__ dst) {
+  const int per_row = K / 8;
+  const int64_t n = M * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per_row;
+    const int c8 = (int)(i - r * per_row);
+    int64_t sr = r;
+    if (row_index) {
+      sr = row_index[r] / row_div;
+      sr = sr < 0 ? 0 : (sr >= src_rows ? src_rows - 1 : sr);
+    }
+    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(codes + sr * K + (int64_t)c8 * 8);
+    const float step = ckpt_step(scales[sr * (K / 32) + (c8 >> 2)]);
+    float x[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) x[m] = (float)((int32_t)(v[m >> 2] << (24 - 8 * (m & 3))) >> 24) * step;
+    if (BF16) {
+      u32x4_t o;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) o[m] = pack_bf16x2(x[2 * m], x[2 * m + 1]);
+      st16(static_cast<uint16_t*>(dst) + i * 8, o);
+    } else {
+      f32x4_t* f = reinterpret_cast<f32x4_t*>(static_cast<float*>(dst) + i * 8);
+      f[0] = f32x4_t{x[0], x[1], x[2], x[3]};
+      f[1] = f32x4_t{x[4], x[5], x[6], x[7]};
+    }
+  }
+}
+
+// SwiGLU backward from the 8-bit h = [gate | up] of row r, one wave a row.
+// q = row_slot[r] (or r), w = slot_scale[q] (or 1), s = sigmoid(g):
+//   a = g s u,  dh = [w da u s (1 + g (1 - s)) | w da g s],  dslot_scale[q] = sum_m da a (a unrounded)
+__global__ __launch_bounds__(256) void swiglu_bwd_ckpt_kernel(int64_t M, int mlp, const uint16_t* __restrict__ da,
+                                                              const int8_t* __restrict__ hc,
+                                                              const uint8_t* __restrict__ hs,
+                                                              const int32_t* __restrict__ row_slot,
+                                                              const float* __restrict__ slot_scale,
+                                                              uint16_t* __restrict__ dh, uint16_t* __restrict__ a,
+                                                              float* __restrict__ dscale) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int nch = mlp / 8;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < M; r += (int64_t)gridDim.x * 4) {
+    int64_t q = row_slot ? row_slot[r] : r;
+    const bool inside = q >= 0 && q < M;
+    const float w = inside ? (slot_scale ? slot_scale[q] : 1.0f) : 0.0f;
+    float dot = 0.0f;
+    for (int c = lane; c < nch; c += 64) {
+      const u32x4_t dv = ld16(da + r * mlp + c * 8);
+      const u32x2_t gv = *reinterpret_cast<const u32x2_t*>(hc + r * 2 * mlp + c * 8);
+      const u32x2_t uv = *reinterpret_cast<const u32x2_t*>(hc + r * 2 * mlp + mlp + c * 8);
+      const float gst = ckpt_step(hs[r * (mlp / 16) + (c >> 2)]);
+      const float ust = ckpt_step(hs[r * (mlp / 16) + mlp / 32 + (c >> 2)]);
+      float og[8], ou[8], oa[8];
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        const float g = (float)((int32_t)(gv[m >> 2] << (24 - 8 * (m & 3))) >> 24) * gst;
+        const float u = (float)((int32_t)(uv[m >> 2] << (24 - 8 * (m & 3))) >> 24) * ust;
+        const float d = (m & 1) ? bf16_hi(dv[m >> 1]) : bf16_lo(dv[m >> 1]);
+        const float s = 1.0f / (1.0f + expf(-g));
+        const float gs = g * s;
+        oa[m] = gs * u;
+        dot = __builtin_fmaf(d, oa[m], dot);
+        const float dw = d * w;
+        og[m] = dw * u * (s * (1.0f + g * (1.0f - s)));
+        ou[m] = dw * gs;
+      }
+      u32x4_t vg, vu, va;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        vg[m] = pack_bf16x2(og[2 * m], og[2 * m + 1]);
+        vu[m] = pack_bf16x2(ou[2 * m], ou[2 * m + 1]);
+        va[m] = pack_bf16x2(oa[2 * m], oa[2 * m + 1]);
+      }
+      st16(dh + r * 2 * mlp + c * 8, vg);
+      st16(dh + r * 2 * mlp + mlp + c * 8, vu);
+      if (a) st16(a + r * mlp + c * 8, va);
+    }
+    if (dscale) {
+#pragma unroll
+      for (int s = 32; s >= 1; s >>= 1) dot += __shfl_xor(dot, s);
+      if (lane == 0 && inside) dscale[q] = dot;
+    }
+  }
+}
+
+unsigned grid_of(int64_t items, int64_t per_block) {
+  const int64_t b = (items + per_block - 1) / per_block;
+  return (unsigned)(b < (int64_t(1) << 22) ? b : (int64_t(1) << 22));
+}
+
+// dW[e] [P, Q] = sum over the rows r of group e of X[row(r)]^T D[r], X in 8 bits: a 64 x 64 tile a
+// workgroup, 16 rows at a time through LDS, fp32 vector fmas.
+__global__ __launch_bounds__(256) void wgrad_ckpt_kernel(const int8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
+                                                         int64_t a_rows, const int32_t* __restrict__ row_slot,
+                                                         int slot_div, const uint16_t* __restrict__ D,
+                                                         const int32_t* __restrict__ off, int M, int P, int Q,
+                                                         uint16_t* __restrict__ C) {
+  __shared__ float s_a[16][64], s_d[16][64];
+  const int e = blockIdx.z, p0 = blockIdx.y * 64, q0 = blockIdx.x * 64;
+  const int lo = clamp_rows(off[e], M), hi = max(lo, clamp_rows(off[e + 1], M));
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  float acc[4][4] = {};
+  for (int r0 = lo; r0 < hi; r0 += 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int idx = threadIdx.x + 256 * i, rr = idx >> 6, cc = idx & 63;
+      const int r = r0 + rr;
+      float av = 0.0f, dv = 0.0f;
+      if (r < hi) {
+        int64_t sr = r;
+        if (row_slot) {
+          sr = row_slot[r] / slot_div;
+          sr = sr < 0 ? 0 : (sr >= a_rows ? a_rows - 1 : sr);
+        }
+        if (p0 + cc < P) av = (float)xc[sr * P + p0 + cc] * ckpt_step(xs[sr * (P / 32) + (p0 + cc) / 32]);
+        if (q0 + cc < Q) dv = bf16_to_f32(D[(int64_t)r * Q + q0 + cc]);
+      }
+      s_a[rr][cc] = av;
+      s_d[rr][cc] = dv;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(s_a[k][ty * 4 + i], s_d[k][tx * 4 + j], acc[i][j]);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pr = p0 + ty * 4 + i, qc = q0 + tx * 4;
+    if (pr < P && qc < Q)
+      *reinterpret_cast<u32x2_t*>(C + ((int64_t)e * P + pr) * Q + qc) =
+          u32x2_t{pack_bf16x2(acc[i][0], acc[i][1]), pack_bf16x2(acc[i][2], acc[i][3])};
+  }
+}
+
+}  // namespace
+
+hipError_t launch_ckpt_quantize(const void* src, bool src_bf16, int64_t M, int K, int8_t* codes, uint8_t* scales,
+                                hipStream_t stream) {
+  const int64_t n8 = M * (K / 8);
+  if (n8 == 0) return hipSuccess;
+  if (src_bf16)
+    ckpt_quantize_kernel<true><<<dim3(grid_of(n8, 256)), dim3(256), 0, stream>>>(src, n8, codes, scales);
+  else
+    ckpt_quantize_kernel<false><<<dim3(grid_of(n8, 256)), dim3(256), 0, stream>>>(src, n8, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_dequantize(const int8_t* codes, const uint8_t* scales, int64_t src_rows, int K,
+                                  const int32_t* row_index, int row_div, int64_t M, void* dst, bool dst_bf16,
+                                  hipStream_t stream) {
+  if (M == 0) return hipSuccess;
+  const dim3 grid(grid_of(M * (K / 8), 256));
+  if (dst_bf16)
+    ckpt_dequantize_kernel<true><<<grid, dim3(256), 0, stream>>>(codes, scales, src_rows, K, row_index, row_div, M,
+                                                                 dst);
+  else
+    ckpt_dequantize_kernel<false><<<grid, dim3(256), 0, stream>>>(codes, scales, src_rows, K, row_index, row_div, M,
+                                                                  dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_bwd_ckpt(int64_t M, int mlp, const uint16_t* da, const int8_t* h_codes,
+                                  const uint8_t* h_scales, const int32_t* row_slot, const float* slot_scale,
+                                  uint16_t* dh, uint16_t* a, float* dslot_scale, hipStream_t stream) {
+  if (M == 0) return hipSuccess;
+  swiglu_bwd_ckpt_kernel<<<dim3(grid_of(M, 4)), dim3(256), 0, stream>>>(M, mlp, da, h_codes, h_scales, row_slot,
+                                                                        slot_scale, dh, a, dslot_scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows, const int32_t* row_slot,
+                             int slot_div, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
+                             int Q, uint16_t* C, hipStream_t stream) {
+  wgrad_ckpt_kernel<<<dim3((Q + 63) / 64, (P + 63) / 64, E), dim3(256), 0, stream>>>(
+      A_codes, A_scales, a_rows, row_slot, slot_div, D, group_offsets, (int)M, P, Q, C);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -65,4 +65,25 @@ hipError_t launch_route_bwd(int64_t T, int emb, int E, int k, const uint16_t* x,
                             uint16_t* dx, float* dl, float* dls, int32_t* tok, float* wrt, float* dwrt,
                             hipStream_t stream);
 
+// Routing by scores and its gradient (route_scored.hip); score 0 softmax, 1 sigmoid.
+hipError_t launch_route_scored(int64_t T, int E, int k, int score, int n_group, int topk_group, int group_top,
+                               int renorm, float scale, const void* logits, bool logits_bf16, const float* bias,
+                               int32_t* topk_idx, float* topk_w, hipStream_t stream);
+hipError_t launch_route_scored_bwd(int64_t T, int E, int k, int score, int renorm, float scale, const void* logits,
+                                   bool logits_bf16, const int32_t* topk_idx, const float* topk_w,
+                                   const float* dtopk_w, void* dlogits, hipStream_t stream);
+
+// 8-bit activation checkpoints (ckpt.hip).
+hipError_t launch_ckpt_quantize(const void* src, bool src_bf16, int64_t M, int K, int8_t* codes, uint8_t* scales,
+                                hipStream_t stream);
+hipError_t launch_ckpt_dequantize(const int8_t* codes, const uint8_t* scales, int64_t src_rows, int K,
+                                  const int32_t* row_index, int row_div, int64_t M, void* dst, bool dst_bf16,
+                                  hipStream_t stream);
+hipError_t launch_swiglu_bwd_ckpt(int64_t M, int mlp, const uint16_t* da, const int8_t* h_codes,
+                                  const uint8_t* h_scales, const int32_t* row_slot, const float* slot_scale,
+                                  uint16_t* dh, uint16_t* a, float* dslot_scale, hipStream_t stream);
+hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows, const int32_t* row_slot,
+                             int slot_div, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
+                             int Q, uint16_t* C, hipStream_t stream);
+
 }  // namespace moe

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -155,6 +156,48 @@ int check_wgrad(int32_t E, int64_t M, int32_t P, int32_t Q) {
   if (P % 8 || Q % 8) return fail(MOE_ERR_UNSUPPORTED, "P and Q must be multiples of 8");
   if ((int64_t)E * ((P + 255) / 256) * ((Q + 255) / 256) >= (int64_t(1) << 31))
     return fail(MOE_ERR_UNSUPPORTED, "tile count too large");
+  return MOE_OK;
+}
+
+// rows of K elements held as 8-bit checkpoints
+int check_ckpt(int64_t rows, int32_t K) {
+  if (rows < 0 || K <= 0) return fail(MOE_ERR_SHAPE, "need rows >= 0 and K > 0");
+  if (K % 32) return fail(MOE_ERR_UNSUPPORTED, "row length (%d) is not a multiple of 32", K);
+  if (rows >= (int64_t(1) << 40) / K) return fail(MOE_ERR_UNSUPPORTED, "rows * K >= 2^40");
+  return MOE_OK;
+}
+
+int check_wgrad_ckpt(int64_t a_rows, bool gather, int32_t slot_div, int32_t E, int64_t M, int32_t P, int32_t Q) {
+  if (int rc = check_wgrad(E, M, P, Q)) return rc;
+  if (P % 32) return fail(MOE_ERR_UNSUPPORTED, "P (%d) is not a multiple of 32", P);
+  if (a_rows < 0) return fail(MOE_ERR_SHAPE, "need a_rows >= 0");
+  if (M > 0 && !gather && a_rows != M) return fail(MOE_ERR_SHAPE, "without row_slot, a_rows must equal M");
+  if (gather && slot_div <= 0) return fail(MOE_ERR_SHAPE, "row gather needs slot_div > 0");
+  if (M > 0 && a_rows == 0) return fail(MOE_ERR_SHAPE, "no checkpoint rows for %lld rows", (long long)M);
+  if (a_rows >= (int64_t(1) << 31) || a_rows * P >= (int64_t(1) << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "a_rows * P >= 2^31");
+  return MOE_OK;
+}
+
+int check_type(const char* name, int32_t type) {
+  if (type != MOE_F32 && type != MOE_BF16) return fail(MOE_ERR_SHAPE, "%s must be MOE_F32 or MOE_BF16", name);
+  return MOE_OK;
+}
+
+int check_router(const moe_shape_t* s, const moe_router_t* r) {
+  if (!r) return fail(MOE_ERR_NULL, "router is NULL");
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_SHAPE, "score must be MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID");
+  if (!(r->scale > 0.0f) || !std::isfinite(r->scale)) return fail(MOE_ERR_SHAPE, "scale must be finite and > 0");
+  if (r->n_group < 1 || s->E % r->n_group)
+    return fail(MOE_ERR_SHAPE, "n_group (%d) must divide E (%d)", r->n_group, s->E);
+  const int size = s->E / r->n_group;
+  if (r->topk_group < 1 || r->topk_group > r->n_group)
+    return fail(MOE_ERR_SHAPE, "need 1 <= topk_group (%d) <= n_group (%d)", r->topk_group, r->n_group);
+  if (r->group_top < 1 || r->group_top > 2 || r->group_top > size)
+    return fail(MOE_ERR_SHAPE, "group_top (%d) must be 1 or 2 and at most the group size (%d)", r->group_top, size);
+  if (s->k > r->topk_group * size)
+    return fail(MOE_ERR_SHAPE, "k (%d) > the %d experts of the groups that stay", s->k, r->topk_group * size);
   return MOE_OK;
 }
 
@@ -463,6 +506,116 @@ int moe_route_bwd(const moe_shape_t* s, const moe_bf16_t* x, const float* wr, co
                                           group_offsets, dwr, dbias, s->T > 0 ? dx : nullptr, dl, dls, tok, wrt,
                                           dwrt, (hipStream_t)stream),
                     "moe_route_bwd");
+}
+
+int moe_route_scored(const moe_shape_t* s, const moe_router_t* router, const void* logits, int32_t logits_type,
+                     const float* balance_bias, int32_t* topk_idx, float* topk_w, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_shape(s)) return rc;
+  if (int rc = check_router(s, router)) return rc;
+  if (int rc = check_type("logits_type", logits_type)) return rc;
+  if (s->T == 0) return MOE_OK;
+  NEED(logits);
+  MAYBE(balance_bias);
+  NEED(topk_idx);
+  NEED(topk_w);
+  return hip_status(moe::launch_route_scored(s->T, s->E, s->k, router->score, router->n_group, router->topk_group,
+                                             router->group_top, router->renorm != 0, router->scale, logits,
+                                             logits_type == MOE_BF16, balance_bias, topk_idx, topk_w,
+                                             (hipStream_t)stream),
+                    "moe_route_scored");
+}
+
+int moe_route_scored_bwd(const moe_shape_t* s, const moe_router_t* router, const void* logits, int32_t logits_type,
+                         const int32_t* topk_idx, const float* topk_w, const float* dtopk_w, void* dlogits,
+                         moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_shape(s)) return rc;
+  if (int rc = check_router(s, router)) return rc;
+  if (int rc = check_type("logits_type", logits_type)) return rc;
+  if (s->T == 0) return MOE_OK;
+  NEED(logits);
+  NEED(topk_idx);
+  NEED(topk_w);
+  NEED(dtopk_w);
+  NEED(dlogits);
+  return hip_status(moe::launch_route_scored_bwd(s->T, s->E, s->k, router->score, router->renorm != 0, router->scale,
+                                                 logits, logits_type == MOE_BF16, topk_idx, topk_w, dtopk_w, dlogits,
+                                                 (hipStream_t)stream),
+                    "moe_route_scored_bwd");
+}
+
+int moe_ckpt_quantize(const void* src, int32_t src_type, int64_t M, int32_t K, int8_t* codes, uint8_t* scales,
+                      moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_type("src_type", src_type)) return rc;
+  if (int rc = check_ckpt(M, K)) return rc;
+  if (M == 0) return MOE_OK;
+  NEED(src);
+  NEED(codes);
+  NEED(scales);
+  return hip_status(moe::launch_ckpt_quantize(src, src_type == MOE_BF16, M, K, codes, scales, (hipStream_t)stream),
+                    "moe_ckpt_quantize");
+}
+
+int moe_ckpt_dequantize(const int8_t* codes, const uint8_t* scales, int64_t src_rows, int32_t K,
+                        const int32_t* row_index, int32_t row_div, int64_t M, void* dst, int32_t dst_type,
+                        moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_type("dst_type", dst_type)) return rc;
+  if (int rc = check_ckpt(M, K)) return rc;
+  if (int rc = check_ckpt(src_rows, K)) return rc;
+  if (row_index && row_div <= 0) return fail(MOE_ERR_SHAPE, "row_div must be > 0");
+  if (M == 0) return MOE_OK;
+  if (!row_index && src_rows != M) return fail(MOE_ERR_SHAPE, "without row_index, src_rows must equal M");
+  if (src_rows == 0) return fail(MOE_ERR_SHAPE, "no source rows for %lld output rows", (long long)M);
+  NEED(codes);
+  NEED(scales);
+  MAYBE(row_index);
+  NEED(dst);
+  return hip_status(moe::launch_ckpt_dequantize(codes, scales, src_rows, K, row_index, row_index ? row_div : 1, M,
+                                                dst, dst_type == MOE_BF16, (hipStream_t)stream),
+                    "moe_ckpt_dequantize");
+}
+
+int moe_swiglu_bwd_ckpt(int64_t M, int32_t mlp, const moe_bf16_t* da, const int8_t* h_codes, const uint8_t* h_scales,
+                        const int32_t* row_slot, const float* slot_scale, moe_bf16_t* dh, moe_bf16_t* a,
+                        float* dslot_scale, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (M >= (int64_t(1) << 31)) return fail(MOE_ERR_UNSUPPORTED, "M >= 2^31");
+  if (mlp >= (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "mlp >= 2^30");
+  if (int rc = check_ckpt(M, mlp)) return rc;
+  if (M == 0) return MOE_OK;
+  NEED(da);
+  NEED(h_codes);
+  NEED(h_scales);
+  MAYBE(row_slot);
+  MAYBE(slot_scale);
+  NEED(dh);
+  MAYBE(a);
+  MAYBE(dslot_scale);
+  return hip_status(moe::launch_swiglu_bwd_ckpt(M, mlp, da, h_codes, h_scales, row_slot, slot_scale, dh, a,
+                                                dslot_scale, (hipStream_t)stream),
+                    "moe_swiglu_bwd_ckpt");
+}
+
+int moe_grouped_gemm_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows,
+                                const int32_t* row_slot, int32_t slot_div, const moe_bf16_t* D,
+                                const int32_t* group_offsets, int32_t E, int64_t M, int32_t P, int32_t Q,
+                                moe_bf16_t* C, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_wgrad_ckpt(a_rows, row_slot != nullptr, slot_div, E, M, P, Q)) return rc;
+  NEED(group_offsets);
+  NEED(C);
+  if (M > 0) {
+    NEED(A_codes);
+    NEED(A_scales);
+    MAYBE(row_slot);
+    NEED(D);
+  }
+  return hip_status(moe::launch_wgrad_ckpt(A_codes, A_scales, a_rows, row_slot, row_slot ? slot_div : 1, D,
+                                           group_offsets, E, M, P, Q, C, (hipStream_t)stream),
+                    "moe_grouped_gemm_wgrad_ckpt");
 }
 
 int moe_mx_quantize_rows(const moe_bf16_t* src, int64_t src_rows, int32_t K, const int32_t* row_index,
