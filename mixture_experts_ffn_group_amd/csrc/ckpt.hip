@@ -175,54 +175,6 @@ unsigned grid_of(int64_t items, int64_t per_block) {
   return (unsigned)(b < (int64_t(1) << 22) ? b : (int64_t(1) << 22));
 }
 
-// dW[e] [P, Q] = sum over the rows r of group e of X[row(r)]^T D[r], X in 8 bits: a 64 x 64 tile a
-// workgroup, 16 rows at a time through LDS, fp32 vector fmas.
-__global__ __launch_bounds__(256) void wgrad_ckpt_kernel(const int8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
-                                                         int64_t a_rows, const int32_t* __restrict__ row_slot,
-                                                         int slot_div, const uint16_t* __restrict__ D,
-                                                         const int32_t* __restrict__ off, int M, int P, int Q,
-                                                         uint16_t* __restrict__ C) {
-  __shared__ float s_a[16][64], s_d[16][64];
-  const int e = blockIdx.z, p0 = blockIdx.y * 64, q0 = blockIdx.x * 64;
-  const int lo = clamp_rows(off[e], M), hi = max(lo, clamp_rows(off[e + 1], M));
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  float acc[4][4] = {};
-  for (int r0 = lo; r0 < hi; r0 += 16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int idx = threadIdx.x + 256 * i, rr = idx >> 6, cc = idx & 63;
-      const int r = r0 + rr;
-      float av = 0.0f, dv = 0.0f;
-      if (r < hi) {
-        int64_t sr = r;
-        if (row_slot) {
-          sr = row_slot[r] / slot_div;
-          sr = sr < 0 ? 0 : (sr >= a_rows ? a_rows - 1 : sr);
-        }
-        if (p0 + cc < P) av = (float)xc[sr * P + p0 + cc] * ckpt_step(xs[sr * (P / 32) + (p0 + cc) / 32]);
-        if (q0 + cc < Q) dv = bf16_to_f32(D[(int64_t)r * Q + q0 + cc]);
-      }
-      s_a[rr][cc] = av;
-      s_d[rr][cc] = dv;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(s_a[k][ty * 4 + i], s_d[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pr = p0 + ty * 4 + i, qc = q0 + tx * 4;
-    if (pr < P && qc < Q)
-      *reinterpret_cast<u32x2_t*>(C + ((int64_t)e * P + pr) * Q + qc) =
-          u32x2_t{pack_bf16x2(acc[i][0], acc[i][1]), pack_bf16x2(acc[i][2], acc[i][3])};
-  }
-}
-
 }  // namespace
 
 hipError_t launch_ckpt_quantize(const void* src, bool src_bf16, int64_t M, int K, int8_t* codes, uint8_t* scales,
@@ -256,14 +208,6 @@ hipError_t launch_swiglu_bwd_ckpt(int64_t M, int mlp, const uint16_t* da, const 
   if (M == 0) return hipSuccess;
   swiglu_bwd_ckpt_kernel<<<dim3(grid_of(M, 4)), dim3(256), 0, stream>>>(M, mlp, da, h_codes, h_scales, row_slot,
                                                                         slot_scale, dh, a, dslot_scale);
-  return hipGetLastError();
-}
-
-hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows, const int32_t* row_slot,
-                             int slot_div, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
-                             int Q, uint16_t* C, hipStream_t stream) {
-  wgrad_ckpt_kernel<<<dim3((Q + 63) / 64, (P + 63) / 64, E), dim3(256), 0, stream>>>(
-      A_codes, A_scales, a_rows, row_slot, slot_div, D, group_offsets, (int)M, P, Q, C);
   return hipGetLastError();
 }
 

@@ -1041,6 +1041,332 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_kernel(WgradP p) {
   }
 }
 
+// The weight gradient with its left operand held as an 8-bit checkpoint and
+// read through a row mapping: dW[e] = sum over the rows r of group e of
+// X[row(r)]^T D[r], X [a_rows, P] in int8 codes with a power-of-two step per
+// 32 columns. Every value code * step is a bf16 number, so the bf16 matrix
+// cores multiply the checkpoint itself, without a rounding.
+//
+// Same tile, waves, deal and epilogue as wgrad_kernel; what differs is the
+// path of the left operand. Its codes (8 KB a k-slice, half the bf16 bytes)
+// and step bytes go global -> LDS like D, four k-slices ahead; between two
+// barriers each of the eight waves turns 1 KB of codes of the k-slice after
+// next into bf16, 16 elements a lane, into one of two [32][256] operand tiles.
+// The conversion is done once per element of the tile (each element feeds four
+// waves' fragments) and its 45 vector instructions a wave and k-slice run
+// beside the other wave's MFMAs. Converting into the sorted bf16 rows in
+// memory first would write and read 2 bytes an element and routed row more.
+//
+// The mapping is read the same way: slot indices of 8 k-slices (64 per copying
+// wave, its own 8 rows of each) come in one copy into a ring, and each lane
+// takes the rows it copies from there. k-rows past the group end get a zero
+// step (D's are zeros by the copy's range); their codes are any row's.
+//
+// An iteration kt of the k-loop issues the codes and steps of k-slice kt + 5
+// and D of kt + 4, and its barrier needs codes and steps kt + 2 and D kt + 1:
+// two iterations' copies (14 a copying wave) may still be in flight.
+struct WgradCkptP {
+  const int8_t* A;
+  const uint8_t* S;  // step codes [a_rows, P / 32]
+  const int32_t* row_slot;
+  const uint16_t* D;
+  const int32_t* off;
+  uint16_t* C;
+  int E, M, P, Q, a_rows;
+  uint32_t div_mul, div_shift;  // slot / slot_div = mulhi(2 slot, div_mul) >> div_shift
+};
+
+constexpr int kRawStage = 256 * GBK;      // codes of a k-slice: 8 KB
+constexpr int kStepStage = 8 * GBK * 4;   // steps of a k-slice, a dword each: 1 KB
+constexpr int kIdxChunk = 8;              // k-slices whose indices come in one copy
+constexpr int kIdxRing = 4;               // chunks of the index ring
+
+// 4 bytes per lane (lane L at lds + 4 L): the dword at base + voff, zero past the range
+__device__ __forceinline__ void b2lds4(i32x4_t rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(voff), "s"(rsrc), "s"(lds) : "memory");
+}
+// one byte per lane, zero-extended to a dword at lds + 4 L
+__device__ __forceinline__ void g2lds1(const void* sbase, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_ubyte %0, %1" : : "v"(voff), "s"(sbase), "s"(lds) : "memory");
+}
+
+template <bool GATHER>
+__global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
+  __shared__ __attribute__((aligned(16))) uint8_t s_a[2 * kOpStage];       // bf16 operand tiles
+  __shared__ __attribute__((aligned(16))) uint8_t s_raw[NST * kRawStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s_d[NST * kOpStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s_step[NST * kStepStage];
+  __shared__ __attribute__((aligned(16))) int s_idx[4][kIdxRing][64];
+  __shared__ __attribute__((aligned(16))) uint8_t s_stage[GTHR / 64][2048];
+  __shared__ int s_off[kMaxExperts + 1];
+  for (int i = threadIdx.x; i <= p.E; i += GTHR) s_off[i] = clamp_rows(p.off[i], p.M);
+  __syncthreads();
+  const int tp = (p.P + 255) / 256, tq = (p.Q + 255) / 256;
+  const int tid = opaque((int)threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  const int wm = wave & 1, wn = wave >> 1;
+  const int wave_u = __builtin_amdgcn_readfirstlane(wave);
+  const bool loader = wave_u < 4;
+  const uint32_t lds_raw = lds_addr(s_raw) + wave_u * 2048, lds_step = lds_addr(s_step) + wave_u * 256;
+  const uint32_t lds_d = lds_addr(s_d) + wave_u * 4096;
+  const uint32_t lds_idx = lds_addr(s_idx) + (wave_u & 3) * (kIdxRing * 256);
+  auto kbarrier = []() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  int e = 0, p0 = 0, q0 = 0, lo = 0, n = 0, nk = 0;
+  uint32_t a_col = 0, s_col = 0, d_off[2];
+  auto decode = [&](int64_t it) -> bool {
+    WgradTile wt;
+    if (!wgrad_tile(it, blockIdx.x, gridDim.x, p.E, tp, tq, &wt)) return false;
+    e = __builtin_amdgcn_readfirstlane(wt.e);
+    p0 = __builtin_amdgcn_readfirstlane(wt.pt * 256);
+    q0 = __builtin_amdgcn_readfirstlane(wt.qt * 256);
+    const int l0 = s_off[e], h0 = s_off[e + 1];
+    lo = __builtin_amdgcn_readfirstlane(l0);
+    n = __builtin_amdgcn_readfirstlane(h0 > l0 ? h0 - l0 : 0);
+    nk = (n + GBK - 1) / GBK;
+    if (!loader) return true;
+    // codes: copy j covers rows 8 wave + 4 j + lane / 16, 16 columns a lane; columns past P read
+    // others and only feed outputs that are never stored
+    a_col = (uint32_t)(p0 + 16 * (lane & 15) < p.P ? p0 + 16 * (lane & 15) : 0);
+    s_col = (uint32_t)min((p0 >> 5) + (lane & 7), (p.P >> 5) - 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int krow = (wave_u * 4 + j) * 2 + (lane >> 5);
+      const int c = (lane & 31) ^ ((krow & 3) << 2);
+      d_off[j] = (uint32_t)(krow * p.Q + q0 + c * 8) * 2u;
+    }
+    return true;
+  };
+  // index chunk c of the group: this copying wave's 8 rows of k-slices 8c .. 8c + 7 (lane = slice * 8 + row)
+  auto issue_idx = [&](int c) {
+    const int r0 = c * (kIdxChunk * GBK);
+    const i32x4_t ri = buffer_rsrc(p.row_slot + lo + r0, (uint32_t)min(n - r0, kIdxChunk * GBK) * 4u);
+    b2lds4(ri, (uint32_t)((lane >> 3) * GBK + wave_u * 8 + (lane & 7)) * 4u, lds_idx + (c & (kIdxRing - 1)) * 256);
+  };
+  // checkpoint row of row i (0..7) of this wave's share of k-slice kt
+  auto ckpt_row = [&](int kt, int i) -> uint32_t {
+    if (GATHER) {
+      const int s = s_idx[wave_u & 3][(kt / kIdxChunk) & (kIdxRing - 1)][(kt & (kIdxChunk - 1)) * 8 + i];
+      const uint32_t t = __umulhi((uint32_t)max(s, 0) * 2u, p.div_mul) >> p.div_shift;
+      return min(t, (uint32_t)(p.a_rows - 1));
+    }
+    return (uint32_t)min(lo + kt * GBK + wave_u * 8 + i, p.a_rows - 1);
+  };
+  auto issue_a = [&](int kt) {
+    const uint32_t st = (uint32_t)(kt & (NST - 1));
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      g2lds16(p.A, ckpt_row(kt, 4 * j + (lane >> 4)) * (uint32_t)p.P + a_col, lds_raw + st * kRawStage + j * 1024);
+    g2lds1(p.S, ckpt_row(kt, lane >> 3) * (uint32_t)(p.P >> 5) + s_col, lds_step + st * kStepStage);
+  };
+  auto issue_d = [&](int kt) {
+    const int r0 = lo + kt * GBK, rows = min(GBK, n - kt * GBK);
+    const i32x4_t rd = buffer_rsrc(p.D + (int64_t)r0 * p.Q, (uint32_t)(rows * p.Q * 2));
+    const uint32_t st = (uint32_t)(kt & (NST - 1)) * kOpStage;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b2lds16(rd, d_off[j & 1] + (uint32_t)((j >> 1) * 8 * p.Q), lds_d + st + j * 1024);
+  };
+  auto prologue = [&]() {
+    if (!loader || nk == 0) return;
+    if (GATHER) {
+      issue_idx(0);
+      if (nk > kIdxChunk) issue_idx(1);
+      wait_vm_all();
+    }
+    for (int s = 0; s < NST; ++s)
+      if (s < nk) {
+        issue_a(s);
+        issue_d(s);
+      }
+  };
+  // codes of k-slice kt -> bf16 operand tile kt % 2: lane's 16 elements of row 4 wave + lane / 16
+  const int crow = wave * 4 + (lane >> 4), cch = lane & 15;
+  auto convert = [&](int kt) {
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(s_raw + (kt & (NST - 1)) * kRawStage + crow * 256 + cch * 16);
+    const uint32_t c =
+        *reinterpret_cast<const uint32_t*>(s_step + (kt & (NST - 1)) * kStepStage + crow * 32 + (cch >> 1) * 4);
+    float step = __uint_as_float(c == 255 ? 0x7fc00000u : c << 23) * 0.015625f;
+    step = crow < n - kt * GBK ? step : 0.0f;
+    const float bias = -128.0f * step;
+    uint8_t* tile = s_a + (kt & 1) * kOpStage;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4_t o;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const uint32_t b = v[2 * h + d] ^ 0x80808080u;  // code + 128 in each byte
+        float f[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) f[m] = __builtin_fmaf((float)((b >> (8 * m)) & 0xffu), step, bias);
+        o[2 * d] = pack_bf16x2(f[0], f[1]);
+        o[2 * d + 1] = pack_bf16x2(f[2], f[3]);
+      }
+      *reinterpret_cast<u32x4_t*>(tile + off_n32(crow, 2 * cch + h)) = o;
+    }
+  };
+  // wait until at most the copies issued after those that the barrier of iteration kt needs are in flight
+  auto wait_for = [&](int kt) {
+    if (kt < 2 ? nk > NST + kt : kt + 4 < nk) {
+      if (kt < 2) asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(14)" ::: "memory");
+    } else if (kt >= 2 && kt + 4 == nk) {
+      asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
+    } else if (kt >= 2 && kt + 3 == nk) {
+      asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+  };
+
+  if (!decode(0)) return;
+  prologue();
+  for (int64_t it = 0;; ++it) {
+    f32x16_t acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][f][r] = 0.0f;
+
+    bf16x8_t af[2][4], df[2][2];
+    auto read_frags = [&](int kt, int ks, int set) {
+      const uint8_t* As = s_a + (kt & 1) * kOpStage;
+      const uint8_t* Ds = s_d + (kt & (NST - 1)) * kOpStage;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) af[set][i] = frag_tr(As, lane, ks * 16, wm * 128 + i * 32);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) df[set][f] = frag_tr(Ds, lane, ks * 16, wn * 64 + f * 32);
+    };
+    auto mfmas = [&](int set) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) acc[i][f] = mfma(df[set][f], af[set][i], acc[i][f]);
+    };
+    auto interleave = [&]() {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+    };
+
+    if (nk > 0) {
+      // k-slices 0 and 1 (copies of the two after them may be in flight): convert, publish
+      if (loader) {
+        if (nk >= NST) asm volatile("s_waitcnt vmcnt(14)" ::: "memory");
+        else wait_vm_all();
+      }
+      kbarrier();
+      convert(0);
+      if (nk > 1) convert(1);
+      kbarrier();
+      if (loader && nk > NST) issue_a(NST);
+      read_frags(0, 0, 0);
+    }
+    for (int kt = 0; kt < nk; ++kt) {
+      read_frags(kt, 1, 1);
+      mfmas(0);
+      interleave();
+      if (loader) wait_for(kt);
+      kbarrier();
+      if (GATHER && loader && (kt & (kIdxChunk - 1)) == 0 && (kt / kIdxChunk + 2) * kIdxChunk < nk)
+        issue_idx(kt / kIdxChunk + 2);
+      if (loader && kt + 5 < nk) issue_a(kt + 5);
+      if (kt + 2 < nk) convert(kt + 2);
+      {
+        const uint8_t* As = s_a + ((kt + 1) & 1) * kOpStage;
+        const uint8_t* Ds = s_d + ((kt + 1) & (NST - 1)) * kOpStage;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f) acc[i][f] = mfma(df[1][f], af[1][i], acc[i][f]);
+          af[0][i] = frag_tr(As, lane, 0, wm * 128 + i * 32);
+          if (i & 1) df[0][i >> 1] = frag_tr(Ds, lane, 0, wn * 64 + (i >> 1) * 32);
+        }
+      }
+      if (loader && kt + NST < nk) issue_d(kt + NST);
+    }
+
+    const int ce = e, cp0 = p0, cq0 = q0;
+    const bool more = decode(it + 1);
+    // every ring is free past the last barrier; the operand tiles carry the copying waves' output
+    if (more) prologue();
+    const int hh = lane >> 5, r = lane & 31;
+    uint8_t* const stg = s_stage[wave];
+    auto stg128 = [&](int rr, int c) { return rr * 128 + ((c ^ ((rr >> 1) & 7)) << 4); };
+    uint16_t* const Ce = p.C + (int64_t)ce * p.P * p.Q;
+    const int src = wave_u & 3;
+    uint8_t* const xr = s_a + src * 8192;
+    const int wm_s = src & 1, wn_s = src >> 1;
+#pragma unroll
+    for (int ph = 0; ph < 2; ++ph) {
+      if (loader) {
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii) {
+          const int i = 2 * ph + ii, rr = ii * 32 + r;
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<u32x2_t*>(xr + stg128(rr, f * 4 + q) + hh * 8) =
+                  pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]);
+        }
+      } else if (ph == 0) {
+        const int qw = cq0 + wn * 64;
+        const int valid = min(8, (p.Q - qw) >> 3);
+        uint8_t* const wb = r < 16 ? stg : s_stage[wave - 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int pr0 = cp0 + wm * 128 + i * 32;
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<u32x2_t*>(wb + stg128(r & 15, f * 4 + q) + hh * 8) =
+                  pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]);
+          wave_lds_fence();
+          u32x4_t v[4];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            v[kk] = *reinterpret_cast<const u32x4_t*>((kk < 2 ? stg : s_stage[wave - 4]) +
+                                                      stg128(8 * (kk & 1) + (lane >> 3), lane & 7));
+          wave_lds_fence();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int pr = pr0 + 8 * kk + (lane >> 3), c = lane & 7;
+            if (pr < p.P && c < valid)
+              __builtin_nontemporal_store(v[kk], reinterpret_cast<u32x4_t*>(Ce + (int64_t)pr * p.Q + qw + c * 8));
+          }
+        }
+      }
+      kbarrier();
+      if (!loader) {
+        const int pr0 = cp0 + wm_s * 128 + ph * 64;
+        const int qw = cq0 + wn_s * 64;
+        const int valid = min(8, (p.Q - qw) >> 3);
+        u32x4_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const u32x4_t*>(xr + stg128(8 * j + (lane >> 3), lane & 7));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int pr = pr0 + 8 * j + (lane >> 3), c = lane & 7;
+          if (pr < p.P && c < valid)
+            __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4_t*>(Ce + (int64_t)pr * p.Q + qw + c * 8));
+        }
+      }
+      kbarrier();
+    }
+    if (!more) break;
+  }
+}
+
 }  // namespace
 
 int persistent_grid() {
@@ -1077,6 +1403,21 @@ hipError_t launch_wgrad(const uint16_t* A, const uint16_t* D, const int32_t* gro
   if (E == 0) return hipSuccess;
   WgradP p{A, D, group_offsets, C, E, (int)M, P, Q};
   wgrad_kernel<<<dim3(grid_size > 0 ? grid_size : persistent_grid()), dim3(GTHR), 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows, const int32_t* row_slot,
+                             int slot_div, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
+                             int Q, uint16_t* C, hipStream_t stream) {
+  // slot / slot_div for 31-bit slots: with L = ceil(log2(d)) and m = floor(2^(31+L) / d) + 1 (below 2^32),
+  // m d exceeds 2^(31+L) by at most d <= 2^L, so floor(n m / 2^(31+L)) = floor(n / d)
+  uint32_t L = 0;
+  while ((uint64_t(1) << L) < (uint64_t)slot_div) ++L;
+  const uint32_t mul = (uint32_t)((uint64_t(1) << (31 + L)) / (uint64_t)slot_div + 1);
+  const WgradCkptP p{A_codes, A_scales, row_slot, D, group_offsets, C, E, (int)M, P, Q, (int)a_rows, mul, L};
+  const dim3 grid(persistent_grid()), block(GTHR);
+  if (row_slot) wgrad_ckpt_kernel<true><<<grid, block, 0, stream>>>(p);
+  else wgrad_ckpt_kernel<false><<<grid, block, 0, stream>>>(p);
   return hipGetLastError();
 }
 
