@@ -536,6 +536,52 @@ int moe_ffn_bwd(const moe_shape_t* shape, const moe_bf16_t* dy, const moe_saved_
                 const moe_bf16_t* wo, moe_bf16_t* dx, moe_bf16_t* dwi, moe_bf16_t* dwo, float* dtopk_w, void* ws,
                 size_t ws_bytes, moe_stream_t stream);
 
+/* Caller-owned activations of one forward pass in 8 bits, for moe_ffn_bwd_ckpt.
+   Device pointers: group_sizes [E], group_offsets [E+1], sorted_slot [S],
+   slot_row [S] int32; x_codes [T,emb] int8, x_scales [T,emb/32] bytes: the
+   token rows; h_codes [S,2*mlp], h_scales [S,2*mlp/32]: the gate/up values
+   (checkpoints as moe_ckpt_quantize writes them). The sorted rows xs, the
+   SwiGLU output a and the rows o of moe_saved_t are not kept: the backward
+   reads token rows through sorted_slot, recomputes a from h, and takes
+   dtopk_w from a and the gradient of a. 33/32 * (2*mlp + emb/k) bytes a routed
+   row instead of 10*mlp + 4*emb. */
+typedef struct {
+  int32_t* group_sizes;
+  int32_t* group_offsets;
+  int32_t* sorted_slot;
+  int32_t* slot_row;
+  int8_t* x_codes;
+  uint8_t* x_scales;
+  int8_t* h_codes;
+  uint8_t* h_scales;
+} moe_saved8_t;
+
+/*
+ * moe_ffn_fwd_routed -- moe_ffn_fwd on a given routing: topk_idx [T, k] int32
+ *  in [0, E), distinct per token, and topk_w [T, k] fp32, from moe_route,
+ *  moe_route_scored or the caller. Given moe_route's routing, y is bit for bit
+ *  moe_ffn_fwd's.
+ *  At most one of saved and saved8 is given (both NULL: inference).
+ *  saved: the set of moe_ffn_bwd; its topk_idx and topk_w are not written (set
+ *  them to the routing before moe_ffn_bwd). saved8: the 8-bit set of
+ *  moe_ffn_bwd_ckpt; h is quantized from its fp32 values in GEMM 1's epilogue,
+ *  and y does not depend on it.
+ *  ws: at least moe_workspace_bytes_routed(shape, 0) bytes.
+ *
+ * moe_ffn_bwd_ckpt -- moe_ffn_bwd from the 8-bit set, for the loss
+ *  sum(dy * y): the same gradients, taken at the h and x that the set holds.
+ *  topk_w [T, k] as in the forward. du = dy . wo[e]^T is rounded to bf16 before
+ *  the SwiGLU backward. Outputs as in moe_ffn_bwd (each may be NULL).
+ *  ws: at least moe_workspace_bytes_routed(shape, 1) bytes.
+ */
+size_t moe_workspace_bytes_routed(const moe_shape_t* shape, int backward_ckpt);
+int moe_ffn_fwd_routed(const moe_shape_t* shape, const moe_bf16_t* x, const int32_t* topk_idx, const float* topk_w,
+                       const moe_bf16_t* wi, const moe_bf16_t* wo, moe_bf16_t* y, const moe_saved_t* saved,
+                       const moe_saved8_t* saved8, void* ws, size_t ws_bytes, moe_stream_t stream);
+int moe_ffn_bwd_ckpt(const moe_shape_t* shape, const moe_bf16_t* dy, const float* topk_w, const moe_saved8_t* saved8,
+                     const moe_bf16_t* wi, const moe_bf16_t* wo, moe_bf16_t* dx, moe_bf16_t* dwi, moe_bf16_t* dwo,
+                     float* dtopk_w, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,8 @@ the C ABI in include/moe_ffn.h:
     route_scored, route_scored_bwd: routing by scores, groups and a balance bias
     ckpt_quantize, ckpt_dequantize, swiglu_bwd_ckpt, grouped_gemm_wgrad_ckpt:
     activations kept in 8 bits between the passes
+    ffn_fwd_routed, ffn_bwd_ckpt: the layer on a given routing, and its
+    backward from the 8-bit saved set
 
 Tensors: bf16 activations/weights, fp32 router weights/logits/top-k weights,
 int32 indices, all contiguous and on one CUDA (HIP) device.
@@ -17,6 +19,7 @@ int32 indices, all contiguous and on one CUDA (HIP) device.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -26,7 +29,7 @@ from ._lib import (MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_BWD, MOE_NN, MOE
 
 __all__ = ["route", "permute", "grouped_gemm", "grouped_gemm_wgrad", "combine", "combine_bwd", "ffn_fwd", "ffn_bwd",
            "route_scored", "route_scored_bwd", "ckpt_quantize", "ckpt_dequantize", "swiglu_bwd_ckpt",
-           "grouped_gemm_wgrad_ckpt", "query_support", "workspace_bytes", "MoeError"]
+           "grouped_gemm_wgrad_ckpt", "ffn_fwd_routed", "ffn_bwd_ckpt", "query_support", "workspace_bytes", "MoeError"]
 
 _EPI = {"none": MOE_EPI_NONE, "swiglu": MOE_EPI_SWIGLU, "swiglu_bwd": MOE_EPI_SWIGLU_BWD}
 _OP = {"nn": MOE_NN, "nt": MOE_NT}
@@ -36,7 +39,14 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+# The current stream's handle straight from torch, where it offers that (0.1 us; building a Stream object to
+# read it from costs 1.8 us, half a kernel launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev: torch.device):
+    if _raw_stream is not None and dev.index is not None:
+        return C.c_void_p(_raw_stream(dev.index))
     return C.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
@@ -427,8 +437,11 @@ _TYPE = {torch.float32: _lib.MOE_F32, torch.bfloat16: _lib.MOE_BF16}
 
 def _need_like(t, name, shape, dtype, device):
     """_need, with the shape checked too (the kernels index by the sizes they are given)."""
+    if t is None or (type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous()
+                     and t.shape == shape):
+        return
     _need(t, name, dtype, device)
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -444,10 +457,32 @@ def _need_typed(t, name, ndim):
     return _TYPE[t.dtype]
 
 
+def _need_rank2(t, name, dtype, device):
+    _need(t, name, dtype, device)
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {None if t is None else tuple(t.shape)}")
+
+
+def _call(fn, dev, *args):
+    """Library call `fn` on dev's current stream, with dev current: tensors pass as pointers, None as NULL."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, *args)
+    status = getattr(_lib.lib(), fn)(*[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args], _stream(dev))
+    if status != _lib.MOE_OK:
+        _lib.check(status, fn)
+
+
+@functools.lru_cache(maxsize=256)
+def _route_shape(T, E, k):
+    return C.byref(_lib.shape(T, 64, 64, E, k))
+
+
+@functools.lru_cache(maxsize=256)
 def _router(score, n_group, topk_group, group_top, renorm, scale):
     if score not in _SCORE:
         raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
-    return _lib.MoeRouter(_SCORE[score], n_group, topk_group, group_top, int(bool(renorm)), scale)
+    return C.byref(_lib.MoeRouter(_SCORE[score], n_group, topk_group, group_top, int(bool(renorm)), scale))
 
 
 def route_scored(k: int, logits: torch.Tensor, balance_bias: torch.Tensor | None = None, score: str = "softmax",
@@ -461,12 +496,10 @@ def route_scored(k: int, logits: torch.Tensor, balance_bias: torch.Tensor | None
     T, E = logits.shape
     _need_like(balance_bias, "balance_bias", (E,), torch.float32, dev)
     r = _router(score, n_group, topk_group, group_top, renorm, scale)
-    s = _lib.shape(T, 64, 64, E, k)
-    with torch.cuda.device(dev):
-        idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
-        w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
-        _lib.check(_lib.lib().moe_route_scored(C.byref(s), C.byref(r), _ptr(logits), ty, _ptr(balance_bias),
-                                               _ptr(idx), _ptr(w), _stream(dev)), "moe_route_scored")
+    kk = k if k > 0 else 0  # a k <= 0 is the library's to refuse
+    idx = torch.empty((T, kk), dtype=torch.int32, device=dev)
+    w = torch.empty((T, kk), dtype=torch.float32, device=dev)
+    _call("moe_route_scored", dev, _route_shape(T, E, k), r, logits, ty, balance_bias, idx, w)
     return idx, w
 
 
@@ -477,18 +510,14 @@ def route_scored_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch
     ty = _need_typed(logits, "logits", 2)
     dev = logits.device
     T, E = logits.shape
-    _need(topk_idx, "topk_idx", torch.int32, dev)
-    k = topk_idx.shape[1] if topk_idx.dim() == 2 else -1
-    _need_like(topk_idx, "topk_idx", (T, k), torch.int32, dev)
-    _need_like(topk_w, "topk_w", (T, k), torch.float32, dev)
-    _need_like(dtopk_w, "dtopk_w", (T, k), torch.float32, dev)
-    r = _router(score, 1, 1, 1, renorm, scale)
-    s = _lib.shape(T, 64, 64, E, k)
-    with torch.cuda.device(dev):
-        d = torch.empty_like(logits)
-        _lib.check(_lib.lib().moe_route_scored_bwd(C.byref(s), C.byref(r), _ptr(logits), ty, _ptr(topk_idx),
-                                                   _ptr(topk_w), _ptr(dtopk_w), _ptr(d), _stream(dev)),
-                   "moe_route_scored_bwd")
+    _need_rank2(topk_idx, "topk_idx", torch.int32, dev)
+    k = topk_idx.shape[1]
+    for t, n, d in ((topk_idx, "topk_idx", torch.int32), (topk_w, "topk_w", torch.float32),
+                    (dtopk_w, "dtopk_w", torch.float32)):
+        _need_like(t, n, (T, k), d, dev)
+    d = torch.empty_like(logits)
+    _call("moe_route_scored_bwd", dev, _route_shape(T, E, k), _router(score, 1, 1, 1, renorm, scale), logits, ty,
+          topk_idx, topk_w, dtopk_w, d)
     return d
 
 
@@ -496,20 +525,21 @@ def ckpt_quantize(src: torch.Tensor):
     """8-bit checkpoint of rows src [M, K] fp32 or bf16 (see moe_ckpt_quantize): (codes [M, K] int8,
     scales [M, K/32] uint8). K must be a multiple of 32."""
     ty = _need_typed(src, "src", 2)
+    dev = src.device
     M, K = src.shape
-    with torch.cuda.device(src.device):
-        codes = torch.empty((M, K), dtype=torch.int8, device=src.device)
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=src.device)
-        _lib.check(_lib.lib().moe_ckpt_quantize(_ptr(src), ty, M, K, _ptr(codes), _ptr(scales),
-                                                _stream(src.device)), "moe_ckpt_quantize")
+    codes = torch.empty((M, K), dtype=torch.int8, device=dev)
+    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+    _call("moe_ckpt_quantize", dev, src, ty, M, K, codes, scales)
     return codes, scales
 
 
 def _need_ckpt(codes, scales, name, dev):
-    _need(codes, f"{name}codes", torch.int8, dev)
-    if codes.dim() != 2:
-        raise ValueError(f"{name}codes must have 2 dimensions, got shape {tuple(codes.shape)}")
-    _need_like(scales, f"{name}scales", (codes.shape[0], codes.shape[1] // 32), torch.uint8, dev)
+    """An 8-bit checkpoint: codes [M, K] and scales [M, K/32] of one device."""
+    _need_rank2(codes, f"{name}codes", torch.int8, dev)
+    M, K = codes.shape
+    if scales is None:
+        raise ValueError(f"{name}scales is missing")
+    _need_like(scales, f"{name}scales", (M, K // 32), torch.uint8, codes.device)
 
 
 def ckpt_dequantize(codes: torch.Tensor, scales: torch.Tensor, row_index: torch.Tensor | None = None,
@@ -521,12 +551,12 @@ def ckpt_dequantize(codes: torch.Tensor, scales: torch.Tensor, row_index: torch.
     if dtype not in _TYPE:
         raise TypeError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
     R, K = codes.shape
-    _need(row_index, "row_index", torch.int32, dev)
-    M = R if row_index is None else row_index.numel()
-    with torch.cuda.device(dev):
-        dst = torch.empty((M, K), dtype=dtype, device=dev)
-        _lib.check(_lib.lib().moe_ckpt_dequantize(_ptr(codes), _ptr(scales), R, K, _ptr(row_index), row_div, M,
-                                                  _ptr(dst), _TYPE[dtype], _stream(dev)), "moe_ckpt_dequantize")
+    M = R
+    if row_index is not None:
+        M = row_index.numel()
+        _need_like(row_index, "row_index", (M,), torch.int32, dev)
+    dst = torch.empty((M, K), dtype=dtype, device=dev)
+    _call("moe_ckpt_dequantize", dev, codes, scales, R, K, row_index, row_div, M, dst, _TYPE[dtype])
     return dst
 
 
@@ -536,22 +566,17 @@ def swiglu_bwd_ckpt(da: torch.Tensor, h_codes: torch.Tensor, h_scales: torch.Ten
     """SwiGLU backward from an 8-bit h (see moe_swiglu_bwd_ckpt): (dh [M, 2*mlp] bf16, a [M, mlp] bf16 or None,
     dslot_scale [M] fp32 or None) from da [M, mlp] bf16; row_slot [M] int32 maps rows to entries of slot_scale [M]
     and dslot_scale."""
-    _need(da, "da", torch.bfloat16)
+    _need_rank2(da, "da", torch.bfloat16, None)
     dev = da.device
-    if da.dim() != 2:
-        raise ValueError(f"da must have 2 dimensions, got shape {tuple(da.shape)}")
     M, mlp = da.shape
     _need_ckpt(h_codes, h_scales, "h_", dev)
     _need_like(h_codes, "h_codes", (M, 2 * mlp), torch.int8, dev)
     _need_like(row_slot, "row_slot", (M,), torch.int32, dev)
     _need_like(slot_scale, "slot_scale", (M,), torch.float32, dev)
-    with torch.cuda.device(dev):
-        dh = torch.empty((M, 2 * mlp), dtype=torch.bfloat16, device=dev)
-        a = torch.empty((M, mlp), dtype=torch.bfloat16, device=dev) if want_a else None
-        ds = torch.empty(M, dtype=torch.float32, device=dev) if want_dscale else None
-        _lib.check(_lib.lib().moe_swiglu_bwd_ckpt(M, mlp, _ptr(da), _ptr(h_codes), _ptr(h_scales), _ptr(row_slot),
-                                                  _ptr(slot_scale), _ptr(dh), _ptr(a), _ptr(ds), _stream(dev)),
-                   "moe_swiglu_bwd_ckpt")
+    dh = torch.empty((M, 2 * mlp), dtype=torch.bfloat16, device=dev)
+    a = torch.empty((M, mlp), dtype=torch.bfloat16, device=dev) if want_a else None
+    ds = torch.empty(M, dtype=torch.float32, device=dev) if want_dscale else None
+    _call("moe_swiglu_bwd_ckpt", dev, M, mlp, da, h_codes, h_scales, row_slot, slot_scale, dh, a, ds)
     return dh, a, ds
 
 
@@ -562,16 +587,130 @@ def grouped_gemm_wgrad_ckpt(a_codes: torch.Tensor, a_scales: torch.Tensor, D: to
     row_slot [M] int32, row r of the product reads X row row_slot[r] // slot_div."""
     _need_ckpt(a_codes, a_scales, "a_", None)
     dev = a_codes.device
-    _need(D, "D", torch.bfloat16, dev)
-    if D.dim() != 2:
-        raise ValueError(f"D must have 2 dimensions, got shape {tuple(D.shape)}")
+    _need_rank2(D, "D", torch.bfloat16, dev)
     M, Q = D.shape
     R, P = a_codes.shape
     _need_like(row_slot, "row_slot", (M,), torch.int32, dev)
+    if group_offsets is None:
+        raise ValueError("group_offsets is missing")
     _need_like(group_offsets, "group_offsets", (E + 1,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        C_ = torch.empty((max(E, 0), P, Q), dtype=torch.bfloat16, device=dev)
-        _lib.check(_lib.lib().moe_grouped_gemm_wgrad_ckpt(_ptr(a_codes), _ptr(a_scales), R, _ptr(row_slot), slot_div,
-                                                          _ptr(D), _ptr(group_offsets), E, M, P, Q, _ptr(C_),
-                                                          _stream(dev)), "moe_grouped_gemm_wgrad_ckpt")
+    C_ = torch.empty((max(E, 0), P, Q), dtype=torch.bfloat16, device=dev)
+    _call("moe_grouped_gemm_wgrad_ckpt", dev, a_codes, a_scales, R, row_slot, slot_div, D, group_offsets, E, M, P, Q,
+          C_)
     return C_
+
+
+_SAVED8_NAMES = ("group_sizes", "group_offsets", "sorted_slot", "slot_row", "x_codes", "x_scales", "h_codes",
+                 "h_scales")
+
+
+def alloc_saved8(T: int, emb: int, mlp: int, E: int, k: int, device) -> dict:
+    """Buffers of one forward pass in 8 bits, for ffn_bwd_ckpt."""
+    S = T * k
+    i32, i8, u8 = torch.int32, torch.int8, torch.uint8
+    return dict(group_sizes=torch.empty(E, dtype=i32, device=device),
+                group_offsets=torch.empty(E + 1, dtype=i32, device=device),
+                sorted_slot=torch.empty(S, dtype=i32, device=device),
+                slot_row=torch.empty(S, dtype=i32, device=device),
+                x_codes=torch.empty((T, emb), dtype=i8, device=device),
+                x_scales=torch.empty((T, emb // 32), dtype=u8, device=device),
+                h_codes=torch.empty((S, 2 * mlp), dtype=i8, device=device),
+                h_scales=torch.empty((S, mlp // 16), dtype=u8, device=device))
+
+
+def _layer_sizes(wi, wo, emb, dev):
+    """(E, mlp) of a layer's weights wi [E, emb, 2*mlp], wo [E, mlp, emb]."""
+    _need(wi, "wi", torch.bfloat16, dev)
+    if wi is None or wi.dim() != 3 or wi.shape[1] != emb or wi.shape[2] % 2:
+        raise ValueError(f"wi must have shape [E, {emb}, 2*mlp], got {None if wi is None else tuple(wi.shape)}")
+    E, mlp = wi.shape[0], wi.shape[2] // 2
+    if wo is None:
+        raise ValueError("wo is missing")
+    _need_like(wo, "wo", (E, mlp, emb), torch.bfloat16, dev)
+    return E, mlp
+
+
+def _workspace(workspace, n, dev):
+    """The caller's workspace, checked, or a new one of n bytes."""
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    return workspace
+
+
+def ffn_fwd_routed(x: torch.Tensor, wi: torch.Tensor, wo: torch.Tensor, topk_idx: torch.Tensor,
+                   topk_w: torch.Tensor, save: str | None = None, keep_h: bool = True,
+                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """MoE FFN forward on a given routing (route, route_scored, or the caller's own): (y [T, emb] bf16, saved dict
+    or None). save: None, "full" (the set ffn_bwd takes; keep_h as in ffn_fwd) or "int8" (the set ffn_bwd_ckpt
+    takes). workspace: uint8 of at least workspace_bytes_routed(...) bytes."""
+    if save not in (None, "full", "int8"):
+        raise ValueError(f'save must be None, "full" or "int8", got {save!r}')
+    _need_rank2(x, "x", torch.bfloat16, None)
+    dev = x.device
+    T, emb = x.shape
+    E, mlp = _layer_sizes(wi, wo, emb, dev)
+    _need_rank2(topk_idx, "topk_idx", torch.int32, dev)
+    k = topk_idx.shape[1]
+    for t, n, d in ((topk_idx, "topk_idx", torch.int32), (topk_w, "topk_w", torch.float32)):
+        if t is None:
+            raise ValueError(f"{n} is missing")
+        _need_like(t, n, (T, k), d, dev)
+    _need_like(out, "out", (T, emb), torch.bfloat16, dev)
+    s = _lib.shape(T, emb, mlp, E, k)
+    _lib.check(_lib.lib().moe_query_support(C.byref(s)), "ffn_fwd_routed")
+    ws = _workspace(workspace, int(_lib.lib().moe_workspace_bytes_routed(C.byref(s), 0)), dev)
+    y = out if out is not None else torch.empty((T, emb), dtype=torch.bfloat16, device=dev)
+    saved = full = int8 = None
+    if save == "full":
+        saved = alloc_saved(T, emb, mlp, E, k, dev, keep_h=keep_h)
+        saved["topk_idx"], saved["topk_w"] = topk_idx, topk_w
+        full = C.byref(_saved_struct(saved))
+    elif save == "int8":
+        saved = alloc_saved8(T, emb, mlp, E, k, dev)
+        saved["topk_idx"], saved["topk_w"] = topk_idx, topk_w
+        int8 = C.byref(_lib.MoeSaved8(*[saved[n].data_ptr() for n in _SAVED8_NAMES]))
+    _call("moe_ffn_fwd_routed", dev, C.byref(s), x, topk_idx, topk_w, wi, wo, y, full, int8, ws, ws.numel())
+    return y, saved
+
+
+def ffn_bwd_ckpt(dy: torch.Tensor, saved: dict, wi: torch.Tensor, wo: torch.Tensor,
+                 need=("dx", "dwi", "dwo", "dtopk_w"), workspace: torch.Tensor | None = None) -> dict:
+    """MoE FFN backward from the 8-bit set of ffn_fwd_routed(save="int8"), the routing held fixed; returns the
+    requested gradients, as ffn_bwd does. workspace: uint8 of at least workspace_bytes_routed(..., backward=True)
+    bytes."""
+    _need_rank2(dy, "dy", torch.bfloat16, None)
+    dev = dy.device
+    T, emb = dy.shape
+    E, mlp = _layer_sizes(wi, wo, emb, dev)
+    _need_rank2(saved["topk_w"], "topk_w", torch.float32, dev)
+    k = saved["topk_w"].shape[1]
+    S = T * k
+    s = _lib.shape(T, emb, mlp, E, k)
+    _lib.check(_lib.lib().moe_query_support(C.byref(s)), "ffn_bwd_ckpt")
+    for n, shape, d in (("topk_w", (T, k), torch.float32), ("group_sizes", (E,), torch.int32),
+                        ("group_offsets", (E + 1,), torch.int32), ("sorted_slot", (S,), torch.int32),
+                        ("slot_row", (S,), torch.int32), ("x_codes", (T, emb), torch.int8),
+                        ("x_scales", (T, emb // 32), torch.uint8), ("h_codes", (S, 2 * mlp), torch.int8),
+                        ("h_scales", (S, mlp // 16), torch.uint8)):
+        _need_like(saved[n], n, shape, d, dev)
+    g = {}
+    if "dx" in need:
+        g["dx"] = torch.empty((T, emb), dtype=torch.bfloat16, device=dev)
+    if "dwi" in need:
+        g["dwi"] = torch.empty((E, emb, 2 * mlp), dtype=torch.bfloat16, device=dev)
+    if "dwo" in need:
+        g["dwo"] = torch.empty((E, mlp, emb), dtype=torch.bfloat16, device=dev)
+    if "dtopk_w" in need:
+        g["dtopk_w"] = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ws = _workspace(workspace, int(_lib.lib().moe_workspace_bytes_routed(C.byref(s), 1)), dev)
+    _call("moe_ffn_bwd_ckpt", dev, C.byref(s), dy, saved["topk_w"],
+          C.byref(_lib.MoeSaved8(*[saved[n].data_ptr() for n in _SAVED8_NAMES])), wi, wo, g.get("dx"), g.get("dwi"),
+          g.get("dwo"), g.get("dtopk_w"), ws, ws.numel())
+    return g
+
+
+def workspace_bytes_routed(T: int, emb: int, mlp: int, E: int, k: int, backward: bool = False) -> int:
+    """Workspace bytes of ffn_fwd_routed, or of ffn_bwd_ckpt with backward."""
+    s = _lib.shape(T, emb, mlp, E, k)
+    return int(_lib.lib().moe_workspace_bytes_routed(C.byref(s), int(backward)))

@@ -36,6 +36,11 @@ class MoeSaved(C.Structure):
                                            "slot_row", "xs", "h", "a", "o")]
 
 
+class MoeSaved8(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("group_sizes", "group_offsets", "sorted_slot", "slot_row", "x_codes",
+                                           "x_scales", "h_codes", "h_scales")]
+
+
 class MoeGemmRows(C.Structure):
     _fields_ = [("row_slot", C.c_void_p), ("n_slots", C.c_int32), ("slot_div", C.c_int32),
                 ("slot_scale", C.c_void_p)]
@@ -82,6 +87,10 @@ SIGNATURES = {
     "moe_ckpt_dequantize": ([_p, _p, _i64, _i32, _p, _i32, _i64, _p, _i32, _p], C.c_int),
     "moe_swiglu_bwd_ckpt": ([_i64, _i32, _p, _p, _p, _p, _p, _p, _p, _p, _p], C.c_int),
     "moe_grouped_gemm_wgrad_ckpt": ([_p, _p, _i64, _p, _i32, _p, _p, _i32, _i64, _i32, _i32, _p, _p], C.c_int),
+    "moe_workspace_bytes_routed": ([_SHP, C.c_int], _sz),
+    "moe_ffn_fwd_routed": ([_SHP, _p, _p, _p, _p, _p, _p, C.POINTER(MoeSaved), C.POINTER(MoeSaved8), _p, _sz, _p],
+                           C.c_int),
+    "moe_ffn_bwd_ckpt": ([_SHP, _p, _p, C.POINTER(MoeSaved8), _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
     "moe_route_bwd": ([_SHP, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
 }
 

@@ -21,19 +21,6 @@
 namespace moe {
 namespace {
 
-// 2^(c-133) of a scale code, NaN for 255: 2^(c-127) is the float with exponent field c.
-__device__ __forceinline__ float ckpt_step(uint32_t c) {
-  return __uint_as_float(c == 255 ? 0x7fc00000u : c << 23) * 0.015625f;
-}
-
-__device__ __forceinline__ int ckpt_scale_code(uint32_t amax_bits) {
-  const int c = (int)(amax_bits >> 23);  // floor(log2) + 127; 0 for zero and subnormals
-  return c < 1 ? 1 : c;                  // 255 where amax is inf or NaN
-}
-__device__ __forceinline__ int ckpt_code(float v, int ex) {
-  return (int)fminf(fmaxf(rintf(ldexpf(v, ex)), -127.0f), 127.0f);
-}
-
 // Eight consecutive elements of a row per thread; four threads share a block.
 template <bool BF16>
 __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restrict__ src, int64_t n8,
@@ -63,18 +50,8 @@ __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restri
     am = max(am, (uint32_t)__shfl_xor((int)am, 1));
     am = max(am, (uint32_t)__shfl_xor((int)am, 2));
     const int c = ckpt_scale_code(am);
-    u32x2_t o;
-    if (c == 255) {
-      o = u32x2_t{0u, 0u};
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) w |= ((uint32_t)ckpt_code(x[4 * h + m], 133 - c) & 0xffu) << (8 * m);
-        o[h] = w;
-      }
-    }
+    const float inv = ckpt_inv_step(c);
+    const u32x2_t o = {ckpt_codes4(x[0], x[1], x[2], x[3], inv), ckpt_codes4(x[4], x[5], x[6], x[7], inv)};
     *reinterpret_cast<u32x2_t*>(codes + i * 8) = o;
     if ((i & 3) == 0) scales[i >> 2] = (uint8_t)c;
   }

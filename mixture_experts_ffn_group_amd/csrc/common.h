@@ -81,4 +81,34 @@ __device__ __forceinline__ uint32_t mx_e4m3_x4(float a, float b, float c, float 
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(cl(c), cl(d), lo, true);
 }
 
+// 8-bit activation checkpoints (integer codes with a power-of-two step per 32 elements; see ckpt.hip).
+// Step 2^(c-133) of step code c, NaN for 255: 2^(c-127) is the float with exponent field c.
+__device__ __forceinline__ float ckpt_step(uint32_t c) {
+  return __uint_as_float(c == 255 ? 0x7fc00000u : c << 23) * 0.015625f;
+}
+// Step code of a block whose largest magnitude has fp32 bits amax_bits: its exponent field, at least 1, and
+// 255 for an infinity or a NaN.
+__device__ __forceinline__ int ckpt_scale_code(uint32_t amax_bits) {
+  const int c = (int)(amax_bits >> 23);
+  return c < 1 ? 1 : c;
+}
+// 2^(127-c): values times this lie in (-2, 2), one exact multiplication (for c = 254 the result is the
+// subnormal 2^-127, kept as such); the missing 2^6 of 1 / step = 2^(133-c), which would leave fp32's range
+// for c <= 5, comes with the rounding. 0 for c = 255.
+__device__ __forceinline__ float ckpt_inv_step(int c) {
+  return c == 255 ? 0.0f : (c == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - c) << 23));
+}
+// Four codes, byte i from value i: v / step rounded to nearest even, within +-127. Adding 1.5 * 2^17 to a float below 2 in
+// magnitude rounds it to a multiple of 2^-6 and leaves the integer in the low mantissa bits. inv is 0 for a
+// non-finite block (c = 255), whose codes are 0.
+__device__ __forceinline__ uint32_t ckpt_codes4(float a, float b, float c, float d, float inv) {
+  constexpr float kLim = 127.0f / 64.0f;
+  const auto q = [&](float v) -> uint32_t {
+    const float t = fminf(fmaxf(v * inv, -kLim), kLim);
+    return __float_as_uint(t + 196608.0f);
+  };
+  const uint32_t lo = __builtin_amdgcn_perm(q(b), q(a), 0x0c0c0400u), hi = __builtin_amdgcn_perm(q(d), q(c), 0x04000c0cu);
+  return inv == 0.0f ? 0u : (lo | hi);
+}
+
 }  // namespace moe

@@ -54,7 +54,9 @@ namespace {
 constexpr int BM = 256, BN = 256;
 
 enum { OP_NN = 0, OP_NT = 1 };
-enum { EPI_NONE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_BWD = 2 };
+enum { EPI_NONE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_BWD = 2, EPI_SWIGLU_CKPT = 3 };
+// the two that split the product into gate and up
+constexpr bool epi_swiglu(int epi) { return epi == EPI_SWIGLU || epi == EPI_SWIGLU_CKPT; }
 
 struct GemmP {
   const uint16_t* A;
@@ -67,6 +69,8 @@ struct GemmP {
   const float* slot_scale;  // optional: output row r is scaled by slot_scale[row_slot[r]] (or [r])
   int E, M, K, N;
   int n_slots, slot_div;
+  int8_t* h_codes = nullptr;    // SWIGLU_CKPT: h as an 8-bit checkpoint, codes [M, N]
+  uint8_t* h_scales = nullptr;  // and step codes [M, N / 32]
 };
 
 struct WgradP {
@@ -146,7 +150,7 @@ __device__ __forceinline__ u32x2_t pack4(float a, float b, float c, float d) {
 // SwiGLU: fragment 0 holds 32 gate columns and fragment 1 the matching 32 up columns.
 template <int EPI>
 __device__ __forceinline__ int frag_col8(int wn, int f) {
-  if (EPI == EPI_SWIGLU) return f == 0 ? wn * 32 : 128 + wn * 32;
+  if (epi_swiglu(EPI)) return f == 0 ? wn * 32 : 128 + wn * 32;
   return wn * 64 + f * 32;
 }
 
@@ -191,8 +195,8 @@ __global__ __launch_bounds__(GTHR, 1) void gemm_kernel(GemmP p) {
   // Output staging: 2 KB per wave, 32 rows x 64 bytes of the wave's output at a time.
   __shared__ __attribute__((aligned(16))) uint8_t s_stage[GTHR / 64][2048];
   __shared__ int s_lo[kMaxExperts + 1], s_pref[kMaxExperts + 1], s_wsum[8];
-  const int mlp = EPI == EPI_SWIGLU ? p.N / 2 : p.N;
-  const int tile_n = EPI == EPI_SWIGLU ? 128 : BN;
+  const int mlp = epi_swiglu(EPI) ? p.N / 2 : p.N;
+  const int tile_n = epi_swiglu(EPI) ? 128 : BN;
   const int ntn = (mlp + tile_n - 1) / tile_n;
 
   {  // ragged tile list: tiles of expert e = ceil(rows_e / BM) * ntn, prefix over experts
@@ -320,7 +324,7 @@ __global__ __launch_bounds__(GTHR, 1) void gemm_kernel(GemmP p) {
         const int krow = (wave_u * LPW + j) * 2 + (lane >> 5);
         const int c = (lane & 31) ^ ((krow & 3) << 2);
         int col;
-        if (EPI == EPI_SWIGLU) {
+        if (epi_swiglu(EPI)) {
           const int cc = c < 16 ? n0 + c * 8 : n0 + (c - 16) * 8;
           col = cc < mlp ? (c < 16 ? cc : mlp + cc) : 0;
         } else {
@@ -644,7 +648,7 @@ __global__ __launch_bounds__(GTHR, 1) void gemm_kernel(GemmP p) {
         }
         kbarrier();  // read back: the region may be written again
       }
-    } else if (EPI == EPI_SWIGLU) {
+    } else if (epi_swiglu(EPI)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float sc = sc4[i];
@@ -665,7 +669,43 @@ __global__ __launch_bounds__(GTHR, 1) void gemm_kernel(GemmP p) {
           else *reinterpret_cast<u32x2_t*>(stg + stg64(r, q) + hh * 8) = pk;
         }
         if (!loader) drain(m0r, [&](int m) { return (void*)(p.C + (int64_t)m * mlp + c0); }, min(4, (mlp - c0) >> 3));
-        if (p.aux_out) {  // h kept in fp32 for the backward: the gate/up values the SwiGLU used, unrounded
+        if (EPI == EPI_SWIGLU_CKPT) {
+          // h kept in 8 bits: this fragment's 32 gate columns, and its 32 up columns, of a row are
+          // one block each, half in this lane and half in lane ^ 32. Codes go out as 32-byte row
+          // segments through the staging block ([gate | up] x [32 rows][32 B]), the step bytes
+          // straight (lanes 0-31 the gate's, 32-63 the up's).
+          int sc8[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const f32x4_t* hv = half == 0 ? gv : uv;
+            uint32_t am = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) am = max(am, __float_as_uint(hv[q][u]) & 0x7fffffffu);
+            am = max(am, (uint32_t)__shfl_xor((int)am, 32));
+            sc8[half] = ckpt_scale_code(am);
+            const float inv = ckpt_inv_step(sc8[half]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint32_t*>(stg + half * 1024 + r * 32 + q * 8 + hh * 4) =
+                  ckpt_codes4(hv[q][0], hv[q][1], hv[q][2], hv[q][3], inv);
+          }
+          wave_lds_fence();
+          u32x4_t cv[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) cv[half] = *reinterpret_cast<const u32x4_t*>(stg + half * 1024 + lane * 16);
+          wave_lds_fence();
+          const int m2 = m0r + (lane >> 1);
+          if (m2 < cm_end && c0 < mlp) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              sto(p.h_codes + (int64_t)m2 * 2 * mlp + half * mlp + c0 + (lane & 1) * 16, cv[half]);
+          }
+          if (m0r + r < cm_end && c0 < mlp)
+            p.h_scales[(int64_t)(m0r + r) * (mlp >> 4) + hh * (mlp >> 5) + (c0 >> 5)] = (uint8_t)(hh ? sc8[1] : sc8[0]);
+        }
+        if (EPI == EPI_SWIGLU && p.aux_out) {  // h kept in fp32 for the backward: the gate/up values the SwiGLU used, unrounded
 #pragma unroll
           for (int part = 0; part < 4; ++part) {  // gate cols 0-15, 16-31, then up cols 0-15, 16-31
             const int half = part >> 1, qq = part & 1;
@@ -1185,7 +1225,7 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
     const u32x4_t v = *reinterpret_cast<const u32x4_t*>(s_raw + (kt & (NST - 1)) * kRawStage + crow * 256 + cch * 16);
     const uint32_t c =
         *reinterpret_cast<const uint32_t*>(s_step + (kt & (NST - 1)) * kStepStage + crow * 32 + (cch >> 1) * 4);
-    float step = __uint_as_float(c == 255 ? 0x7fc00000u : c << 23) * 0.015625f;
+    float step = ckpt_step(c);
     step = crow < n - kt * GBK ? step : 0.0f;
     const float bias = -128.0f * step;
     uint8_t* tile = s_a + (kt & 1) * kOpStage;
@@ -1395,6 +1435,16 @@ hipError_t launch_grouped_gemm(int op, int epi, const uint16_t* A, const uint16_
   else if (op == OP_NT && epi == EPI_SWIGLU_BWD) { MOE_GEMM_LAUNCH(OP_NT, EPI_SWIGLU_BWD) }
   else return hipErrorInvalidValue;
 #undef MOE_GEMM_LAUNCH
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_swiglu_ckpt(const uint16_t* A, const uint16_t* B, const int32_t* group_offsets, int E, int64_t M,
+                                   int K, int N, const int32_t* row_slot, int n_slots, int slot_div, uint16_t* C,
+                                   int8_t* h_codes, uint8_t* h_scales, hipStream_t stream) {
+  if (M == 0) return hipSuccess;
+  const GemmP p{A, B, nullptr, nullptr, C, group_offsets, row_slot, nullptr, E, (int)M, K, N, n_slots, slot_div,
+                h_codes, h_scales};
+  gemm_kernel<OP_NN, EPI_SWIGLU_CKPT, true, false><<<dim3(persistent_grid()), dim3(GTHR), 0, stream>>>(p);
   return hipGetLastError();
 }
 

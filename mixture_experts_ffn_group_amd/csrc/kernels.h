@@ -38,6 +38,11 @@ hipError_t launch_grouped_gemm(int op, int epi, const uint16_t* A, const uint16_
                                const int32_t* row_slot, int n_slots, int slot_div, const float* slot_scale,
                                uint16_t* C, hipStream_t stream, int grid = 0);
 
+// GEMM 1 with the SwiGLU epilogue on gathered rows, keeping h as an 8-bit checkpoint.
+hipError_t launch_gemm_swiglu_ckpt(const uint16_t* A, const uint16_t* B, const int32_t* group_offsets, int E, int64_t M,
+                                   int K, int N, const int32_t* row_slot, int n_slots, int slot_div, uint16_t* C,
+                                   int8_t* h_codes, uint8_t* h_scales, hipStream_t stream);
+
 hipError_t launch_wgrad(const uint16_t* A, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
                         int Q, uint16_t* C, hipStream_t stream, int grid = 0);
 

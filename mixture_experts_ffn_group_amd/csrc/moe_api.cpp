@@ -911,4 +911,177 @@ int moe_ffn_bwd(const moe_shape_t* s, const moe_bf16_t* dy, const moe_saved_t* s
   return MOE_OK;
 }
 
+// Forward on a given routing: permute scratch, the index, the SwiGLU output and the rows of GEMM 2 (and, when the
+// full saved set is asked for, nothing of them is used but the scratch).
+size_t routed_ws(const moe_shape_t* s) {
+  const size_t S = (size_t)s->T * s->k;
+  return permute_ws(s) + round_up(s->E * 4) + round_up((s->E + 1) * 4) + round_up(S * 4) * 2 +
+         round_up(S * s->mlp * 2) /*a*/ + round_up(S * s->emb * 2) /*o*/;
+}
+// Backward from the 8-bit set: du and a, dh, and one [S, emb] buffer that holds do and then dxs.
+size_t bwd_ckpt_ws(const moe_shape_t* s) {
+  const size_t S = (size_t)s->T * s->k;
+  return 2 * round_up(S * s->mlp * 2) + round_up(S * 2 * s->mlp * 2) + round_up(S * s->emb * 2);
+}
+
+size_t moe_workspace_bytes_routed(const moe_shape_t* shape, int backward_ckpt) {
+  if (check_shape(shape) != MOE_OK) return 0;
+  return backward_ckpt ? bwd_ckpt_ws(shape) : routed_ws(shape);
+}
+
+int moe_ffn_fwd_routed(const moe_shape_t* s, const moe_bf16_t* x, const int32_t* topk_idx, const float* topk_w,
+                       const moe_bf16_t* wi, const moe_bf16_t* wo, moe_bf16_t* y, const moe_saved_t* saved,
+                       const moe_saved8_t* saved8, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_shape(s)) return rc;
+  if (saved && saved8) return fail(MOE_ERR_SHAPE, "saved and saved8 exclude each other");
+  const bool any = s->T > 0;
+  if (any) {
+    NEED(x);
+    NEED(topk_idx);
+    NEED(topk_w);
+    NEED(y);
+  }
+  NEED(wi);
+  NEED(wo);
+  NEED_WS(routed_ws(s));
+  if (saved) {
+    NEED(saved->group_sizes);
+    NEED(saved->group_offsets);
+    if (any) {
+      NEED(saved->sorted_slot);
+      NEED(saved->slot_row);
+      NEED(saved->xs);
+      MAYBE(saved->h);
+      NEED(saved->a);
+      NEED(saved->o);
+    }
+  }
+  if (saved8) {
+    NEED(saved8->group_sizes);
+    NEED(saved8->group_offsets);
+    if (any) {
+      NEED(saved8->sorted_slot);
+      NEED(saved8->slot_row);
+      NEED(saved8->x_codes);
+      NEED(saved8->x_scales);
+      NEED(saved8->h_codes);
+      NEED(saved8->h_scales);
+    }
+  }
+  const int64_t T = s->T, S = T * s->k;
+  const int emb = s->emb, mlp = s->mlp, E = s->E, k = s->k;
+  const hipStream_t st = (hipStream_t)stream;
+  Carver c{static_cast<char*>(ws)};
+  uint64_t* masks = c.take<uint64_t>(((T + moe::kPermuteBlock - 1) / moe::kPermuteBlock) * E);
+  int32_t* base = c.take<int32_t>(((T + moe::kPermuteBlock - 1) / moe::kPermuteBlock) * E);
+  moe_saved_t v;
+  v.group_sizes = c.take<int32_t>(E);
+  v.group_offsets = c.take<int32_t>(E + 1);
+  v.sorted_slot = c.take<int32_t>(S);
+  v.slot_row = c.take<int32_t>(S);
+  v.a = c.take<moe_bf16_t>(S * mlp);
+  v.o = c.take<moe_bf16_t>(S * emb);
+  v.xs = nullptr;
+  v.h = nullptr;
+  if (saved) v = *saved;
+  if (saved8) {
+    v.group_sizes = saved8->group_sizes;
+    v.group_offsets = saved8->group_offsets;
+    v.sorted_slot = saved8->sorted_slot;
+    v.slot_row = saved8->slot_row;
+  }
+  const bool gather = !saved;  // only the full set keeps the sorted rows
+  if (int rc = hip_status(moe::launch_permute(T, emb, E, k, x, topk_idx, v.group_sizes, v.group_offsets, v.sorted_slot,
+                                              v.slot_row, gather ? nullptr : v.xs, masks, base, st),
+                          "permute"))
+    return rc;
+  if (saved8) {
+    if (int rc = hip_status(moe::launch_ckpt_quantize(x, true, T, emb, saved8->x_codes, saved8->x_scales, st), "x"))
+      return rc;
+    if (int rc = hip_status(moe::launch_gemm_swiglu_ckpt(x, wi, v.group_offsets, E, S, emb, 2 * mlp, v.sorted_slot,
+                                                         (int)S, k, v.a, saved8->h_codes, saved8->h_scales, st),
+                            "gemm1"))
+      return rc;
+  } else if (int rc = hip_status(moe::launch_grouped_gemm(MOE_NN, MOE_EPI_SWIGLU, gather ? x : v.xs, wi, nullptr, v.h,
+                                                          v.group_offsets, E, S, emb, 2 * mlp,
+                                                          gather ? v.sorted_slot : nullptr, gather ? (int)S : 0,
+                                                          gather ? k : 1, nullptr, v.a, st),
+                                 "gemm1")) {
+    return rc;
+  }
+  if (int rc = hip_status(moe::launch_grouped_gemm(MOE_NN, MOE_EPI_NONE, v.a, wo, nullptr, nullptr, v.group_offsets,
+                                                   E, S, mlp, emb, nullptr, 0, 1, nullptr, v.o, st),
+                          "gemm2"))
+    return rc;
+  return hip_status(moe::launch_combine(T, emb, k, v.o, v.slot_row, topk_w, y, st), "combine");
+}
+
+int moe_ffn_bwd_ckpt(const moe_shape_t* s, const moe_bf16_t* dy, const float* topk_w, const moe_saved8_t* saved8,
+                     const moe_bf16_t* wi, const moe_bf16_t* wo, moe_bf16_t* dx, moe_bf16_t* dwi, moe_bf16_t* dwo,
+                     float* dtopk_w, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_shape(s)) return rc;
+  if (!saved8) return fail(MOE_ERR_NULL, "saved8 is NULL");
+  NEED(saved8->group_offsets);
+  if (s->T > 0) {
+    NEED(dy);
+    NEED(topk_w);
+    NEED(saved8->sorted_slot);
+    NEED(saved8->slot_row);
+    NEED(saved8->x_codes);
+    NEED(saved8->x_scales);
+    NEED(saved8->h_codes);
+    NEED(saved8->h_scales);
+  }
+  NEED(wi);
+  NEED(wo);
+  MAYBE(dx);
+  MAYBE(dwi);
+  MAYBE(dwo);
+  MAYBE(dtopk_w);
+  NEED_WS(bwd_ckpt_ws(s));
+  const int64_t T = s->T, S = T * s->k;
+  const int emb = s->emb, mlp = s->mlp, E = s->E, k = s->k;
+  const hipStream_t st = (hipStream_t)stream;
+  Carver c{static_cast<char*>(ws)};
+  moe_bf16_t* du = c.take<moe_bf16_t>(S * mlp);
+  moe_bf16_t* a = c.take<moe_bf16_t>(S * mlp);
+  moe_bf16_t* dh = c.take<moe_bf16_t>(S * 2 * mlp);
+  moe_bf16_t* rows = c.take<moe_bf16_t>(S * emb);
+  // the gradient of the unscaled SwiGLU output, dy . wo[e]^T, dy rows read in place through sorted_slot
+  if (int rc = hip_status(moe::launch_grouped_gemm(MOE_NT, MOE_EPI_NONE, dy, wo, nullptr, nullptr,
+                                                   saved8->group_offsets, E, S, emb, mlp, saved8->sorted_slot, (int)S,
+                                                   k, nullptr, du, st),
+                          "du"))
+    return rc;
+  if (int rc = hip_status(moe::launch_swiglu_bwd_ckpt(S, mlp, du, saved8->h_codes, saved8->h_scales,
+                                                      saved8->sorted_slot, topk_w, dh, dwo ? a : nullptr, dtopk_w, st),
+                          "swiglu_bwd"))
+    return rc;
+  if (dwo) {
+    if (int rc = hip_status(moe::launch_combine_bwd(T, emb, k, dy, nullptr, saved8->slot_row, topk_w, rows, nullptr,
+                                                    st),
+                            "combine_bwd"))
+      return rc;
+    if (int rc = hip_status(moe::launch_wgrad(a, rows, saved8->group_offsets, E, S, mlp, emb, dwo, st), "dwo"))
+      return rc;
+  }
+  if (dwi) {
+    if (int rc = hip_status(moe::launch_wgrad_ckpt(saved8->x_codes, saved8->x_scales, T, saved8->sorted_slot, k, dh,
+                                                   saved8->group_offsets, E, S, emb, 2 * mlp, dwi, st),
+                            "dwi"))
+      return rc;
+  }
+  if (dx) {
+    if (int rc = hip_status(moe::launch_grouped_gemm(MOE_NT, MOE_EPI_NONE, dh, wi, nullptr, nullptr,
+                                                     saved8->group_offsets, E, S, 2 * mlp, emb, nullptr, 0, 1, nullptr,
+                                                     rows, st),
+                            "dxs"))
+      return rc;
+    if (int rc = hip_status(moe::launch_combine(T, emb, k, rows, saved8->slot_row, nullptr, dx, st), "dx")) return rc;
+  }
+  return MOE_OK;
+}
+
 }  // extern "C"

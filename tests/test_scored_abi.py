@@ -96,6 +96,40 @@ def test_wgrad_ckpt_refusals(lib):
     assert w(out=ODD) == _lib.MOE_ERR_ALIGN
 
 
+def test_routed_layer_refusals(lib):
+    S = C.byref(_lib.shape(64, 128, 256, 8, 2))
+    full, int8 = _lib.MoeSaved(*([0x1000] * 10)), _lib.MoeSaved8(*([0x1000] * 8))
+    big = 1 << 40
+
+    def fwd(shape=S, x=FAKE, idx=FAKE, w=FAKE, wi=FAKE, y=FAKE, saved=None, saved8=None, ws=FAKE, n=big):
+        return lib.moe_ffn_fwd_routed(shape, x, idx, w, wi, FAKE, y, saved, saved8, ws, n, None)
+
+    assert fwd(saved=C.byref(full), saved8=C.byref(int8)) == _lib.MOE_ERR_SHAPE
+    assert fwd(idx=None) == _lib.MOE_ERR_NULL
+    assert fwd(w=ODD) == _lib.MOE_ERR_ALIGN
+    assert fwd(wi=None) == _lib.MOE_ERR_NULL
+    assert fwd(n=64) == _lib.MOE_ERR_WORKSPACE
+    assert fwd(shape=C.byref(_lib.shape(64, 96, 256, 8, 2))) == _lib.MOE_ERR_UNSUPPORTED
+    for i in range(8):
+        part = _lib.MoeSaved8(*[0 if j == i else 0x1000 for j in range(8)])
+        assert fwd(saved8=C.byref(part)) == _lib.MOE_ERR_NULL
+
+    def bwd(shape=S, dy=FAKE, w=FAKE, saved8=int8, dx=FAKE, n=big):
+        return lib.moe_ffn_bwd_ckpt(shape, dy, w, None if saved8 is None else C.byref(saved8), FAKE, FAKE, dx, FAKE,
+                                    FAKE, FAKE, FAKE, n, None)
+
+    assert bwd(saved8=None) == _lib.MOE_ERR_NULL
+    assert bwd(dy=None) == _lib.MOE_ERR_NULL
+    assert bwd(w=None) == _lib.MOE_ERR_NULL
+    assert bwd(dx=ODD) == _lib.MOE_ERR_ALIGN
+    assert bwd(n=64) == _lib.MOE_ERR_WORKSPACE
+    for i in range(1, 8):  # group_sizes alone is not read by the backward
+        part = _lib.MoeSaved8(*[0 if j == i else 0x1000 for j in range(8)])
+        assert bwd(saved8=part) == _lib.MOE_ERR_NULL
+    assert lib.moe_workspace_bytes_routed(S, 1) >= 128 * (4 * 256 * 2 + 128 * 2)
+    assert lib.moe_workspace_bytes_routed(C.byref(_lib.shape(64, 96, 256, 8, 2)), 0) == 0
+
+
 def test_binding_refuses_host_tensors_types_and_shapes():
     l = torch.zeros(4, 8)
     with pytest.raises(ValueError, match="HIP device"):
