@@ -17,6 +17,7 @@
 // the logits, which is exact.
 #include "common.h"
 #include "kernels.h"
+#include "lanes.h"
 
 namespace moe {
 namespace {
@@ -54,18 +55,11 @@ struct RouteP {
 };
 
 __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-#pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) {
-    const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)v, s);
-    v = o > v ? o : v;
-  }
-  return v;
+  const uint32_t hi = wave_max_u32((uint32_t)(v >> 32));
+  const uint32_t lo = wave_max_u32((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((uint64_t)hi << 32) | lo;
 }
-__device__ __forceinline__ int wave_min_i32(int v) {
-#pragma unroll
-  for (int s = 32; s >= 1; s >>= 1) v = min(v, __shfl_xor(v, s));
-  return v;
-}
+__device__ __forceinline__ int wave_min_i32(int v) { return (int)~wave_max_u32(~(uint32_t)v); }  // v >= 0
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
   for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s);
@@ -134,6 +128,7 @@ __device__ void route_row_exact(const RouteP& p, int64_t t, const float (&l)[4],
     wave_lds_fence();
     for (int g = lane; g < p.n_group; g += 64) {
       double a = -(double)INFINITY, b = -(double)INFINITY;
+#pragma unroll 8
       for (int i = 0; i < gs; ++i) {
         const double v = row_c[g * gs + i];
         b = fmax(b, fmin(a, v));
@@ -148,6 +143,7 @@ __device__ void route_row_exact(const RouteP& p, int64_t t, const float (&l)[4],
     for (int i = 0, g = lane; g < p.n_group; ++i, g += 64) {
       const uint64_t mine = row_g[g];
       int before = 0;
+#pragma unroll 8
       for (int h = 0; h < p.n_group; ++h) before += row_g[h] > mine || (row_g[h] == mine && h < g);
       if (before < p.topk_group) keep |= 1u << i;
     }
@@ -205,6 +201,309 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __
 #pragma unroll
     for (int q = 0; q < 4; ++q) l[q] = lane + 64 * q < p.E ? load_logit(logits + t * p.E + lane + 64 * q) : -INFINITY;
     route_row_exact(p, t, l, s_c[wave], s_g[wave]);
+  }
+}
+
+// Four tokens a wave, token g of the group on lanes 16g .. 16g+15, for k <= 16.
+//
+// The choice runs on 28-bit integers: lane r holds experts 4 (r + 16 q) + i as
+// keys value << 4 | (15 - (4 q + i)), so a sort is min and max only and a pick's
+// key tells which of its lane's experts it is. Without a bias the value is
+// (l - row maximum) in units of 2^-22, which never inverts the order of two
+// logits; with one it is c in units of 2^-26 from 32-bit arithmetic, off by
+// less than `thr` / 2 units. The picks stand if every pick and the first expert
+// not picked differ from the next by more than thr. Otherwise (about one token
+// in 1000 with a bias) the 16 best candidates are ranked by their exact values,
+// one a lane; that needs 64-bit scores of 16 experts rather than all. What is
+// left goes to route_row_exact: groups at the edge that are closer than their
+// error, a pick that is disabled, values out of the integers' range, more close
+// values than candidates, close softmax scores under a bias (their 64-bit sum
+// runs over all experts). bf16 logits without a bias leave 16 bits for the
+// expert itself: those keys are exact, ties included.
+//
+// Per four tokens of 128 experts about 400 vector instructions and no LDS
+// without groups, against some 4000 of the 64-bit form.
+constexpr int kHalf28 = 1 << 27;
+
+template <class V, int N>
+__device__ __forceinline__ void load_row16(const V* row, int E, int r, float (&l)[N]) {
+  const bool vec = (E & 3) == 0;
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) {
+    const int e0 = 4 * (r + 16 * q);
+    if (vec) {
+      if (e0 < E) {
+        if (sizeof(V) == 4) {
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + e0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[4 * q + i] = v[i];
+        } else {
+          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(row + e0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[4 * q + i] = (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[4 * q + i] = -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[4 * q + i] = e0 + i < E ? load_logit(row + e0 + i) : -INFINITY;
+    }
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_max_f32(float v) {
+  v = fmaxf(v, dpp_f32<0xb1>(v));
+  v = fmaxf(v, dpp_f32<0x4e>(v));
+  v = fmaxf(v, dpp_f32<0x141>(v));
+  return fmaxf(v, dpp_f32<0x140>(v));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double row_sum_f64(double v) {
+  v += dpp_f64<0xb1>(v);
+  v += dpp_f64<0x4e>(v);
+  v += dpp_f64<0x141>(v);
+  return v + dpp_f64<0x140>(v);
+}
+__device__ __forceinline__ uint32_t row_min_u32(uint32_t v) { return ~row_max_fused(~v); }
+
+// group values before this lane's own, over the 16 lanes of the row (rotations by 1 .. 15)
+template <int S>
+__device__ __forceinline__ int count_larger(uint32_t v) {
+  const int c = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + S, 0xf, 0xf, true) > v;
+  if constexpr (S < 15) return c + count_larger<S + 1>(v);
+  return c;
+}
+
+// the same by (value, lower id first), a total order: a rank
+template <int S>
+__device__ __forceinline__ int count_before(double v, int id) {
+  const double ov = dpp_f64<0x120 + S>(v);
+  const int oid = __builtin_amdgcn_mov_dpp(id, 0x120 + S, 0xf, 0xf, true);
+  const int c = ov > v || (ov == v && oid < id);
+  if constexpr (S < 15) return c + count_before<S + 1>(v, id);
+  return c;
+}
+
+// CHOICE: the order is that of c (a bias, or group values that are sums of scores), else of the logits.
+template <class V, int N, bool CHOICE>
+__global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* __restrict__ logits) {
+  constexpr bool EXACT16 = sizeof(V) == 2 && !CHOICE;
+  __shared__ double s_c[4][kMaxE];
+  __shared__ uint64_t s_g[4][kMaxE];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, r = lane & 15;
+  const int E = p.E, k = p.k;
+  const bool groups = p.topk_group < p.n_group;
+  // 2 x the error of c in 2^-26: sigmoid 20 units (exponential, 1 + e, reciprocal, + b, truncation);
+  // softmax 100 (its sum, 20 additions); and none for logits
+  const uint32_t thr = CHOICE ? (p.score == 0 ? 256u : 64u) : 0u;
+  for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4; t0 < p.T; t0 += (int64_t)gridDim.x * 16) {
+    const int64_t t = min(t0 + g, p.T - 1);
+    const V* row = logits + t * E;
+    float l[N];
+    load_row16<V, N>(row, E, r, l);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      l[i] = fmaxf(l[i], -INFINITY);  // NaN -> -inf
+      mx = fmaxf(mx, l[i]);
+    }
+    mx = row_max_f32(mx);
+    bool flag = !(fabsf(mx) < INFINITY);
+    uint32_t key[N];
+    if (CHOICE) {
+      float c[N];
+      if (p.score == 0) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          c[i] = __expf(l[i] - mx);
+          sum += c[i];
+        }
+        sum = row_sum(sum);
+        const float inv = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] *= inv;
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = sigmoid_f(l[i]);
+      }
+      if (p.bias) {
+        float b[N];
+        load_row16<float, N>(p.bias, E, r, b);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          c[i] += b[i];
+          if (!(b[i] > -INFINITY)) l[i] = -INFINITY;  // disabled by its bias
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool on = l[i] > -INFINITY;
+        flag |= on && !(fabsf(c[i]) < 1.99f);
+        const int v = (int)(c[i] * 67108864.0f) + kHalf28;
+        key[i] = on ? ((uint32_t)max(v, 1) << 4) | (uint32_t)(15 - i) : 0u;
+      }
+    } else if (EXACT16) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint32_t u = __float_as_uint(l[i]) >> 16;
+        if ((u & 0x7fffu) == 0) u = 0;
+        u = (u & 0x8000u) ? (~u & 0xffffu) : (u | 0x8000u);
+        const int e = 4 * (r + 16 * (i >> 2)) + (i & 3);
+        key[i] = l[i] > -INFINITY ? (u << 16) | (uint32_t)(0xffff - e) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int v = (int)((l[i] - mx) * 4194304.0f) + kHalf28;  // saturates below
+        key[i] = v > 0 && l[i] > -INFINITY ? ((uint32_t)v << 4) | (uint32_t)(15 - i) : 0u;
+      }
+    }
+    if (groups) {
+      // the two largest values of each run of four experts, then of each group on its own lane
+      const int gs = E / p.n_group, nq = gs >> 2;
+      uint32_t* quad = reinterpret_cast<uint32_t*>(s_c[wave]) + g * 128;
+      constexpr int SH = EXACT16 ? 16 : 4;
+      wave_lds_fence();
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const uint32_t a = max(key[4 * q], key[4 * q + 1]) >> SH, b = min(key[4 * q], key[4 * q + 1]) >> SH;
+        const uint32_t c = max(key[4 * q + 2], key[4 * q + 3]) >> SH, d = min(key[4 * q + 2], key[4 * q + 3]) >> SH;
+        *reinterpret_cast<u32x2_t*>(quad + 2 * (r + 16 * q)) = u32x2_t{max(a, c), max(min(a, c), max(b, d))};
+      }
+      wave_lds_fence();
+      uint32_t a = 0, b = 0;
+      if (r < p.n_group)
+        for (int i = 0; i < nq; ++i) {
+          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(quad + 2 * (r * nq + i));
+          b = max(min(a, v[0]), max(b, v[1]));
+          a = max(a, v[0]);
+        }
+      wave_lds_fence();
+      uint32_t gv = a;
+      if (EXACT16) gv = r < p.n_group ? (a << 4) | (uint32_t)(15 - r) : 0u;  // ties to the lower group
+      else if (p.group_top == 2 && a != 0) gv = a + (b != 0 ? b : (uint32_t)kHalf28);
+      const bool keep = r < p.n_group && count_larger<1>(gv) < p.topk_group;
+      const uint64_t kept = __ballot(keep);
+      const uint32_t mask = (uint32_t)(kept >> (16 * g)) & 0xffffu;
+      const uint32_t lo = row_min_u32(keep ? gv : 0xffffffffu);
+      const uint32_t hi = row_max_fused(r < p.n_group && !keep ? gv : 0u);
+      flag |= __builtin_popcount(mask) != p.topk_group || lo <= hi + 2 * thr;
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const bool in = (mask >> min((4 * (r + 16 * q)) / gs, 31)) & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) key[4 * q + i] = in ? key[4 * q + i] : 0u;
+      }
+    }
+    sort_desc(key);
+    uint32_t my = 0, prev = 0xffffffffu;
+    int my_r = 0;
+    bool near = false;
+    constexpr uint32_t kFirst = EXACT16 ? 0x10000u : 16u;  // smallest key of an enabled expert
+    // round j: the row's largest key goes to lane j (of its holders the lowest lane's; equal keys are near)
+    auto round = [&](int j) -> uint32_t {
+      const uint32_t m = row_max_fused(key[0]);
+      const uint64_t wins = __ballot(key[0] == m);
+      const int first = __builtin_ctz((uint32_t)(wins >> (16 * g)) & 0xffffu);
+      if (r == j) {
+        my = m;
+        my_r = first;
+      }
+      // the winner's keys move up by one: a bitwise select on an opaque mask, which the compiler cannot
+      // turn into a choice of registers at run time
+      uint32_t pop = 0u - (uint32_t)(r == first);
+      asm volatile("" : "+v"(pop));
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = ((i + 1 < N ? key[i + 1] : 0u) & pop) | (key[i] & ~pop);
+      return m;
+    };
+    for (int j = 0; j < k; ++j) {
+      const uint32_t m = round(j);
+      if (!EXACT16) near |= ((prev >> 4) - (m >> 4)) <= thr;
+      flag |= m < kFirst;
+      prev = m;
+    }
+    if (!EXACT16) {  // the first one not picked, if there is one
+      const uint32_t m = row_max_fused(key[0]);
+      const bool close = m >= kFirst && ((prev >> 4) - (m >> 4)) <= thr;
+      near |= close;
+      flag |= close && k == 16;
+      if (CHOICE && p.bias && p.score == 0) {
+        flag |= near;
+        near = false;
+      }
+    }
+    auto expert = [&]() -> int {
+      if (EXACT16) return (int)(0xffffu - (my & 0xffffu));
+      const int i = 15 - (int)(my & 15u);
+      return 4 * (my_r + 16 * (i >> 2)) + (i & 3);
+    };
+    int e = expert();
+    if (!EXACT16 && __ballot(near) != 0) {
+      // Close values: the 16 best candidates, one a lane, ranked by their exact choice values. The order
+      // stands if none beyond them can reach the picks.
+      for (int j = k; j < 16; ++j) {
+        const uint32_t m = round(j);
+        if (j == 15) flag |= near && m >= kFirst && ((prev >> 4) - (m >> 4)) <= thr;
+      }
+      e = expert();
+      double o = -(double)INFINITY;
+      int id = 0x10000 + r;  // no candidate: after all others
+      if (my >= kFirst) {
+        id = e;
+        o = (double)load_logit(row + e);
+        if (p.bias) o = 1.0 / (1.0 + exp(-o)) + (double)p.bias[e];
+      }
+      const int rank = count_before<1>(o, id);
+      e = __builtin_amdgcn_ds_permute((16 * g + rank) << 2, e);
+    }
+    const uint64_t flags = __ballot(flag);
+    const bool slow = ((flags >> (16 * g)) & 0xffffull) != 0;
+    // weights in 64 bits, a lane a pick
+    double s = 0.0;
+    if (r < k && !slow) {
+      const double x = (double)load_logit(row + e);
+      s = p.score == 0 ? exp(x - (double)mx) : 1.0 / (1.0 + exp(-x));
+    }
+    if (p.renorm) {
+      const double tot = row_sum_f64(s);
+      s = tot > 0.0 ? s / tot : 0.0;
+    } else if (p.score == 0) {
+      double sum = 0.0;
+      // (a bias may have disabled experts that count in the sum: their logits are read again)
+      if (CHOICE) load_row16<V, N>(row, E, r, l);
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum += (double)expf(fmaxf(l[i], -INFINITY) - mx);
+      s /= row_sum_f64(sum);
+    }
+    if (r < k && !slow && t0 + g < p.T) {
+      p.idx[t * k + r] = e;
+      p.w[t * k + r] = (float)(s * (double)p.scale);
+    }
+    if (flags != 0) {
+      for (int h = 0; h < 4; ++h) {
+        if (((flags >> (16 * h)) & 0xffffull) == 0 || t0 + h >= p.T) continue;
+        float lw[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          lw[q] = lane + 64 * q < E ? load_logit(logits + (t0 + h) * E + lane + 64 * q) : -INFINITY;
+        route_row_exact(p, t0 + h, lw, s_c[wave], s_g[wave]);
+      }
+    }
   }
 }
 
@@ -280,6 +579,14 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(RouteBwdP p, cons
   }
 }
 
+template <class V, int N>
+void launch16(const RouteP& p, const V* logits, bool choice, hipStream_t stream) {
+  const int64_t b = (p.T + 15) / 16;
+  const dim3 grid((unsigned)(b < (int64_t(1) << 20) ? b : (int64_t(1) << 20)));
+  if (choice) route_scored16_kernel<V, N, true><<<grid, dim3(256), 0, stream>>>(p, logits);
+  else route_scored16_kernel<V, N, false><<<grid, dim3(256), 0, stream>>>(p, logits);
+}
+
 dim3 row_grid(int64_t T) {
   const int64_t b = (T + 3) / 4;
   return dim3((unsigned)(b < (int64_t(1) << 20) ? b : (int64_t(1) << 20)));
@@ -292,10 +599,25 @@ hipError_t launch_route_scored(int64_t T, int E, int k, int score, int n_group, 
                                int32_t* topk_idx, float* topk_w, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const RouteP p{T, E, k, score, n_group, topk_group, group_top, renorm, scale, bias, topk_idx, topk_w};
-  if (logits_bf16)
+  const bool groups = topk_group < n_group;
+  const bool choice = bias != nullptr || (groups && group_top == 2);
+  if (k <= 16 && (!groups || (n_group <= 16 && (E / n_group) % 4 == 0))) {
+    if (logits_bf16) {
+      const uint16_t* l = static_cast<const uint16_t*>(logits);
+      if (E <= 64) launch16<uint16_t, 4>(p, l, choice, stream);
+      else if (E <= 128) launch16<uint16_t, 8>(p, l, choice, stream);
+      else launch16<uint16_t, 16>(p, l, choice, stream);
+    } else {
+      const float* l = static_cast<const float*>(logits);
+      if (E <= 64) launch16<float, 4>(p, l, choice, stream);
+      else if (E <= 128) launch16<float, 8>(p, l, choice, stream);
+      else launch16<float, 16>(p, l, choice, stream);
+    }
+  } else if (logits_bf16) {
     route_scored_kernel<uint16_t><<<row_grid(T), dim3(256), 0, stream>>>(p, static_cast<const uint16_t*>(logits));
-  else
+  } else {
     route_scored_kernel<float><<<row_grid(T), dim3(256), 0, stream>>>(p, static_cast<const float*>(logits));
+  }
   return hipGetLastError();
 }
 
