@@ -71,93 +71,94 @@ __device__ __forceinline__ float wave_max_f32(float v) {
   return v;
 }
 
-// One token on one wave, everything in 64 bits. l[q] is the logit of expert
-// lane + 64 q (ignored at or past E); row_c and row_g are the wave's own LDS.
-__device__ void route_row_exact(const RouteP& p, int64_t t, const float (&l)[4], double* row_c, uint64_t* row_g) {
+// One token on one wave, everything in 64 bits. The row's scores and keys stay
+// in LDS (row_s, row_k [E], row_g [n_group], the wave's own) rather than in
+// registers: the four-token kernel below runs this for few tokens, and the
+// registers it would hold there cost that kernel half its waves.
+template <class V>
+__device__ void route_row_exact(const RouteP& p, int64_t t, const V* row, double* row_s, uint64_t* row_k,
+                                uint64_t* row_g) {
   const int lane = threadIdx.x & 63;
   const int E = p.E;
-  bool on[4];
   float mx = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    on[q] = lane + 64 * q < E && l[q] == l[q] && l[q] != -INFINITY;
-    if (on[q]) mx = fmaxf(mx, l[q]);
-  }
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) mx = fmaxf(mx, fmaxf(load_logit(row + e), -INFINITY));
   mx = wave_max_f32(mx);
-  double s[4];
   double sum = 0.0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    s[q] = 0.0;
-    if (!on[q]) continue;
-    if (p.score == 0) s[q] = l[q] == mx ? 1.0 : exp((double)l[q] - (double)mx);
-    else s[q] = 1.0 / (1.0 + exp(-(double)l[q]));
-    sum += s[q];
-  }
-  if (p.score == 0) {
-    sum = wave_sum_f64(sum);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (on[q]) s[q] /= sum;
-  }
-  uint64_t key[4];
-  double choice[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = lane + 64 * q;
-    double c = s[q];
-    if (e < E && p.bias) {
-      const float b = p.bias[e];
-      on[q] = on[q] && b == b && b != -INFINITY;
-      c += (double)b;
+  wave_lds_fence();
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    const float l = load_logit(row + e);
+    double s = 0.0;
+    if (l > -INFINITY) {  // false for NaN
+      const double x = p.score == 0 ? (l == mx ? 0.0 : (double)l - (double)mx) : -(double)l;
+      s = exp(x);
+      if (p.score != 0) s = 1.0 / (1.0 + s);
     }
-    choice[q] = on[q] ? c : -(double)INFINITY;
-    const double o = p.bias ? c : (double)l[q];
-    key[q] = e < E ? (on[q] ? order_key64(o) : kKeyNegInf) : 0ull;
+    row_s[e] = s;
+    sum += s;
   }
+  if (p.score == 0) sum = wave_sum_f64(sum);
+  else sum = 1.0;
+  const bool by_logit = p.group_top == 1 && !p.bias;  // group values that order as the logits
+  wave_lds_fence();
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    const float l = load_logit(row + e), b = p.bias ? p.bias[e] : 0.0f;
+    const bool on = l > -INFINITY && b > -INFINITY;
+    const double s = row_s[e] / sum;  // sum 0: no logit is on
+    if (on) row_s[e] = s;
+    row_k[e] = on ? order_key64(p.bias ? s + (double)b : (double)l) : kKeyNegInf;
+  }
+  wave_lds_fence();
   if (p.topk_group < p.n_group) {
-    // group values by lane (several groups a lane past 64), from the row in LDS; a group's value
-    // orders by the logits where it is one of them
     const int gs = E / p.n_group;
-    wave_lds_fence();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e = lane + 64 * q;
-      if (e < E) row_c[e] = (!p.bias && p.group_top == 1 && on[q]) ? (double)l[q] : choice[q];
-    }
-    wave_lds_fence();
+#pragma unroll 1
     for (int g = lane; g < p.n_group; g += 64) {
-      double a = -(double)INFINITY, b = -(double)INFINITY;
-#pragma unroll 8
+      uint64_t ka = 0, kb = 0;            // the two largest keys
+      double a = 0.0, b = 0.0;            // and the two largest choice values of enabled experts
+#pragma unroll 1
       for (int i = 0; i < gs; ++i) {
-        const double v = row_c[g * gs + i];
-        b = fmax(b, fmin(a, v));
-        a = fmax(a, v);
+        const int e = g * gs + i;
+        const uint64_t kk = row_k[e];
+        if (kk <= kKeyNegInf) continue;
+        const double v = row_s[e] + (p.bias ? (double)p.bias[e] : 0.0);
+        if (kb == 0 && ka == 0) a = v;
+        else if (kb == 0) b = v > a ? a : v, a = v > a ? v : a;
+        else if (v > a) b = a, a = v;
+        else if (v > b) b = v;
+        kb = max(kb, min(ka, kk));
+        ka = max(ka, kk);
       }
-      if (p.group_top == 2 && b != -(double)INFINITY) a += b;
-      row_g[g] = order_key64(a);
+      const uint64_t top2 = kb != 0 ? order_key64(a + b) : (ka != 0 ? order_key64(a) : kKeyNegInf);
+      row_g[g] = p.group_top == 2 ? top2 : (by_logit || ka == 0 ? (ka != 0 ? ka : kKeyNegInf) : order_key64(a));
     }
     wave_lds_fence();
-    // a group stays if fewer than topk_group others come before it
+    // a group stays if fewer than topk_group others come before it (4 groups a lane at most)
     uint32_t keep = 0;
+#pragma unroll 1
     for (int i = 0, g = lane; g < p.n_group; ++i, g += 64) {
       const uint64_t mine = row_g[g];
       int before = 0;
-#pragma unroll 8
+#pragma unroll 1
       for (int h = 0; h < p.n_group; ++h) before += row_g[h] > mine || (row_g[h] == mine && h < g);
       if (before < p.topk_group) keep |= 1u << i;
     }
     wave_lds_fence();
+#pragma unroll 1
     for (int i = 0, g = lane; g < p.n_group; ++i, g += 64) row_g[g] = (keep >> i) & 1;
     wave_lds_fence();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int e = lane + 64 * q;
-      if (e < E && !row_g[e / gs]) key[q] = kKeyNegInf;
-    }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64)
+      if (!row_g[e / gs]) row_k[e] = kKeyNegInf;
+    wave_lds_fence();
   }
   int my_e = 0;
   double my_s = 0.0;
+  uint64_t key[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) key[q] = lane + 64 * q < E ? row_k[lane + 64 * q] : 0ull;
+#pragma unroll 1
   for (int j = 0; j < p.k; ++j) {
     uint64_t best = 0;
 #pragma unroll
@@ -168,17 +169,12 @@ __device__ void route_row_exact(const RouteP& p, int64_t t, const float (&l)[4],
     for (int q = 3; q >= 0; --q)
       if (key[q] == best && lane + 64 * q < E) e = min(e, lane + 64 * q);
     e = wave_min_i32(e);
-    double sj = 0.0;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (e == lane + 64 * q) {
-        sj = key[q] > kKeyNegInf ? s[q] : 0.0;
-        key[q] = 0ull;
-      }
-    sj = __shfl(sj, e & 63);
+      if (e == lane + 64 * q) key[q] = 0ull;
     if (lane == j) {
       my_e = e;
-      my_s = sj;
+      my_s = best > kKeyNegInf ? row_s[e] : 0.0;
     }
   }
   if (p.renorm) {
@@ -189,19 +185,16 @@ __device__ void route_row_exact(const RouteP& p, int64_t t, const float (&l)[4],
     p.idx[t * p.k + lane] = my_e;
     p.w[t * p.k + lane] = (float)(my_s * (double)p.scale);
   }
+  wave_lds_fence();
 }
 
 template <class V>
 __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __restrict__ logits) {
-  __shared__ double s_c[4][kMaxE];
-  __shared__ uint64_t s_g[4][kMaxE];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < p.T; t += (int64_t)gridDim.x * 4) {
-    float l[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) l[q] = lane + 64 * q < p.E ? load_logit(logits + t * p.E + lane + 64 * q) : -INFINITY;
-    route_row_exact(p, t, l, s_c[wave], s_g[wave]);
-  }
+  __shared__ double s_s[4][kMaxE];
+  __shared__ uint64_t s_k[4][kMaxE], s_g[4][kMaxE];
+  const int wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t < p.T) route_row_exact(p, t, logits + t * p.E, s_s[wave], s_k[wave], s_g[wave]);
 }
 
 // Four tokens a wave, token g of the group on lanes 16g .. 16g+15, for k <= 16.
@@ -215,10 +208,10 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __
 // not picked differ from the next by more than thr. Otherwise (about one token
 // in 1000 with a bias) the 16 best candidates are ranked by their exact values,
 // one a lane; that needs 64-bit scores of 16 experts rather than all. What is
-// left goes to route_row_exact: groups at the edge that are closer than their
-// error, a pick that is disabled, values out of the integers' range, more close
-// values than candidates, close softmax scores under a bias (their 64-bit sum
-// runs over all experts). bf16 logits without a bias leave 16 bits for the
+// left goes to route_row_exact: a pick that is disabled, values out of the
+// integers' range, more close values than candidates, close softmax scores
+// (their 64-bit sum runs over all experts). Groups too close at the edge of
+// those that stay are ranked the same way, by the exact scores of their two best. bf16 logits without a bias leave 16 bits for the
 // expert itself: those keys are exact, ties included.
 //
 // Per four tokens of 128 experts about 400 vector instructions and no LDS
@@ -300,8 +293,9 @@ __device__ __forceinline__ int count_before(double v, int id) {
 template <class V, int N, bool CHOICE>
 __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* __restrict__ logits) {
   constexpr bool EXACT16 = sizeof(V) == 2 && !CHOICE;
-  __shared__ double s_c[4][kMaxE];
-  __shared__ uint64_t s_g[4][kMaxE];
+  // a wave's row in the 64-bit form (scores, keys), or its four rows of 32-bit group values or keys
+  __shared__ double s_x[4][2 * kMaxE];
+  __shared__ uint64_t s_g[4][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r = lane & 15;
   const int E = p.E, k = p.k;
@@ -309,7 +303,8 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
   // 2 x the error of c in 2^-26: sigmoid 20 units (exponential, 1 + e, reciprocal, + b, truncation);
   // softmax 100 (its sum, 20 additions); and none for logits
   const uint32_t thr = CHOICE ? (p.score == 0 ? 256u : 64u) : 0u;
-  for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4; t0 < p.T; t0 += (int64_t)gridDim.x * 16) {
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4;
+  if (t0 < p.T) {  // no loop over tokens: it would keep every 64-bit constant in registers
     const int64_t t = min(t0 + g, p.T - 1);
     const V* row = logits + t * E;
     float l[N];
@@ -375,13 +370,13 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
     if (groups) {
       // the two largest values of each run of four experts, then of each group on its own lane
       const int gs = E / p.n_group, nq = gs >> 2;
-      uint32_t* quad = reinterpret_cast<uint32_t*>(s_c[wave]) + g * 128;
+      uint32_t* quad = reinterpret_cast<uint32_t*>(s_x[wave]) + g * 128;
       constexpr int SH = EXACT16 ? 16 : 4;
       wave_lds_fence();
 #pragma unroll
       for (int q = 0; q < N / 4; ++q) {
-        const uint32_t a = max(key[4 * q], key[4 * q + 1]) >> SH, b = min(key[4 * q], key[4 * q + 1]) >> SH;
-        const uint32_t c = max(key[4 * q + 2], key[4 * q + 3]) >> SH, d = min(key[4 * q + 2], key[4 * q + 3]) >> SH;
+        const uint32_t a = max(key[4 * q], key[4 * q + 1]), b = min(key[4 * q], key[4 * q + 1]);
+        const uint32_t c = max(key[4 * q + 2], key[4 * q + 3]), d = min(key[4 * q + 2], key[4 * q + 3]);
         *reinterpret_cast<u32x2_t*>(quad + 2 * (r + 16 * q)) = u32x2_t{max(a, c), max(min(a, c), max(b, d))};
       }
       wave_lds_fence();
@@ -392,16 +387,55 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
           b = max(min(a, v[0]), max(b, v[1]));
           a = max(a, v[0]);
         }
-      wave_lds_fence();
+      a >>= SH;
+      b >>= SH;
       uint32_t gv = a;
       if (EXACT16) gv = r < p.n_group ? (a << 4) | (uint32_t)(15 - r) : 0u;  // ties to the lower group
       else if (p.group_top == 2 && a != 0) gv = a + (b != 0 ? b : (uint32_t)kHalf28);
-      const bool keep = r < p.n_group && count_larger<1>(gv) < p.topk_group;
-      const uint64_t kept = __ballot(keep);
-      const uint32_t mask = (uint32_t)(kept >> (16 * g)) & 0xffffu;
+      bool keep = r < p.n_group && count_larger<1>(gv) < p.topk_group;
+      uint32_t mask = (uint32_t)(__ballot(keep) >> (16 * g)) & 0xffffu;
       const uint32_t lo = row_min_u32(keep ? gv : 0xffffffffu);
       const uint32_t hi = row_max_fused(r < p.n_group && !keep ? gv : 0u);
-      flag |= __builtin_popcount(mask) != p.topk_group || lo <= hi + 2 * thr;
+      const bool edge = __builtin_popcount(mask) != p.topk_group || lo <= hi + 2 * thr;
+      if (!EXACT16 && __ballot(edge) != 0) {
+        // Groups too close at the edge: ranked by their exact values, from the two best experts of each,
+        // scored in 64 bits on the group's lane. That needs both certain (the third further off than thr),
+        // and scores that do not hang on the row's sum.
+        uint32_t* const all = reinterpret_cast<uint32_t*>(s_x[wave]) + g * 256;
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < N; ++i) all[4 * (r + 16 * (i >> 2)) + (i & 3)] = key[i];
+        wave_lds_fence();
+        uint32_t ka = 0, kb = 0, kc = 0;
+        int ea = 0, eb = 0;
+        if (r < p.n_group)
+          for (int i = 0; i < gs; ++i) {
+            const uint32_t kk = all[r * gs + i];
+            const bool fa = kk > ka, fb = kk > kb;
+            kc = max(kc, fb ? kb : kk);
+            eb = fa ? ea : (fb ? r * gs + i : eb);
+            kb = fa ? ka : (fb ? kk : kb);
+            ea = fa ? r * gs + i : ea;
+            ka = fa ? kk : ka;
+          }
+        flag |= edge && (kc >= 16u && ((kb >> 4) - (kc >> 4)) <= thr);
+        if (p.score == 0 && CHOICE) flag |= edge;
+        double va = -(double)INFINITY, vb = -(double)INFINITY;
+        if (ka >= 16u) {
+          va = (double)load_logit(row + ea);
+          if (CHOICE) va = 1.0 / (1.0 + exp(-va)) + (p.bias ? (double)p.bias[ea] : 0.0);
+        }
+        if (kb >= 16u) {
+          vb = (double)load_logit(row + eb);
+          if (CHOICE) vb = 1.0 / (1.0 + exp(-vb)) + (p.bias ? (double)p.bias[eb] : 0.0);
+        }
+        double v = fmax(va, vb);
+        if (p.group_top == 2 && kb >= 16u) v = va > vb ? va + vb : vb + va;
+        const int rank = count_before<1>(v, r < p.n_group ? r : 16 + r);
+        if (edge) keep = r < p.n_group && rank < p.topk_group;
+        mask = (uint32_t)(__ballot(keep) >> (16 * g)) & 0xffffu;
+      }
+      wave_lds_fence();
 #pragma unroll
       for (int q = 0; q < N / 4; ++q) {
         const bool in = (mask >> min((4 * (r + 16 * q)) / gs, 31)) & 1;
@@ -497,11 +531,8 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
     if (flags != 0) {
       for (int h = 0; h < 4; ++h) {
         if (((flags >> (16 * h)) & 0xffffull) == 0 || t0 + h >= p.T) continue;
-        float lw[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          lw[q] = lane + 64 * q < E ? load_logit(logits + (t0 + h) * E + lane + 64 * q) : -INFINITY;
-        route_row_exact(p, t0 + h, lw, s_c[wave], s_g[wave]);
+        route_row_exact(p, t0 + h, logits + (t0 + h) * E, s_x[wave],
+                        reinterpret_cast<uint64_t*>(s_x[wave] + kMaxE), s_g[wave]);
       }
     }
   }
@@ -529,7 +560,8 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(RouteBwdP p, cons
   __shared__ float s_row[4][kMaxE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float* row = s_row[wave];
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < p.T; t += (int64_t)gridDim.x * 4) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t < p.T) {
     const V* lt = logits + t * p.E;
     int e = -1;
     float w = 0.0f, g = 0.0f;
@@ -581,16 +613,12 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(RouteBwdP p, cons
 
 template <class V, int N>
 void launch16(const RouteP& p, const V* logits, bool choice, hipStream_t stream) {
-  const int64_t b = (p.T + 15) / 16;
-  const dim3 grid((unsigned)(b < (int64_t(1) << 20) ? b : (int64_t(1) << 20)));
+  const dim3 grid((unsigned)((p.T + 15) / 16));  // T * 64 < 2^31: the shape check of the call
   if (choice) route_scored16_kernel<V, N, true><<<grid, dim3(256), 0, stream>>>(p, logits);
   else route_scored16_kernel<V, N, false><<<grid, dim3(256), 0, stream>>>(p, logits);
 }
 
-dim3 row_grid(int64_t T) {
-  const int64_t b = (T + 3) / 4;
-  return dim3((unsigned)(b < (int64_t(1) << 20) ? b : (int64_t(1) << 20)));
-}
+dim3 row_grid(int64_t T) { return dim3((unsigned)((T + 3) / 4)); }
 
 }  // namespace
 
