@@ -1087,24 +1087,22 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_kernel(WgradP p) {
 // 32 columns. Every value code * step is a bf16 number, so the bf16 matrix
 // cores multiply the checkpoint itself, without a rounding.
 //
-// Same tile, waves, deal and epilogue as wgrad_kernel; what differs is the
-// path of the left operand. Its codes (8 KB a k-slice, half the bf16 bytes)
-// and step bytes go global -> LDS like D, four k-slices ahead; between two
-// barriers each of the eight waves turns 1 KB of codes of the k-slice after
-// next into bf16, 16 elements a lane, into one of two [32][256] operand tiles.
-// The conversion is done once per element of the tile (each element feeds four
-// waves' fragments) and its 45 vector instructions a wave and k-slice run
-// beside the other wave's MFMAs. Converting into the sorted bf16 rows in
-// memory first would write and read 2 bytes an element and routed row more.
+// Waves, deal and roles as in wgrad_kernel (waves 0-3 copy, waves 4-7 store;
+// each owns 128 x 64 outputs), but the tile is 128 x 512: a code is turned into
+// bf16 once per 512 columns of D rather than once per 256, and that conversion
+// is what the kernel adds to the bf16 one. Codes and step bytes go global ->
+// LDS like D (codes four k-slices ahead, D two); between two barriers each of
+// the eight waves turns 512 bytes of the k-slice after next into one of two
+// [32][128] operand tiles. k-rows past the group end get a zero step (D's are
+// zeros by the copy's range); their codes are any row's.
 //
 // The mapping is read the same way: slot indices of 8 k-slices (64 per copying
 // wave, its own 8 rows of each) come in one copy into a ring, and each lane
-// takes the rows it copies from there. k-rows past the group end get a zero
-// step (D's are zeros by the copy's range); their codes are any row's.
+// takes the rows it copies from there.
 //
-// An iteration kt of the k-loop issues the codes and steps of k-slice kt + 5
-// and D of kt + 4, and its barrier needs codes and steps kt + 2 and D kt + 1:
-// two iterations' copies (14 a copying wave) may still be in flight.
+// An iteration kt of the k-loop issues codes and steps of k-slice kt + 5 and D
+// of kt + 3, and its barrier needs codes and steps kt + 2 and D kt + 1: one
+// iteration's copies (10 a copying wave) may still be in flight.
 struct WgradCkptP {
   const int8_t* A;
   const uint8_t* S;  // step codes [a_rows, P / 32]
@@ -1116,10 +1114,14 @@ struct WgradCkptP {
   uint32_t div_mul, div_shift;  // slot / slot_div = mulhi(2 slot, div_mul) >> div_shift
 };
 
-constexpr int kRawStage = 256 * GBK;      // codes of a k-slice: 8 KB
-constexpr int kStepStage = 8 * GBK * 4;   // steps of a k-slice, a dword each: 1 KB
-constexpr int kIdxChunk = 8;              // k-slices whose indices come in one copy
-constexpr int kIdxRing = 4;               // chunks of the index ring
+constexpr int kCkP = 128, kCkQ = 512;         // output tile
+constexpr int kCkTile = kCkP * GBK * 2;       // bf16 operand tile: 8 KB
+constexpr int kRawStage = kCkP * GBK;         // codes of a k-slice: 4 KB
+constexpr int kStepStage = kCkP / 32 * GBK * 4;  // steps of a k-slice, a dword each: 512 B
+constexpr int kCkDStage = kCkQ * GBK * 2;     // D of a k-slice: 32 KB
+constexpr int kCkDRing = 3;
+constexpr int kIdxChunk = 8;                  // k-slices whose indices come in one copy
+constexpr int kIdxRing = 4;                   // chunks of the index ring
 
 // 4 bytes per lane (lane L at lds + 4 L): the dword at base + voff, zero past the range
 __device__ __forceinline__ void b2lds4(i32x4_t rsrc, uint32_t voff, uint32_t lds) {
@@ -1132,48 +1134,44 @@ __device__ __forceinline__ void g2lds1(const void* sbase, uint32_t voff, uint32_
 
 template <bool GATHER>
 __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_a[2 * kOpStage];       // bf16 operand tiles
+  __shared__ __attribute__((aligned(1024))) uint8_t s_a[2 * kCkTile];  // bf16 operand tiles
+  __shared__ __attribute__((aligned(1024))) uint8_t s_d[kCkDRing * kCkDStage];
   __shared__ __attribute__((aligned(16))) uint8_t s_raw[NST * kRawStage];
-  __shared__ __attribute__((aligned(16))) uint8_t s_d[NST * kOpStage];
   __shared__ __attribute__((aligned(16))) uint8_t s_step[NST * kStepStage];
   __shared__ __attribute__((aligned(16))) int s_idx[4][kIdxRing][64];
   __shared__ __attribute__((aligned(16))) uint8_t s_stage[GTHR / 64][2048];
   __shared__ int s_off[kMaxExperts + 1];
   for (int i = threadIdx.x; i <= p.E; i += GTHR) s_off[i] = clamp_rows(p.off[i], p.M);
   __syncthreads();
-  const int tp = (p.P + 255) / 256, tq = (p.Q + 255) / 256;
+  const int tp = (p.P + kCkP - 1) / kCkP, tq = (p.Q + kCkQ - 1) / kCkQ;
   const int tid = opaque((int)threadIdx.x), lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 1, wn = wave >> 1;
-  const int wave_u = __builtin_amdgcn_readfirstlane(wave);
+  const int wave_u = __builtin_amdgcn_readfirstlane(wave);  // its 64 columns of the tile
   const bool loader = wave_u < 4;
-  const uint32_t lds_raw = lds_addr(s_raw) + wave_u * 2048, lds_step = lds_addr(s_step) + wave_u * 256;
-  const uint32_t lds_d = lds_addr(s_d) + wave_u * 4096;
+  const uint32_t lds_raw = lds_addr(s_raw) + wave_u * 1024, lds_step = lds_addr(s_step) + wave_u * 128;
+  const uint32_t lds_d = lds_addr(s_d) + wave_u * 8192;
   const uint32_t lds_idx = lds_addr(s_idx) + (wave_u & 3) * (kIdxRing * 256);
   auto kbarrier = []() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
   int e = 0, p0 = 0, q0 = 0, lo = 0, n = 0, nk = 0;
-  uint32_t a_col = 0, s_col = 0, d_off[2];
+  uint32_t a_col = 0, s_col = 0, d_off[4];
   auto decode = [&](int64_t it) -> bool {
     WgradTile wt;
     if (!wgrad_tile(it, blockIdx.x, gridDim.x, p.E, tp, tq, &wt)) return false;
     e = __builtin_amdgcn_readfirstlane(wt.e);
-    p0 = __builtin_amdgcn_readfirstlane(wt.pt * 256);
-    q0 = __builtin_amdgcn_readfirstlane(wt.qt * 256);
+    p0 = __builtin_amdgcn_readfirstlane(wt.pt * kCkP);
+    q0 = __builtin_amdgcn_readfirstlane(wt.qt * kCkQ);
     const int l0 = s_off[e], h0 = s_off[e + 1];
     lo = __builtin_amdgcn_readfirstlane(l0);
     n = __builtin_amdgcn_readfirstlane(h0 > l0 ? h0 - l0 : 0);
     nk = (n + GBK - 1) / GBK;
     if (!loader) return true;
-    // codes: copy j covers rows 8 wave + 4 j + lane / 16, 16 columns a lane; columns past P read
-    // others and only feed outputs that are never stored
-    a_col = (uint32_t)(p0 + 16 * (lane & 15) < p.P ? p0 + 16 * (lane & 15) : 0);
-    s_col = (uint32_t)min((p0 >> 5) + (lane & 7), (p.P >> 5) - 1);
+    // codes: rows 8 wave + lane / 8, 16 columns a lane; steps: rows 8 wave + lane / 4, lanes 0-31. Columns past P
+    // read others and only feed outputs that are never stored.
+    a_col = (uint32_t)(p0 + 16 * (lane & 7) < p.P ? p0 + 16 * (lane & 7) : 0);
+    s_col = (uint32_t)min((p0 >> 5) + (lane & 3), (p.P >> 5) - 1);
+    // D: copy j is row 8 wave + j (1 KB), lane L at chunk L holding chunk L ^ ((j & 3) << 2)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int krow = (wave_u * 4 + j) * 2 + (lane >> 5);
-      const int c = (lane & 31) ^ ((krow & 3) << 2);
-      d_off[j] = (uint32_t)(krow * p.Q + q0 + c * 8) * 2u;
-    }
+    for (int j = 0; j < 4; ++j) d_off[j] = (uint32_t)((wave_u * 8 + j) * p.Q + q0 + (lane ^ (j << 2)) * 8) * 2u;
     return true;
   };
   // index chunk c of the group: this copying wave's 8 rows of k-slices 8c .. 8c + 7 (lane = slice * 8 + row)
@@ -1182,31 +1180,45 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
     const i32x4_t ri = buffer_rsrc(p.row_slot + lo + r0, (uint32_t)min(n - r0, kIdxChunk * GBK) * 4u);
     b2lds4(ri, (uint32_t)((lane >> 3) * GBK + wave_u * 8 + (lane & 7)) * 4u, lds_idx + (c & (kIdxRing - 1)) * 256);
   };
-  // checkpoint row of row i (0..7) of this wave's share of k-slice kt
-  auto ckpt_row = [&](int kt, int i) -> uint32_t {
-    if (GATHER) {
-      const int s = s_idx[wave_u & 3][(kt / kIdxChunk) & (kIdxRing - 1)][(kt & (kIdxChunk - 1)) * 8 + i];
-      const uint32_t t = __umulhi((uint32_t)max(s, 0) * 2u, p.div_mul) >> p.div_shift;
-      return min(t, (uint32_t)(p.a_rows - 1));
-    }
-    return (uint32_t)min(lo + kt * GBK + wave_u * 8 + i, p.a_rows - 1);
+  // slot (or row) of row i (0..7) of this wave's share of k-slice kt, and its checkpoint row
+  auto slot_of = [&](int kt, int i) -> int {
+    if (GATHER) return s_idx[wave_u & 3][(kt / kIdxChunk) & (kIdxRing - 1)][(kt & (kIdxChunk - 1)) * 8 + i];
+    return lo + kt * GBK + wave_u * 8 + i;
+  };
+  auto ckpt_row = [&](int s) -> uint32_t {
+    uint32_t t = (uint32_t)max(s, 0);
+    if (GATHER) t = __umulhi(t * 2u, p.div_mul) >> p.div_shift;
+    return min(t, (uint32_t)(p.a_rows - 1));
+  };
+  // the next k-slice's rows (code copy, step copy), first as slots, then as byte offsets
+  uint32_t a_adr[2];
+  auto slots_a = [&](int kt) {
+    wave_lds_fence();
+    a_adr[0] = (uint32_t)slot_of(kt, lane >> 3);
+    a_adr[1] = (uint32_t)slot_of(kt, (lane >> 2) & 7);
+  };
+  auto addr_a = [&]() {
+    a_adr[0] = ckpt_row((int)a_adr[0]) * (uint32_t)p.P + a_col;
+    a_adr[1] = ckpt_row((int)a_adr[1]) * (uint32_t)(p.P >> 5) + s_col;
+  };
+  auto copy_a = [&](int kt) {
+    const uint32_t st = (uint32_t)(kt & (NST - 1));
+    g2lds16(p.A, a_adr[0], lds_raw + st * kRawStage);
+    if (lane < 32) g2lds1(p.S, a_adr[1], lds_step + st * kStepStage);
   };
   auto issue_a = [&](int kt) {
-    const uint32_t st = (uint32_t)(kt & (NST - 1));
-    wave_lds_fence();
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      g2lds16(p.A, ckpt_row(kt, 4 * j + (lane >> 4)) * (uint32_t)p.P + a_col, lds_raw + st * kRawStage + j * 1024);
-    g2lds1(p.S, ckpt_row(kt, lane >> 3) * (uint32_t)(p.P >> 5) + s_col, lds_step + st * kStepStage);
+    slots_a(kt);
+    addr_a();
+    copy_a(kt);
   };
-  auto issue_d = [&](int kt) {
+  auto issue_d = [&](int kt, int st) {  // st = kt % 3
     const int r0 = lo + kt * GBK, rows = min(GBK, n - kt * GBK);
     const i32x4_t rd = buffer_rsrc(p.D + (int64_t)r0 * p.Q, (uint32_t)(rows * p.Q * 2));
-    const uint32_t st = (uint32_t)(kt & (NST - 1)) * kOpStage;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b2lds16(rd, d_off[j & 1] + (uint32_t)((j >> 1) * 8 * p.Q), lds_d + st + j * 1024);
+    for (int j = 0; j < 8; ++j)
+      b2lds16(rd, d_off[j & 3] + (uint32_t)((j >> 2) * 8 * p.Q), lds_d + st * kCkDStage + j * 1024);
   };
-  auto prologue = [&]() {
+  auto prologue = [&]() {  // codes of the first four k-slices, D of the first three
     if (!loader || nk == 0) return;
     if (GATHER) {
       issue_idx(0);
@@ -1216,47 +1228,49 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
     for (int s = 0; s < NST; ++s)
       if (s < nk) {
         issue_a(s);
-        issue_d(s);
+        if (s < kCkDRing) issue_d(s, s);
       }
   };
-  // codes of k-slice kt -> bf16 operand tile kt % 2: lane's 16 elements of row 4 wave + lane / 16
+  // codes of k-slice kt -> operand tile kt % 2: lane's 8 elements of row 4 wave + lane / 16
   const int crow = wave * 4 + (lane >> 4), cch = lane & 15;
-  auto convert = [&](int kt) {
-    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(s_raw + (kt & (NST - 1)) * kRawStage + crow * 256 + cch * 16);
-    const uint32_t c =
-        *reinterpret_cast<const uint32_t*>(s_step + (kt & (NST - 1)) * kStepStage + crow * 32 + (cch >> 1) * 4);
-    float step = ckpt_step(c);
-    step = crow < n - kt * GBK ? step : 0.0f;
-    const float bias = -128.0f * step;
-    uint8_t* tile = s_a + (kt & 1) * kOpStage;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4_t o;
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const uint32_t b = v[2 * h + d] ^ 0x80808080u;  // code + 128 in each byte
-        float f[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) f[m] = __builtin_fmaf((float)((b >> (8 * m)) & 0xffu), step, bias);
-        o[2 * d] = pack_bf16x2(f[0], f[1]);
-        o[2 * d + 1] = pack_bf16x2(f[2], f[3]);
-      }
-      *reinterpret_cast<u32x4_t*>(tile + off_n32(crow, 2 * cch + h)) = o;
-    }
+  u32x2_t cv;
+  uint32_t cs;
+  auto conv_read = [&](int kt) {
+    cv = *reinterpret_cast<const u32x2_t*>(s_raw + (kt & (NST - 1)) * kRawStage + crow * kCkP + cch * 8);
+    cs = *reinterpret_cast<const uint32_t*>(s_step + (kt & (NST - 1)) * kStepStage + crow * 16 + (cch >> 2) * 4);
   };
-  // wait until at most the copies issued after those that the barrier of iteration kt needs are in flight
-  auto wait_for = [&](int kt) {
-    if (kt < 2 ? nk > NST + kt : kt + 4 < nk) {
-      if (kt < 2) asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(14)" ::: "memory");
-    } else if (kt >= 2 && kt + 4 == nk) {
-      asm volatile("s_waitcnt vmcnt(11)" ::: "memory");
-    } else if (kt >= 2 && kt + 3 == nk) {
-      asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  auto conv_write = [&](int kt) {
+    const float held = ckpt_step(cs);
+    const float step = crow < n - kt * GBK ? held : 0.0f, bias = -128.0f * step;
+    u32x4_t o;
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const uint32_t b = cv[d] ^ 0x80808080u;  // code + 128 in each byte
+      float f[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) f[m] = __builtin_fmaf((float)((b >> (8 * m)) & 0xffu), step, bias);
+      o[2 * d] = pack_bf16x2(f[0], f[1]);
+      o[2 * d + 1] = pack_bf16x2(f[2], f[3]);
     }
+    *reinterpret_cast<u32x4_t*>(s_a + (kt & 1) * kCkTile + crow * 256 + ((cch ^ ((crow & 3) << 2)) << 4)) = o;
   };
+  // Fragment addresses (frag_tr's): chunk c of row k sits at c ^ ((k & 3) << 2), and the 32-column blocks of a
+  // wave differ in the chunk bits that this turns, so block i is the lane's address with i << 6 flipped in: one
+  // register serves all of an operand's fragments.
+  const int fkr = 8 * (lane >> 5) + ((lane & 15) >> 2), fnc = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const uint32_t fa = lds_addr(s_a) + fkr * 256 + (((fnc >> 3) ^ ((fkr & 3) << 2)) << 4) + (fnc & 7) * 2;
+  const uint32_t fd =
+      lds_addr(s_d) + fkr * 1024 + (((wave * 8 + (fnc >> 3)) ^ ((fkr & 3) << 2)) << 4) + (fnc & 7) * 2;
+  auto frag = [&](uint32_t base, int imm, int four_rows) -> bf16x8_t {
+    typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4;
+    typedef __attribute__((address_space(3))) uint8_t lds_u8;
+    lds_u8* const q = (lds_u8*)(uintptr_t)base;
+    const bf16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(q + imm));
+    const bf16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(q + imm + four_rows));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto frag_a = [&](uint32_t tile, int i, int ks) { return frag((fa + tile) ^ (uint32_t)(i << 6), ks * 4096, 1024); };
+  auto frag_d = [&](uint32_t st, int f, int ks) { return frag((fd + st) ^ (uint32_t)(f << 6), ks * 16384, 4096); };
 
   if (!decode(0)) return;
   prologue();
@@ -1270,14 +1284,6 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
         for (int r = 0; r < 16; ++r) acc[i][f][r] = 0.0f;
 
     bf16x8_t af[2][4], df[2][2];
-    auto read_frags = [&](int kt, int ks, int set) {
-      const uint8_t* As = s_a + (kt & 1) * kOpStage;
-      const uint8_t* Ds = s_d + (kt & (NST - 1)) * kOpStage;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) af[set][i] = frag_tr(As, lane, ks * 16, wm * 128 + i * 32);
-#pragma unroll
-      for (int f = 0; f < 2; ++f) df[set][f] = frag_tr(Ds, lane, ks * 16, wn * 64 + f * 32);
-    };
     auto mfmas = [&](int set) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -1296,112 +1302,149 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
     };
+    const bool busy = q0 + wave_u * 64 < p.Q;  // a wave without columns converts and copies only
 
     if (nk > 0) {
-      // k-slices 0 and 1 (copies of the two after them may be in flight): convert, publish
+      // codes of k-slices 0 and 1 and D of 0 have landed: convert, publish
       if (loader) {
-        if (nk >= NST) asm volatile("s_waitcnt vmcnt(14)" ::: "memory");
+        if (nk >= 4) asm volatile("s_waitcnt vmcnt(20)" ::: "memory");
+        else if (nk == 3) asm volatile("s_waitcnt vmcnt(18)" ::: "memory");
+        else if (nk == 2) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
         else wait_vm_all();
       }
       kbarrier();
-      convert(0);
-      if (nk > 1) convert(1);
+      conv_read(0);
+      conv_write(0);
+      if (nk > 1) {
+        conv_read(1);
+        conv_write(1);
+      }
       kbarrier();
       if (loader && nk > NST) issue_a(NST);
-      read_frags(0, 0, 0);
+      if (loader && nk > NST + 1) {
+        slots_a(NST + 1);
+        addr_a();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) af[0][i] = frag_a(0, i, 0);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) df[0][f] = frag_d(0, f, 0);
     }
-    for (int kt = 0; kt < nk; ++kt) {
-      read_frags(kt, 1, 1);
-      mfmas(0);
-      interleave();
-      if (loader) wait_for(kt);
+    // One k-slice, D stage st = kt % 3. Schedule as in wgrad_kernel: the barrier sits before the second 16 rows;
+    // past it operand tile kt % 2 and D stage st are free. FULL: kt + 5 < nk, nothing to check.
+    int st = 0;
+    auto body = [&](auto FULLc, auto BUSYc, int kt) {
+      constexpr bool FULL = decltype(FULLc)::value, BUSY = decltype(BUSYc)::value;
+      const int st1 = st == 2 ? 0 : st + 1;
+      const uint32_t ta = (uint32_t)(kt & 1) * kCkTile, td = (uint32_t)st * kCkDStage;
+      if (BUSY) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) af[1][i] = frag_a(ta, i, 1);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) df[1][f] = frag_d(td, f, 1);
+        mfmas(0);
+        interleave();
+      }
+      if (loader) {
+        if (FULL || kt + 4 < nk) asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
+        else if (kt + 2 < nk) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+        else wait_vm_all();
+      }
       kbarrier();
+      const bool cv_on = FULL || kt + 2 < nk;
+      if (cv_on) conv_read(kt + 2);
       if (GATHER && loader && (kt & (kIdxChunk - 1)) == 0 && (kt / kIdxChunk + 2) * kIdxChunk < nk)
         issue_idx(kt / kIdxChunk + 2);
-      if (loader && kt + 5 < nk) issue_a(kt + 5);
-      if (kt + 2 < nk) convert(kt + 2);
-      {
-        const uint8_t* As = s_a + ((kt + 1) & 1) * kOpStage;
-        const uint8_t* Ds = s_d + ((kt + 1) & (NST - 1)) * kOpStage;
+      if (loader && (FULL || kt + 5 < nk)) copy_a(kt + 5);
+      const uint32_t ta1 = ta ^ kCkTile, td1 = (uint32_t)st1 * kCkDStage;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {
+        if (BUSY) {
 #pragma unroll
           for (int f = 0; f < 2; ++f) acc[i][f] = mfma(df[1][f], af[1][i], acc[i][f]);
-          af[0][i] = frag_tr(As, lane, 0, wm * 128 + i * 32);
-          if (i & 1) df[0][i >> 1] = frag_tr(Ds, lane, 0, wn * 64 + (i >> 1) * 32);
+          af[0][i] = frag_a(ta1, i, 0);
+          if (i & 1) df[0][i >> 1] = frag_d(td1, i >> 1, 0);
         }
+        if (i == 1 && cv_on) conv_write(kt + 2);
+        // the rows of the next iteration's code copies: slots here, offsets two MFMAs later
+        if (i == 2 && loader && kt + 6 < nk) slots_a(kt + 6);
       }
-      if (loader && kt + NST < nk) issue_d(kt + NST);
+      if (loader && (FULL || kt + kCkDRing < nk)) issue_d(kt + kCkDRing, st);
+      if (loader && kt + 6 < nk) addr_a();
+      st = st1;
+    };
+    using Yes = std::integral_constant<bool, true>;
+    using No = std::integral_constant<bool, false>;
+    int kt = 0;
+    if (busy) {
+      for (; kt + 5 < nk; ++kt) body(Yes{}, Yes{}, kt);
+      for (; kt < nk; ++kt) body(No{}, Yes{}, kt);
+    } else {
+      for (; kt < nk; ++kt) body(No{}, No{}, kt);
     }
 
     const int ce = e, cp0 = p0, cq0 = q0;
     const bool more = decode(it + 1);
-    // every ring is free past the last barrier; the operand tiles carry the copying waves' output
+    // the rings are free past the last barrier; operand tile 0 and 1 carry the copying waves' output, 32 rows of
+    // 128 bytes (4 KB) of each at a time
     if (more) prologue();
     const int hh = lane >> 5, r = lane & 31;
     uint8_t* const stg = s_stage[wave];
     auto stg128 = [&](int rr, int c) { return rr * 128 + ((c ^ ((rr >> 1) & 7)) << 4); };
     uint16_t* const Ce = p.C + (int64_t)ce * p.P * p.Q;
     const int src = wave_u & 3;
-    uint8_t* const xr = s_a + src * 8192;
-    const int wm_s = src & 1, wn_s = src >> 1;
+    uint8_t* const xr = s_a + src * 4096;
 #pragma unroll
-    for (int ph = 0; ph < 2; ++ph) {
+    for (int i = 0; i < 4; ++i) {
       if (loader) {
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii) {
-          const int i = 2 * ph + ii, rr = ii * 32 + r;
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<u32x2_t*>(xr + stg128(rr, f * 4 + q) + hh * 8) =
-                  pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]);
-        }
-      } else if (ph == 0) {
-        const int qw = cq0 + wn * 64;
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<u32x2_t*>(xr + stg128(r, f * 4 + q) + hh * 8) =
+                pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]);
+      } else {
+        // the storing wave's own output: rows 0-15 in this wave's 2 KB, rows 16-31 in that of its copying wave
+        const int qw = cq0 + wave * 64;
         const int valid = min(8, (p.Q - qw) >> 3);
         uint8_t* const wb = r < 16 ? stg : s_stage[wave - 4];
+        const int pr0 = cp0 + i * 32;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int pr0 = cp0 + wm * 128 + i * 32;
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<u32x2_t*>(wb + stg128(r & 15, f * 4 + q) + hh * 8) =
+                pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]);
+        wave_lds_fence();
+        u32x4_t v[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<u32x2_t*>(wb + stg128(r & 15, f * 4 + q) + hh * 8) =
-                  pack4(acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]);
-          wave_lds_fence();
-          u32x4_t v[4];
+        for (int kk = 0; kk < 4; ++kk)
+          v[kk] = *reinterpret_cast<const u32x4_t*>((kk < 2 ? stg : s_stage[wave - 4]) +
+                                                    stg128(8 * (kk & 1) + (lane >> 3), lane & 7));
+        wave_lds_fence();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            v[kk] = *reinterpret_cast<const u32x4_t*>((kk < 2 ? stg : s_stage[wave - 4]) +
-                                                      stg128(8 * (kk & 1) + (lane >> 3), lane & 7));
-          wave_lds_fence();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int pr = pr0 + 8 * kk + (lane >> 3), c = lane & 7;
-            if (pr < p.P && c < valid)
-              __builtin_nontemporal_store(v[kk], reinterpret_cast<u32x4_t*>(Ce + (int64_t)pr * p.Q + qw + c * 8));
-          }
+        for (int kk = 0; kk < 4; ++kk) {
+          const int pr = pr0 + 8 * kk + (lane >> 3), c = lane & 7;
+          if (pr < p.P && c < valid)
+            __builtin_nontemporal_store(v[kk], reinterpret_cast<u32x4_t*>(Ce + (int64_t)pr * p.Q + qw + c * 8));
         }
       }
-      kbarrier();
+      kbarrier();  // the copying waves' rows are in LDS
       if (!loader) {
-        const int pr0 = cp0 + wm_s * 128 + ph * 64;
-        const int qw = cq0 + wn_s * 64;
+        const int pr0 = cp0 + i * 32;
+        const int qw = cq0 + src * 64;
         const int valid = min(8, (p.Q - qw) >> 3);
-        u32x4_t v[8];
+        u32x4_t v[4];  // reads first, then the masked stores
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const u32x4_t*>(xr + stg128(8 * j + (lane >> 3), lane & 7));
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const u32x4_t*>(xr + stg128(8 * j + (lane >> 3), lane & 7));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const int pr = pr0 + 8 * j + (lane >> 3), c = lane & 7;
           if (pr < p.P && c < valid)
             __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4_t*>(Ce + (int64_t)pr * p.Q + qw + c * 8));
         }
       }
-      kbarrier();
+      kbarrier();  // read back: the region may be written again
     }
     if (!more) break;
   }
