@@ -414,11 +414,17 @@ int moe_swiglu_bwd_ckpt(int64_t M, int32_t mlp, const moe_bf16_t* da, const int8
  *  fp32 accumulate; the values of X enter the products unrounded. An empty
  *  group gives exact zeros. P % 32 == 0, Q % 8 == 0, a_rows * P < 2^31,
  *  M < 2^31.
+ *  ws: scratch of moe_wgrad_ckpt_workspace_bytes(E, M, P, Q) bytes, or less, or
+ *  NULL. With it an expert that holds more rows than a workgroup's mean load is
+ *  cut along its rows and the pieces' sums are added in row order; with less,
+ *  fewer are cut, and without, none, which changes no more than the order of
+ *  the fp32 additions.
  */
+size_t moe_wgrad_ckpt_workspace_bytes(int32_t E, int64_t M, int32_t P, int32_t Q);
 int moe_grouped_gemm_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows,
                                 const int32_t* row_slot, int32_t slot_div, const moe_bf16_t* D,
                                 const int32_t* group_offsets, int32_t E, int64_t M, int32_t P, int32_t Q,
-                                moe_bf16_t* C, moe_stream_t stream);
+                                moe_bf16_t* C, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * MXFP8 ("[DRAFT][JAX] Optimize MoE block", Changes: MXFP8 quantization in

@@ -582,9 +582,10 @@ def swiglu_bwd_ckpt(da: torch.Tensor, h_codes: torch.Tensor, h_scales: torch.Ten
 
 def grouped_gemm_wgrad_ckpt(a_codes: torch.Tensor, a_scales: torch.Tensor, D: torch.Tensor,
                             group_offsets: torch.Tensor, E: int, row_slot: torch.Tensor | None = None,
-                            slot_div: int = 1) -> torch.Tensor:
+                            slot_div: int = 1, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """C [E, P, Q] = per-group X^T D with X an 8-bit checkpoint [R, P] (see moe_grouped_gemm_wgrad_ckpt); with
-    row_slot [M] int32, row r of the product reads X row row_slot[r] // slot_div."""
+    row_slot [M] int32, row r of the product reads X row row_slot[r] // slot_div. workspace: uint8, by default a new
+    one of moe_wgrad_ckpt_workspace_bytes; a smaller one only cuts fewer long groups."""
     _need_ckpt(a_codes, a_scales, "a_", None)
     dev = a_codes.device
     _need_rank2(D, "D", torch.bfloat16, dev)
@@ -594,9 +595,10 @@ def grouped_gemm_wgrad_ckpt(a_codes: torch.Tensor, a_scales: torch.Tensor, D: to
     if group_offsets is None:
         raise ValueError("group_offsets is missing")
     _need_like(group_offsets, "group_offsets", (E + 1,), torch.int32, dev)
+    ws = _workspace(workspace, int(_lib.lib().moe_wgrad_ckpt_workspace_bytes(E, M, P, Q)), dev)
     C_ = torch.empty((max(E, 0), P, Q), dtype=torch.bfloat16, device=dev)
     _call("moe_grouped_gemm_wgrad_ckpt", dev, a_codes, a_scales, R, row_slot, slot_div, D, group_offsets, E, M, P, Q,
-          C_)
+          C_, ws, ws.numel())
     return C_
 
 

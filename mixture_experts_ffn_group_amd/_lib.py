@@ -86,7 +86,9 @@ SIGNATURES = {
     "moe_ckpt_quantize": ([_p, _i32, _i64, _i32, _p, _p, _p], C.c_int),
     "moe_ckpt_dequantize": ([_p, _p, _i64, _i32, _p, _i32, _i64, _p, _i32, _p], C.c_int),
     "moe_swiglu_bwd_ckpt": ([_i64, _i32, _p, _p, _p, _p, _p, _p, _p, _p, _p], C.c_int),
-    "moe_grouped_gemm_wgrad_ckpt": ([_p, _p, _i64, _p, _i32, _p, _p, _i32, _i64, _i32, _i32, _p, _p], C.c_int),
+    "moe_wgrad_ckpt_workspace_bytes": ([_i32, _i64, _i32, _i32], _sz),
+    "moe_grouped_gemm_wgrad_ckpt": ([_p, _p, _i64, _p, _i32, _p, _p, _i32, _i64, _i32, _i32, _p, _p, _sz, _p],
+                                    C.c_int),
     "moe_workspace_bytes_routed": ([_SHP, C.c_int], _sz),
     "moe_ffn_fwd_routed": ([_SHP, _p, _p, _p, _p, _p, _p, C.POINTER(MoeSaved), C.POINTER(MoeSaved8), _p, _sz, _p],
                            C.c_int),

@@ -43,6 +43,7 @@
 //    waves' output reaches the storing waves through the last ring stage.
 //  - A wave whose 128 rows lie past the group end skips its MFMAs, and one
 //    with at most 64 output rows multiplies only its first two 32-row blocks.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -1103,6 +1104,13 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_kernel(WgradP p) {
 // An iteration kt of the k-loop issues codes and steps of k-slice kt + 5 and D
 // of kt + 3, and its barrier needs codes and steps kt + 2 and D kt + 1: one
 // iteration's copies (10 a copying wave) may still be in flight.
+//
+// Work list, made for skewed loads, which routers have in practice: the tiles are dealt longest first, in turns
+// of one a workgroup, every second turn backwards, an expert's tiles (which share its rows) to one XCD. Where the
+// caller gives a workspace, an expert longer than half the mean load of a workgroup is cut along its rows into
+// pieces of at most that; they leave fp32 partial tiles in the workspace, which a second kernel adds in
+// row order. Dealt by expert, as wgrad_kernel does, a hot expert holds one XCD, and each of its tiles one
+// workgroup, for its whole length.
 struct WgradCkptP {
   const int8_t* A;
   const uint8_t* S;  // step codes [a_rows, P / 32]
@@ -1112,6 +1120,17 @@ struct WgradCkptP {
   uint16_t* C;
   int E, M, P, Q, a_rows;
   uint32_t div_mul, div_shift;  // slot / slot_div = mulhi(2 slot, div_mul) >> div_shift
+  struct WgradCkptCuts* cuts;   // workspace, or NULL: the cut experts, then the partial tiles
+  float* part;                  // partial tiles [cap][8 waves][32][64 lanes][4]
+  int cap, grid;                // their number; workgroups the work is dealt to
+};
+
+// The cut experts of a launch, for the kernel that joins their pieces.
+struct WgradCkptCuts {
+  int sum[4];  // how many with expert % 4 == u
+  struct {
+    int e, count, part, pad;  // pieces, first partial tile
+  } cut[kMaxExperts];          // cut[64 u ..]
 };
 
 constexpr int kCkP = 128, kCkQ = 512;         // output tile
@@ -1132,6 +1151,135 @@ __device__ __forceinline__ void g2lds1(const void* sbase, uint32_t voff, uint32_
   asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_ubyte %0, %1" : : "v"(voff), "s"(sbase), "s"(lds) : "memory");
 }
 
+constexpr size_t kCkCutBytes = 8192;   // holds a WgradCkptCuts
+static_assert(sizeof(WgradCkptCuts) <= kCkCutBytes, "the list fits its place");
+constexpr int kCkPart = kCkP * kCkQ;  // floats of a partial tile
+constexpr int kCkMinCut = 32;         // k-slices below which an expert is not cut
+constexpr int kCkNoCut = 0x3fffffff;
+constexpr int kCkMinRows = 2048;      // rows in all below which none is
+
+// An expert of ns k-slices in pieces of at most cut: their number and length (none is empty; an expert without
+// rows is one piece of none).
+__device__ __forceinline__ void ckpt_pieces(int ns, int cut, int* count, int* len) {
+  *count = 1;
+  *len = ns;
+  if (ns <= cut) return;
+  const uint32_t n = (uint32_t)ns, c = (n + cut - 1) / (uint32_t)cut, l = (n + c - 1) / c;
+  *len = (int)l;
+  *count = (int)((n + l - 1) / l);
+}
+
+// The work list of a launch, from the group offsets: each expert's pieces, and the experts by falling length of
+// a piece.
+struct WgradCkptPlan {
+  int off[kMaxExperts + 1];   // group offsets, clamped to [0, M]
+  int order[kMaxExperts];     // experts in list order
+  int unit[kMaxExperts + 1];  // first unit of the i-th of them; a unit is a piece, all its tiles
+  int part[kMaxExperts];      // first partial tile of a cut expert
+  __attribute__((aligned(16))) uint32_t key[kMaxExperts];
+  int cut;                    // k-slices of the longest piece
+};
+// Exclusive sums over the experts 4 lane + u, and their total.
+__device__ __forceinline__ int plan_scan(const int (&v)[4], int (&before)[4]) {
+  const int lane = threadIdx.x & 63;
+  int incl = v[0] + v[1] + v[2] + v[3];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  before[0] = incl - (v[0] + v[1] + v[2] + v[3]);
+#pragma unroll
+  for (int u = 1; u < 4; ++u) before[u] = before[u - 1] + v[u - 1];
+  return __builtin_amdgcn_readlane(incl, 63);
+}
+__device__ __forceinline__ void ckpt_plan(const WgradCkptP& p, int tt, WgradCkptPlan& pl) {
+  const int tid = threadIdx.x;
+  for (int i = tid; i <= p.E; i += GTHR) pl.off[i] = clamp_rows(p.off[i], p.M);
+  if (p.cap == 0 && p.E * tt <= p.grid) {  // one turn of uncut tiles: any order does
+    for (int i = tid; i <= p.E; i += GTHR) pl.unit[i] = i;
+    if (tid < p.E) pl.order[tid] = tid;
+    if (tid == 0) pl.cut = kCkNoCut;
+    __syncthreads();
+    return;
+  }
+  __syncthreads();
+  const int lane = tid & 63;
+  if (tid < 64) {
+    int ns[4], count[4], len[4], v[4], parts[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = 4 * lane + u;
+      ns[u] = e < p.E ? (max(0, pl.off[e + 1] - pl.off[e]) + GBK - 1) / GBK : 0;
+    }
+    const float mean = (float)plan_scan(ns, parts) * (float)tt / (float)p.grid;  // load of a workgroup
+    int cut = p.cap > 0 && mean < 1e9f ? max(kCkMinCut, (int)(0.5f * mean)) : kCkNoCut;
+    for (;;) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        ckpt_pieces(ns[u], cut, &count[u], &len[u]);
+        v[u] = count[u] > 1 ? (int)min((int64_t)count[u] * tt, (int64_t)(1 << 22)) : 0;  // sums stay in an int
+      }
+      if (plan_scan(v, parts) <= p.cap || cut == kCkNoCut) break;
+      cut = cut < (1 << 28) ? 2 * cut : kCkNoCut;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = 4 * lane + u;
+      if (p.cuts && blockIdx.x == 0) {  // one workgroup leaves the list for the joining kernel
+        const bool is = e < p.E && count[u] > 1;
+        const uint64_t cuts = __ballot(is);
+        if (is) {
+          auto& c = p.cuts->cut[64 * u + __popcll(cuts & ((1ull << lane) - 1))];
+          c.e = e;
+          c.count = count[u];
+          c.part = parts[u];
+        }
+        if (lane == 0) p.cuts->sum[u] = __popcll(cuts);
+      }
+      if (e < p.E) {
+        pl.part[e] = parts[u];
+        // count and length are recomputed where they are needed; the key orders by length, then expert
+        pl.key[e] = ((uint32_t)min(len[u], (1 << 24) - 1) << 8) | (uint32_t)(255 - e);
+      } else if (e < kMaxExperts) {
+        pl.key[e] = 0;
+      }
+    }
+    if (lane == 0) pl.cut = cut;
+  }
+  __syncthreads();
+  if (tid < p.E) {
+    const uint32_t mine = pl.key[tid];
+    int rank = 0;
+    for (int i = 0; i < (p.E + 3) / 4; ++i) {
+      const u32x4_t o = *reinterpret_cast<const u32x4_t*>(&pl.key[4 * i]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) rank += o[u] > mine;
+    }
+    pl.order[rank] = tid;
+  }
+  __syncthreads();
+  if (tid < 64) {
+    int v[4], first[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[u] = 0;
+      if (4 * lane + u < p.E) {
+        const int e = pl.order[4 * lane + u];
+        int count, len;
+        ckpt_pieces((max(0, pl.off[e + 1] - pl.off[e]) + GBK - 1) / GBK, pl.cut, &count, &len);
+        v[u] = count;
+      }
+    }
+    const int units = plan_scan(v, first);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (4 * lane + u < p.E) pl.unit[4 * lane + u] = first[u];
+    if (lane == 0) pl.unit[p.E] = units;
+  }
+  __syncthreads();
+}
+
 template <bool GATHER>
 __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
   __shared__ __attribute__((aligned(1024))) uint8_t s_a[2 * kCkTile];  // bf16 operand tiles
@@ -1140,10 +1288,9 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
   __shared__ __attribute__((aligned(16))) uint8_t s_step[NST * kStepStage];
   __shared__ __attribute__((aligned(16))) int s_idx[4][kIdxRing][64];
   __shared__ __attribute__((aligned(16))) uint8_t s_stage[GTHR / 64][2048];
-  __shared__ int s_off[kMaxExperts + 1];
-  for (int i = threadIdx.x; i <= p.E; i += GTHR) s_off[i] = clamp_rows(p.off[i], p.M);
-  __syncthreads();
+  __shared__ WgradCkptPlan s_plan;
   const int tp = (p.P + kCkP - 1) / kCkP, tq = (p.Q + kCkQ - 1) / kCkQ;
+  ckpt_plan(p, tp * tq, s_plan);
   const int tid = opaque((int)threadIdx.x), lane = tid & 63, wave = tid >> 6;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);  // its 64 columns of the tile
   const bool loader = wave_u < 4;
@@ -1152,17 +1299,35 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
   const uint32_t lds_idx = lds_addr(s_idx) + (wave_u & 3) * (kIdxRing * 256);
   auto kbarrier = []() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
-  int e = 0, p0 = 0, q0 = 0, lo = 0, n = 0, nk = 0;
+  int e = 0, p0 = 0, q0 = 0, lo = 0, n = 0, nk = 0, part = -1;
   uint32_t a_col = 0, s_col = 0, d_off[4];
+  // Turn `it` of this workgroup: the items (units' tiles) are dealt in turns of one a workgroup, every second turn
+  // backwards, an XCD's workgroups taking neighbouring items. (Whole units dealt to XCDs were 1.5 % faster with
+  // 128 equal experts and 18 % slower with Zipf(1.1) ones.)
   auto decode = [&](int64_t it) -> bool {
-    WgradTile wt;
-    if (!wgrad_tile(it, blockIdx.x, gridDim.x, p.E, tp, tq, &wt)) return false;
-    e = __builtin_amdgcn_readfirstlane(wt.e);
-    p0 = __builtin_amdgcn_readfirstlane(wt.pt * kCkP);
-    q0 = __builtin_amdgcn_readfirstlane(wt.qt * kCkQ);
-    const int l0 = s_off[e], h0 = s_off[e + 1];
-    lo = __builtin_amdgcn_readfirstlane(l0);
-    n = __builtin_amdgcn_readfirstlane(h0 > l0 ? h0 - l0 : 0);
+    const int tt = tp * tq, units = s_plan.unit[p.E];
+    const int g = gridDim.x, at = (int)xcd_tile(0, blockIdx.x, g);
+    const int64_t j = it * g + ((it & 1) ? g - 1 - at : at);
+    if (j >= (int64_t)units * tt) return false;
+    const uint32_t u = (uint32_t)j / (uint32_t)tt, tl = (uint32_t)j - u * (uint32_t)tt;  // items fit an int
+    int a = 0, b = p.E;
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (s_plan.unit[mid] <= (int)u) a = mid;
+      else b = mid;
+    }
+    e = __builtin_amdgcn_readfirstlane(s_plan.order[a]);
+    const int piece = __builtin_amdgcn_readfirstlane((int)u - s_plan.unit[a]);
+    const int tile = __builtin_amdgcn_readfirstlane((int)tl);
+    const int l0 = s_plan.off[e], rows = max(0, s_plan.off[e + 1] - l0);
+    int count, len;
+    ckpt_pieces((rows + GBK - 1) / GBK, s_plan.cut, &count, &len);
+    // the dimension with fewer tiles varies fastest, so its panels stay in L2
+    p0 = __builtin_amdgcn_readfirstlane((tq <= tp ? tile / tq : tile % tp) * kCkP);
+    q0 = __builtin_amdgcn_readfirstlane((tq <= tp ? tile % tq : tile / tp) * kCkQ);
+    lo = __builtin_amdgcn_readfirstlane(l0 + piece * len * GBK);
+    n = __builtin_amdgcn_readfirstlane(min(rows - piece * len * GBK, len * GBK));
+    part = __builtin_amdgcn_readfirstlane(count > 1 ? s_plan.part[e] + piece * tt + tile : -1);
     nk = (n + GBK - 1) / GBK;
     if (!loader) return true;
     // codes: rows 8 wave + lane / 8, 16 columns a lane; steps: rows 8 wave + lane / 4, lanes 0-31. Columns past P
@@ -1383,11 +1548,25 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
       for (; kt < nk; ++kt) body(No{}, No{}, kt);
     }
 
-    const int ce = e, cp0 = p0, cq0 = q0;
+    const int ce = e, cp0 = p0, cq0 = q0, cpart = part;
     const bool more = decode(it + 1);
     // the rings are free past the last barrier; operand tile 0 and 1 carry the copying waves' output, 32 rows of
     // 128 bytes (4 KB) of each at a time
     if (more) prologue();
+    if (cpart >= 0) {  // a piece: the accumulators as they lie, 1 KB a store
+      f32x4_t* const out = reinterpret_cast<f32x4_t*>(p.part + (int64_t)cpart * kCkPart) + wave * 2048 + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            out[((i * 2 + f) * 4 + q) * 64] = f32x4_t{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2],
+                                                       acc[i][f][4 * q + 3]};
+      kbarrier();  // as the output's barriers below: the operand tiles may be written again
+      if (!more) break;
+      continue;
+    }
     const int hh = lane >> 5, r = lane & 31;
     uint8_t* const stg = s_stage[wave];
     auto stg128 = [&](int rr, int c) { return rr * 128 + ((c ^ ((rr >> 1) & 7)) << 4); };
@@ -1450,6 +1629,51 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
   }
 }
 
+// Output tiles of the cut experts: their pieces' partial tiles added in row order, rounded once.
+__global__ __launch_bounds__(GTHR) void wgrad_ckpt_join_kernel(WgradCkptP p) {
+  const int tp = (p.P + kCkP - 1) / kCkP, tq = (p.Q + kCkQ - 1) / kCkQ, tt = tp * tq;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int seen = 0;  // units of the cut experts before this one, modulo the grid: unit u of all is workgroup u's
+  for (int k = 0; k < kMaxExperts; ++k) {
+    if ((k & 63) >= p.cuts->sum[k >> 6]) {
+      k |= 63;
+      continue;
+    }
+    const int e = p.cuts->cut[k].e, count = p.cuts->cut[k].count, part = p.cuts->cut[k].part;
+    // a unit is an eighth of a tile: four of the 32 stores of a wave (index k = (i * 2 + f) * 4 + q)
+    int unit = (int)blockIdx.x - seen;
+    if (unit < 0) unit += gridDim.x;
+    seen = (seen + 8 * tt) % (int)gridDim.x;
+    for (; unit < 8 * tt; unit += gridDim.x) {
+      const int tile = unit >> 3, k0 = (unit & 7) * 4;
+      const int p0 = (tq <= tp ? tile / tq : tile % tp) * kCkP, q0 = (tq <= tp ? tile % tq : tile / tp) * kCkQ;
+      const f32x4_t* in = reinterpret_cast<const f32x4_t*>(p.part + (int64_t)(part + tile) * kCkPart) +
+                          wave * 2048 + k0 * 64 + lane;
+      const int64_t piece = (int64_t)tt * (kCkPart / 4);
+      f32x4_t v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = in[x * 64];
+#pragma unroll 2
+      for (int c = 1; c < count; ++c) {
+        f32x4_t w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w[x] = in[c * piece + x * 64];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) v[x][u] += w[x][u];
+      }
+      uint16_t* const Ce = p.C + (int64_t)e * p.P * p.Q;
+      const int pr = p0 + (k0 >> 3) * 32 + (lane & 31);
+      const int qc = q0 + wave * 64 + ((k0 >> 2) & 1) * 32 + (lane >> 5) * 4;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (pr < p.P && qc + 8 * x < p.Q)
+          *reinterpret_cast<u32x2_t*>(Ce + (int64_t)pr * p.Q + qc + 8 * x) = pack4(v[x][0], v[x][1], v[x][2], v[x][3]);
+    }
+  }
+}
+
 }  // namespace
 
 int persistent_grid() {
@@ -1499,18 +1723,34 @@ hipError_t launch_wgrad(const uint16_t* A, const uint16_t* D, const int32_t* gro
   return hipGetLastError();
 }
 
+size_t wgrad_ckpt_workspace(int E, int64_t M, int P, int Q) {
+  // An expert is cut into pieces of at least the mean load of a workgroup, and at least kCkMinCut k-slices, so
+  // there are at most twice the workgroups, or 2 / kCkMinCut of all k-slices, of them.
+  const int64_t tt = (int64_t)((P + kCkP - 1) / kCkP) * ((Q + kCkQ - 1) / kCkQ);
+  const int64_t slices = (M / GBK + E) * tt;
+  if (M < kCkMinRows) return 0;
+  const int64_t n = std::min<int64_t>(2 * persistent_grid(), 2 * slices / kCkMinCut + 2 * tt);
+  return kCkCutBytes + (size_t)n * kCkPart * sizeof(float);
+}
+
 hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows, const int32_t* row_slot,
                              int slot_div, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
-                             int Q, uint16_t* C, hipStream_t stream) {
+                             int Q, uint16_t* C, void* ws, size_t ws_bytes, hipStream_t stream) {
   // slot / slot_div for 31-bit slots: with L = ceil(log2(d)) and m = floor(2^(31+L) / d) + 1 (below 2^32),
   // m d exceeds 2^(31+L) by at most d <= 2^L, so floor(n m / 2^(31+L)) = floor(n / d)
   uint32_t L = 0;
   while ((uint64_t(1) << L) < (uint64_t)slot_div) ++L;
   const uint32_t mul = (uint32_t)((uint64_t(1) << (31 + L)) / (uint64_t)slot_div + 1);
-  const WgradCkptP p{A_codes, A_scales, row_slot, D, group_offsets, C, E, (int)M, P, Q, (int)a_rows, mul, L};
   const dim3 grid(persistent_grid()), block(GTHR);
+  // with few rows the longest expert is short: not cut, and the second launch (5 us) is saved
+  const bool fits = ws && M >= kCkMinRows && ws_bytes >= kCkCutBytes + kCkPart * sizeof(float);
+  const int64_t cap = fits ? std::min<int64_t>((ws_bytes - kCkCutBytes) / (kCkPart * sizeof(float)), 1 << 20) : 0;
+  const WgradCkptP p{A_codes, A_scales, row_slot, D, group_offsets, C,   E,   (int)M,
+                     P,       Q,        (int)a_rows, mul, L, cap > 0 ? static_cast<WgradCkptCuts*>(ws) : nullptr,
+                     reinterpret_cast<float*>(static_cast<char*>(ws) + kCkCutBytes), (int)cap, (int)grid.x};
   if (row_slot) wgrad_ckpt_kernel<true><<<grid, block, 0, stream>>>(p);
   else wgrad_ckpt_kernel<false><<<grid, block, 0, stream>>>(p);
+  if (cap > 0) wgrad_ckpt_join_kernel<<<grid, block, 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -87,8 +87,9 @@ hipError_t launch_ckpt_dequantize(const int8_t* codes, const uint8_t* scales, in
 hipError_t launch_swiglu_bwd_ckpt(int64_t M, int mlp, const uint16_t* da, const int8_t* h_codes,
                                   const uint8_t* h_scales, const int32_t* row_slot, const float* slot_scale,
                                   uint16_t* dh, uint16_t* a, float* dslot_scale, hipStream_t stream);
+size_t wgrad_ckpt_workspace(int E, int64_t M, int P, int Q);
 hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows, const int32_t* row_slot,
                              int slot_div, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
-                             int Q, uint16_t* C, hipStream_t stream);
+                             int Q, uint16_t* C, void* ws, size_t ws_bytes, hipStream_t stream);
 
 }  // namespace moe

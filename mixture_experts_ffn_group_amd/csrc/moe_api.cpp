@@ -599,10 +599,15 @@ int moe_swiglu_bwd_ckpt(int64_t M, int32_t mlp, const moe_bf16_t* da, const int8
                     "moe_swiglu_bwd_ckpt");
 }
 
+size_t moe_wgrad_ckpt_workspace_bytes(int32_t E, int64_t M, int32_t P, int32_t Q) {
+  if (check_wgrad_ckpt(1, true, 1, E, M, P, Q) != MOE_OK) return 0;
+  return moe::wgrad_ckpt_workspace(E, M, P, Q);
+}
+
 int moe_grouped_gemm_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows,
                                 const int32_t* row_slot, int32_t slot_div, const moe_bf16_t* D,
                                 const int32_t* group_offsets, int32_t E, int64_t M, int32_t P, int32_t Q,
-                                moe_bf16_t* C, moe_stream_t stream) {
+                                moe_bf16_t* C, void* ws, size_t ws_bytes, moe_stream_t stream) {
   g_detail[0] = 0;
   if (int rc = check_wgrad_ckpt(a_rows, row_slot != nullptr, slot_div, E, M, P, Q)) return rc;
   NEED(group_offsets);
@@ -613,8 +618,9 @@ int moe_grouped_gemm_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, 
     MAYBE(row_slot);
     NEED(D);
   }
+  MAYBE(ws);
   return hip_status(moe::launch_wgrad_ckpt(A_codes, A_scales, a_rows, row_slot, row_slot ? slot_div : 1, D,
-                                           group_offsets, E, M, P, Q, C, (hipStream_t)stream),
+                                           group_offsets, E, M, P, Q, C, ws, ws_bytes, (hipStream_t)stream),
                     "moe_grouped_gemm_wgrad_ckpt");
 }
 
@@ -1069,7 +1075,8 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* s, const moe_bf16_t* dy, const float* to
   }
   if (dwi) {
     if (int rc = hip_status(moe::launch_wgrad_ckpt(saved8->x_codes, saved8->x_scales, T, saved8->sorted_slot, k, dh,
-                                                   saved8->group_offsets, E, S, emb, 2 * mlp, dwi, st),
+                                                   saved8->group_offsets, E, S, emb, 2 * mlp, dwi, du,
+                                                   2 * round_up(S * mlp * 2), st),  // du and a: done with by now
                             "dwi"))
       return rc;
   }

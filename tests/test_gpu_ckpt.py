@@ -215,9 +215,9 @@ def _wgrad_case(T, k, E, P, Q, seed, sizes=None):
     return codes, scales, slot, off, D
 
 
-def _check_wgrad(codes, scales, slot, off, D, k, E):
+def _check_wgrad(codes, scales, slot, off, D, k, E, workspace=None):
     out = moe.grouped_gemm_wgrad_ckpt(_np_dev(codes), _np_dev(scales), D.to(DEV), _np_dev(off), E,
-                                      row_slot=_np_dev(slot), slot_div=k)
+                                      row_slot=_np_dev(slot), slot_div=k, workspace=workspace)
     x = su.ckpt_values(codes, scales)
     xr = x if slot is None else x[slot // k]
     d = D.double().numpy()
@@ -263,6 +263,23 @@ def test_wgrad_ckpt_many_tiles_a_workgroup():
     """More output tiles than workgroups, of unlike k-lengths, so that workgroups go from tile to tile."""
     T, k, E, P, Q = 900, 2, 40, 1056, 1032
     _check_wgrad(*_wgrad_case(T, k, E, P, Q, 11), k, E)
+
+
+@pytest.mark.parametrize("sizes,P,Q", [([3000, 500, 20, 0, 481], 256, 520), ([0, 0, 4096], 64, 64), ([4095], 160, 1032),
+                                       ([1, 2, 2500, 1, 2500], 96, 8), ([900, 700, 800, 600, 1001], 288, 264)])
+def test_wgrad_ckpt_long_groups_cut_along_their_rows(sizes, P, Q):
+    """Groups longer than a workgroup's mean load, with every size of workspace: none, too small for the pieces
+    wanted, and the one asked for (some of it past the end of what is needed); the same bits on every run."""
+    E, M = len(sizes), sum(sizes)
+    case = _wgrad_case(M, 1, E, P, Q, M, sizes=sizes)
+    n = moe._lib.lib().moe_wgrad_ckpt_workspace_bytes(E, M, P, Q)
+    assert n >= 1 << 18
+    for bytes_ in (0, (1 << 18) + 16, 5 << 18, n, n + (1 << 20)):
+        ws = torch.full((bytes_ + 4096,), 0x5a, dtype=torch.uint8, device=DEV)
+        out = _check_wgrad(*case, 1, E, workspace=ws[:bytes_])
+        assert (ws[bytes_:] == 0x5a).all()
+        again = _check_wgrad(*case, 1, E, workspace=ws[:bytes_])
+        assert torch.equal(out, again)
 
 
 def test_wgrad_ckpt_rows_of_other_groups_never_enter():

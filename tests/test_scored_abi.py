@@ -79,8 +79,9 @@ def test_ckpt_refusals(lib):
 
 
 def test_wgrad_ckpt_refusals(lib):
-    def w(codes=FAKE, scales=FAKE, a_rows=64, slot=FAKE, div=2, D=FAKE, off=FAKE, E=4, M=128, P=64, Q=64, out=FAKE):
-        return lib.moe_grouped_gemm_wgrad_ckpt(codes, scales, a_rows, slot, div, D, off, E, M, P, Q, out, None)
+    def w(codes=FAKE, scales=FAKE, a_rows=64, slot=FAKE, div=2, D=FAKE, off=FAKE, E=4, M=128, P=64, Q=64, out=FAKE,
+          ws=None):
+        return lib.moe_grouped_gemm_wgrad_ckpt(codes, scales, a_rows, slot, div, D, off, E, M, P, Q, out, ws, 0, None)
 
     assert w(P=48) == _lib.MOE_ERR_UNSUPPORTED
     assert w(Q=60) == _lib.MOE_ERR_UNSUPPORTED
@@ -94,6 +95,10 @@ def test_wgrad_ckpt_refusals(lib):
     assert w(off=None) == _lib.MOE_ERR_NULL
     assert w(codes=None) == _lib.MOE_ERR_NULL
     assert w(out=ODD) == _lib.MOE_ERR_ALIGN
+    assert w(ws=ODD) == _lib.MOE_ERR_ALIGN
+    size = lib.moe_wgrad_ckpt_workspace_bytes
+    assert size(4, 2047, 64, 64) == 0 and size(4, 1 << 16, 64, 64) > 0
+    assert size(4, 1 << 16, 48, 64) == 0 and size(0, 1 << 16, 64, 64) == 0
 
 
 def test_routed_layer_refusals(lib):
