@@ -29,7 +29,8 @@ __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restri
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
     float x[8];
     if (BF16) {
-      const u32x4_t v = ld16(static_cast<const uint16_t*>(src) + i * 8);
+      const u32x4_t v =
+          __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(src) + i * 8));
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         x[2 * m] = bf16_lo(v[m]);
@@ -37,7 +38,7 @@ __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restri
       }
     } else {
       const f32x4_t* f = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(src) + i * 8);
-      const f32x4_t a = f[0], b = f[1];
+      const f32x4_t a = __builtin_nontemporal_load(f), b = __builtin_nontemporal_load(f + 1);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         x[m] = a[m];
@@ -82,7 +83,7 @@ __global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __re
       u32x4_t o;
 #pragma unroll
       for (int m = 0; m < 4; ++m) o[m] = pack_bf16x2(x[2 * m], x[2 * m + 1]);
-      st16(static_cast<uint16_t*>(dst) + i * 8, o);
+      __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(dst) + i * 8));
     } else {
       f32x4_t* f = reinterpret_cast<f32x4_t*>(static_cast<float*>(dst) + i * 8);
       f[0] = f32x4_t{x[0], x[1], x[2], x[3]};
@@ -91,9 +92,12 @@ __global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __re
   }
 }
 
-// SwiGLU backward from the 8-bit h = [gate | up] of row r, one wave a row.
-// q = row_slot[r] (or r), w = slot_scale[q] (or 1), s = sigmoid(g):
+// SwiGLU backward from the 8-bit h = [gate | up] of row r, LPR lanes a row (64 / LPR rows a wave), 8 columns a
+// lane and round. q = row_slot[r] (or r), w = slot_scale[q] (or 1), s = sigmoid(g):
 //   a = g s u,  dh = [w da u s (1 + g (1 - s)) | w da g s],  dslot_scale[q] = sum_m da a (a unrounded)
+// Bound by memory: 4 bytes read and 6 written a column. The outputs are read by other kernels much later and the
+// inputs not again: both go past the caches.
+template <int LPR>
 __global__ __launch_bounds__(256) void swiglu_bwd_ckpt_kernel(int64_t M, int mlp, const uint16_t* __restrict__ da,
                                                               const int8_t* __restrict__ hc,
                                                               const uint8_t* __restrict__ hs,
@@ -101,49 +105,49 @@ __global__ __launch_bounds__(256) void swiglu_bwd_ckpt_kernel(int64_t M, int mlp
                                                               const float* __restrict__ slot_scale,
                                                               uint16_t* __restrict__ dh, uint16_t* __restrict__ a,
                                                               float* __restrict__ dscale) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & (LPR - 1);
   const int nch = mlp / 8;
-  for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < M; r += (int64_t)gridDim.x * 4) {
-    int64_t q = row_slot ? row_slot[r] : r;
-    const bool inside = q >= 0 && q < M;
-    const float w = inside ? (slot_scale ? slot_scale[q] : 1.0f) : 0.0f;
-    float dot = 0.0f;
-    for (int c = lane; c < nch; c += 64) {
-      const u32x4_t dv = ld16(da + r * mlp + c * 8);
-      const u32x2_t gv = *reinterpret_cast<const u32x2_t*>(hc + r * 2 * mlp + c * 8);
-      const u32x2_t uv = *reinterpret_cast<const u32x2_t*>(hc + r * 2 * mlp + mlp + c * 8);
-      const float gst = ckpt_step(hs[r * (mlp / 16) + (c >> 2)]);
-      const float ust = ckpt_step(hs[r * (mlp / 16) + mlp / 32 + (c >> 2)]);
-      float og[8], ou[8], oa[8];
+  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  if (r >= M) return;  // whole rows leave together; the sum below stays within a row's lanes
+  const int64_t q = row_slot ? row_slot[r] : r;
+  const bool inside = q >= 0 && q < M;
+  const float w = inside ? (slot_scale ? slot_scale[q] : 1.0f) : 0.0f;
+  float dot = 0.0f;
+  for (int c = lane; c < nch; c += LPR) {
+    const u32x4_t dv = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(da + r * mlp + c * 8));
+    const u32x2_t gv = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(hc + r * 2 * mlp + c * 8));
+    const u32x2_t uv = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(hc + r * 2 * mlp + mlp + c * 8));
+    const float gst = ckpt_step(hs[r * (mlp / 16) + (c >> 2)]);
+    const float ust = ckpt_step(hs[r * (mlp / 16) + mlp / 32 + (c >> 2)]);
+    float og[8], ou[8], oa[8];
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const float g = (float)((int32_t)(gv[m >> 2] << (24 - 8 * (m & 3))) >> 24) * gst;
-        const float u = (float)((int32_t)(uv[m >> 2] << (24 - 8 * (m & 3))) >> 24) * ust;
-        const float d = (m & 1) ? bf16_hi(dv[m >> 1]) : bf16_lo(dv[m >> 1]);
-        const float s = 1.0f / (1.0f + expf(-g));
-        const float gs = g * s;
-        oa[m] = gs * u;
-        dot = __builtin_fmaf(d, oa[m], dot);
-        const float dw = d * w;
-        og[m] = dw * u * (s * (1.0f + g * (1.0f - s)));
-        ou[m] = dw * gs;
-      }
-      u32x4_t vg, vu, va;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        vg[m] = pack_bf16x2(og[2 * m], og[2 * m + 1]);
-        vu[m] = pack_bf16x2(ou[2 * m], ou[2 * m + 1]);
-        va[m] = pack_bf16x2(oa[2 * m], oa[2 * m + 1]);
-      }
-      st16(dh + r * 2 * mlp + c * 8, vg);
-      st16(dh + r * 2 * mlp + mlp + c * 8, vu);
-      if (a) st16(a + r * mlp + c * 8, va);
+    for (int m = 0; m < 8; ++m) {
+      const float g = (float)((int32_t)(gv[m >> 2] << (24 - 8 * (m & 3))) >> 24) * gst;
+      const float u = (float)((int32_t)(uv[m >> 2] << (24 - 8 * (m & 3))) >> 24) * ust;
+      const float d = (m & 1) ? bf16_hi(dv[m >> 1]) : bf16_lo(dv[m >> 1]);
+      const float s = 1.0f / (1.0f + expf(-g));
+      const float gs = g * s;
+      oa[m] = gs * u;
+      dot = __builtin_fmaf(d, oa[m], dot);
+      const float dw = d * w;
+      og[m] = dw * u * (s * (1.0f + g * (1.0f - s)));
+      ou[m] = dw * gs;
     }
-    if (dscale) {
+    u32x4_t vg, vu, va;
 #pragma unroll
-      for (int s = 32; s >= 1; s >>= 1) dot += __shfl_xor(dot, s);
-      if (lane == 0 && inside) dscale[q] = dot;
+    for (int m = 0; m < 4; ++m) {
+      vg[m] = pack_bf16x2(og[2 * m], og[2 * m + 1]);
+      vu[m] = pack_bf16x2(ou[2 * m], ou[2 * m + 1]);
+      va[m] = pack_bf16x2(oa[2 * m], oa[2 * m + 1]);
     }
+    __builtin_nontemporal_store(vg, reinterpret_cast<u32x4_t*>(dh + r * 2 * mlp + c * 8));
+    __builtin_nontemporal_store(vu, reinterpret_cast<u32x4_t*>(dh + r * 2 * mlp + mlp + c * 8));
+    if (a) __builtin_nontemporal_store(va, reinterpret_cast<u32x4_t*>(a + r * mlp + c * 8));
+  }
+  if (dscale) {
+#pragma unroll
+    for (int s = LPR / 2; s >= 1; s >>= 1) dot += __shfl_xor(dot, s);
+    if (lane == 0 && inside) dscale[q] = dot;
   }
 }
 
@@ -183,8 +187,20 @@ hipError_t launch_swiglu_bwd_ckpt(int64_t M, int mlp, const uint16_t* da, const 
                                   const uint8_t* h_scales, const int32_t* row_slot, const float* slot_scale,
                                   uint16_t* dh, uint16_t* a, float* dslot_scale, hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  swiglu_bwd_ckpt_kernel<<<dim3(grid_of(M, 4)), dim3(256), 0, stream>>>(M, mlp, da, h_codes, h_scales, row_slot,
-                                                                        slot_scale, dh, a, dslot_scale);
+  // lanes a row: the largest of 64, 32, 16, 8 that leaves the fewest lanes idle in the last round
+  const int nch = mlp / 8;
+  int lpr = 64, idle = (64 - nch % 64) % 64;
+  for (int l = 32; l >= 8; l /= 2)
+    if ((l - nch % l) % l < idle) lpr = l, idle = (l - nch % l) % l;
+  const dim3 grid((unsigned)((M * lpr + 255) / 256)), block(256);
+#define MOE_SWIGLU_BWD(L)                                                                                       \
+  swiglu_bwd_ckpt_kernel<L><<<grid, block, 0, stream>>>(M, mlp, da, h_codes, h_scales, row_slot, slot_scale, dh, a, \
+                                                        dslot_scale)
+  if (lpr == 64) MOE_SWIGLU_BWD(64);
+  else if (lpr == 32) MOE_SWIGLU_BWD(32);
+  else if (lpr == 16) MOE_SWIGLU_BWD(16);
+  else MOE_SWIGLU_BWD(8);
+#undef MOE_SWIGLU_BWD
   return hipGetLastError();
 }
 
