@@ -412,8 +412,8 @@ int moe_swiglu_bwd_ckpt(int64_t M, int32_t mlp, const moe_bf16_t* da, const int8
  *  checkpointed once, read through sorted_slot with slot_div = k), or r
  *  without row_slot (a_rows must be M). D [M, Q] bf16, C [E, P, Q] bf16,
  *  fp32 accumulate; the values of X enter the products unrounded. An empty
- *  group gives exact zeros. P % 32 == 0, Q % 8 == 0, a_rows * P < 2^31,
- *  M < 2^31.
+ *  group gives exact zeros. P % 32 == 0, Q % 8 == 0, Q < 2^25,
+ *  a_rows * P < 2^31, M < 2^31.
  *  ws: scratch of moe_wgrad_ckpt_workspace_bytes(E, M, P, Q) bytes, or less, or
  *  NULL. With it an expert that holds more rows than a workgroup's mean load is
  *  cut along its rows and the pieces' sums are added in row order; with less,

@@ -446,15 +446,17 @@ def _need_like(t, name, shape, dtype, device):
 
 
 def _need_typed(t, name, ndim):
-    """A float32 or bfloat16 tensor of ndim dimensions; returns its MOE_* type."""
+    """A contiguous float32 or bfloat16 device tensor of ndim dimensions; returns its MOE_* type."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _TYPE:
+    ty = _TYPE.get(t.dtype)
+    if ty is None:
         raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
-    _need(t, name, t.dtype)
+    if not (t.is_cuda and t.is_contiguous()):
+        _need(t, name, t.dtype)
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
-    return _TYPE[t.dtype]
+    return ty
 
 
 def _need_rank2(t, name, dtype, device):
@@ -463,12 +465,19 @@ def _need_rank2(t, name, dtype, device):
         raise ValueError(f"{name} must have 2 dimensions, got {None if t is None else tuple(t.shape)}")
 
 
+@functools.lru_cache(maxsize=None)
+def _entry(fn):
+    return getattr(_lib.lib(), fn)
+
+
 def _call(fn, dev, *args):
     """Library call `fn` on dev's current stream, with dev current: tensors pass as pointers, None as NULL."""
-    if dev.index != torch.cuda.current_device():
+    i = dev.index
+    if i != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(fn, dev, *args)
-    status = getattr(_lib.lib(), fn)(*[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args], _stream(dev))
+    stream = _raw_stream(i) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    status = _entry(fn)(*[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args], stream)
     if status != _lib.MOE_OK:
         _lib.check(status, fn)
 

@@ -1634,8 +1634,10 @@ __global__ __launch_bounds__(GTHR) void wgrad_ckpt_join_kernel(WgradCkptP p) {
   const int tp = (p.P + kCkP - 1) / kCkP, tq = (p.Q + kCkQ - 1) / kCkQ, tt = tp * tq;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int seen = 0;  // units of the cut experts before this one, modulo the grid: unit u of all is workgroup u's
+  const u32x4_t sum = ld16(p.cuts->sum);
+  if ((sum[0] | sum[1] | sum[2] | sum[3]) == 0) return;
   for (int k = 0; k < kMaxExperts; ++k) {
-    if ((k & 63) >= p.cuts->sum[k >> 6]) {
+    if ((uint32_t)(k & 63) >= sum[k >> 6]) {
       k |= 63;
       continue;
     }

@@ -176,6 +176,9 @@ int check_wgrad_ckpt(int64_t a_rows, bool gather, int32_t slot_div, int32_t E, i
   if (M > 0 && a_rows == 0) return fail(MOE_ERR_SHAPE, "no checkpoint rows for %lld rows", (long long)M);
   if (a_rows >= (int64_t(1) << 31) || a_rows * P >= (int64_t(1) << 31))
     return fail(MOE_ERR_UNSUPPORTED, "a_rows * P >= 2^31");
+  if (Q >= (1 << 25)) return fail(MOE_ERR_UNSUPPORTED, "Q >= 2^25");  // 32 rows of D in 32-bit byte offsets
+  if ((int64_t)E * (((int64_t)P + 127) / 128) * (((int64_t)Q + 511) / 512) >= (int64_t(1) << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "tile count too large");
   return MOE_OK;
 }
 

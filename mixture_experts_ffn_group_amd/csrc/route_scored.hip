@@ -348,7 +348,7 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
       for (int i = 0; i < N; ++i) {
         const bool on = l[i] > -INFINITY;
         flag |= on && !(fabsf(c[i]) < 1.99f);
-        const int v = (int)(c[i] * 67108864.0f) + kHalf28;
+        const int v = (int)(__builtin_amdgcn_fmed3f(c[i], -1.995f, 1.995f) * 67108864.0f) + kHalf28;
         key[i] = on ? ((uint32_t)max(v, 1) << 4) | (uint32_t)(15 - i) : 0u;
       }
     } else if (EXACT16) {
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int v = (int)((l[i] - mx) * 4194304.0f) + kHalf28;  // saturates below
+        const int v = (int)(fmaxf(l[i] - mx, -33.0f) * 4194304.0f) + kHalf28;  // negative from 32 below mx on
         key[i] = v > 0 && l[i] > -INFINITY ? ((uint32_t)v << 4) | (uint32_t)(15 - i) : 0u;
       }
     }

@@ -350,3 +350,59 @@ def test_graph_replays_and_streams_equal_eager():
     torch.cuda.synchronize()
     for a, b, r in zip(o1, o2, step(x)):
         assert torch.equal(a, r) and torch.equal(b, r)
+
+
+def test_cut_groups_in_a_graph_on_one_workspace():
+    """A captured gradient whose groups are cut, replayed with other loads in between: some cut nothing, some other
+    groups, all on the same workspace."""
+    E, M, P, Q = 4, 5000, 128, 520
+    codes, scales, slot, off, D = _wgrad_case(M, 1, E, P, Q, 3, sizes=[4000, 1000, 0, 0])
+    codes, scales, slot, off, D = (_np_dev(v) if isinstance(v, np.ndarray) else v.to(DEV)
+                                   for v in (codes, scales, slot, off, D))
+    ws = torch.empty(moe._lib.lib().moe_wgrad_ckpt_workspace_bytes(E, M, P, Q), dtype=torch.uint8, device=DEV)
+
+    def run(o, w):
+        return moe.grouped_gemm_wgrad_ckpt(codes, scales, D, o, E, row_slot=slot, slot_div=1, workspace=w)
+
+    run(off, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(off, ws)
+    for sizes in ([0, 0, 5000, 0], [1250, 1250, 1250, 1250], [10, 20, 0, 4970], [0, 0, 0, 0], [4000, 1000, 0, 0]):
+        o = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device=DEV)
+        off.copy_(o)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, run(o, None)), sizes
+
+
+def test_outputs_end_where_they_should():
+    """Every output inside a larger buffer, through the C interface: nothing past its end changes."""
+    import ctypes as C
+    lib = moe._lib.lib()
+    st = C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    p = lambda t: C.c_void_p(t.data_ptr())  # noqa: E731
+
+    def buf(n):
+        return torch.full((n + 4096,), 0x5a, dtype=torch.uint8, device=DEV)
+
+    M, K = 37, 96
+    x = _rows(M, K, 1).to(DEV)
+    c, s, v = buf(M * K), buf(M * K // 32), buf(M * K * 2)
+    assert lib.moe_ckpt_quantize(p(x), 0, M, K, p(c), p(s), st) == 0
+    assert lib.moe_ckpt_dequantize(p(c), p(s), M, K, None, 1, M, p(v), 1, st) == 0
+    mlp = K // 2 // 32 * 32
+    da = torch.ones((M, mlp), dtype=torch.bfloat16, device=DEV)
+    h = torch.zeros(M * 2 * mlp, dtype=torch.int8, device=DEV)
+    hs = torch.full((M * mlp // 16,), 120, dtype=torch.uint8, device=DEV)
+    dh, a, ds = buf(M * 2 * mlp * 2), buf(M * mlp * 2), buf(M * 4)
+    assert lib.moe_swiglu_bwd_ckpt(M, mlp, p(da), p(h), p(hs), None, None, p(dh), p(a), p(ds), st) == 0
+    E, Q = 3, 72
+    off = torch.tensor([0, 20, 20, M], dtype=torch.int32, device=DEV)
+    D = torch.ones((M, Q), dtype=torch.bfloat16, device=DEV)
+    w = buf(E * K * Q * 2)
+    assert lib.moe_grouped_gemm_wgrad_ckpt(p(c), p(s), M, None, 1, p(D), p(off), E, M, K, Q, p(w), None, 0, st) == 0
+    torch.cuda.synchronize()
+    for b in (c, s, v, dh, a, ds, w):
+        assert (b[-4096:] == 0x5a).all()

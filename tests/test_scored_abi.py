@@ -85,6 +85,8 @@ def test_wgrad_ckpt_refusals(lib):
 
     assert w(P=48) == _lib.MOE_ERR_UNSUPPORTED
     assert w(Q=60) == _lib.MOE_ERR_UNSUPPORTED
+    assert w(Q=1 << 25) == _lib.MOE_ERR_UNSUPPORTED
+    assert w(E=256, P=1 << 25, Q=1 << 14, a_rows=1) == _lib.MOE_ERR_UNSUPPORTED
     assert w(E=0) == _lib.MOE_ERR_SHAPE
     assert w(E=257) == _lib.MOE_ERR_UNSUPPORTED
     assert w(div=0) == _lib.MOE_ERR_SHAPE
