@@ -578,8 +578,11 @@ def swiglu_bwd_ckpt(da: torch.Tensor, h_codes: torch.Tensor, h_scales: torch.Ten
     _need_rank2(da, "da", torch.bfloat16, None)
     dev = da.device
     M, mlp = da.shape
-    _need_ckpt(h_codes, h_scales, "h_", dev)
-    _need_like(h_codes, "h_codes", (M, 2 * mlp), torch.int8, dev)
+    for t, n, sh, d in ((h_codes, "h_codes", (M, 2 * mlp), torch.int8),
+                        (h_scales, "h_scales", (M, mlp // 16), torch.uint8)):
+        if t is None:
+            raise ValueError(f"{n} is missing")
+        _need_like(t, n, sh, d, dev)
     _need_like(row_slot, "row_slot", (M,), torch.int32, dev)
     _need_like(slot_scale, "slot_scale", (M,), torch.float32, dev)
     dh = torch.empty((M, 2 * mlp), dtype=torch.bfloat16, device=dev)

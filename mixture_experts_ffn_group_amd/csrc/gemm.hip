@@ -1383,18 +1383,22 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
     for (int j = 0; j < 8; ++j)
       b2lds16(rd, d_off[j & 3] + (uint32_t)((j >> 2) * 8 * p.Q), lds_d + st * kCkDStage + j * 1024);
   };
-  auto prologue = [&]() {  // codes of the first four k-slices, D of the first three
+  // codes of the first four k-slices, D of the first three; D, which needs no index, on its way before the wait
+  auto prologue = [&]() {
     if (!loader || nk == 0) return;
     if (GATHER) {
       issue_idx(0);
       if (nk > kIdxChunk) issue_idx(1);
-      wait_vm_all();
+    }
+    for (int s = 0; s < kCkDRing; ++s)
+      if (s < nk) issue_d(s, s);
+    if (GATHER) {
+      if (nk >= 3) asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
+      else if (nk == 2) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
     }
     for (int s = 0; s < NST; ++s)
-      if (s < nk) {
-        issue_a(s);
-        if (s < kCkDRing) issue_d(s, s);
-      }
+      if (s < nk) issue_a(s);
   };
   // codes of k-slice kt -> operand tile kt % 2: lane's 8 elements of row 4 wave + lane / 16
   const int crow = wave * 4 + (lane >> 4), cch = lane & 15;
@@ -1470,11 +1474,10 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
     const bool busy = q0 + wave_u * 64 < p.Q;  // a wave without columns converts and copies only
 
     if (nk > 0) {
-      // codes of k-slices 0 and 1 and D of 0 have landed: convert, publish
+      // codes of k-slices 0, 1 and 2 and D of 0 to 2 have landed (only the codes and steps of 3 may be in flight):
+      // convert the first two, publish
       if (loader) {
-        if (nk >= 4) asm volatile("s_waitcnt vmcnt(20)" ::: "memory");
-        else if (nk == 3) asm volatile("s_waitcnt vmcnt(18)" ::: "memory");
-        else if (nk == 2) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+        if (nk >= 4) asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
         else wait_vm_all();
       }
       kbarrier();
@@ -1752,7 +1755,7 @@ hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int
                      reinterpret_cast<float*>(static_cast<char*>(ws) + kCkCutBytes), (int)cap, (int)grid.x};
   if (row_slot) wgrad_ckpt_kernel<true><<<grid, block, 0, stream>>>(p);
   else wgrad_ckpt_kernel<false><<<grid, block, 0, stream>>>(p);
-  if (cap > 0) wgrad_ckpt_join_kernel<<<grid, block, 0, stream>>>(p);
+  if (cap > 0) wgrad_ckpt_join_kernel<<<dim3(4 * grid.x), block, 0, stream>>>(p);
   return hipGetLastError();
 }
 
