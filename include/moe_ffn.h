@@ -333,8 +333,9 @@ int moe_route_bwd(const moe_shape_t* shape, const moe_bf16_t* x, const float* wr
  *  Weights: w = s at the picks; renorm: divided by their sum (0 where the sum
  *  is 0); times scale.
  * Choice values are compared in 64 bits, and without a bias experts (and
- * groups with group_top 1) are compared by their logits; weights are rounded
- * once to fp32 from more than 32 bits.
+ * groups with group_top 1) are compared by their logits; weights are computed
+ * in 64 bits (but for the terms of softmax's sum, which may have 32) and
+ * rounded once to fp32.
  *  Needs E % n_group == 0, 1 <= topk_group <= n_group, group_top 1 or 2 and
  *  at most E / n_group, k <= topk_group * (E / n_group), scale finite and > 0.
  *

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import operator
 
 import torch
 
@@ -491,7 +492,7 @@ def _route_shape(T, E, k):
 def _router(score, n_group, topk_group, group_top, renorm, scale):
     if score not in _SCORE:
         raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
-    return C.byref(_lib.MoeRouter(_SCORE[score], n_group, topk_group, group_top, int(bool(renorm)), scale))
+    return C.byref(_lib.MoeRouter(_SCORE[score], n_group, topk_group, group_top, renorm, scale))
 
 
 def route_scored(k: int, logits: torch.Tensor, balance_bias: torch.Tensor | None = None, score: str = "softmax",
@@ -504,7 +505,10 @@ def route_scored(k: int, logits: torch.Tensor, balance_bias: torch.Tensor | None
     dev = logits.device
     T, E = logits.shape
     _need_like(balance_bias, "balance_bias", (E,), torch.float32, dev)
-    r = _router(score, n_group, topk_group, group_top, renorm, scale)
+    # plain numbers, as the structures below are kept by value
+    k = operator.index(k)
+    r = _router(score, operator.index(n_group), operator.index(topk_group), operator.index(group_top), bool(renorm),
+                float(scale))
     kk = k if k > 0 else 0  # a k <= 0 is the library's to refuse
     idx = torch.empty((T, kk), dtype=torch.int32, device=dev)
     w = torch.empty((T, kk), dtype=torch.float32, device=dev)
@@ -525,7 +529,7 @@ def route_scored_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch
                     (dtopk_w, "dtopk_w", torch.float32)):
         _need_like(t, n, (T, k), d, dev)
     d = torch.empty_like(logits)
-    _call("moe_route_scored_bwd", dev, _route_shape(T, E, k), _router(score, 1, 1, 1, renorm, scale), logits, ty,
+    _call("moe_route_scored_bwd", dev, _route_shape(T, E, k), _router(score, 1, 1, 1, bool(renorm), float(scale)), logits, ty,
           topk_idx, topk_w, dtopk_w, d)
     return d
 
@@ -657,7 +661,7 @@ def ffn_fwd_routed(x: torch.Tensor, wi: torch.Tensor, wo: torch.Tensor, topk_idx
                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """MoE FFN forward on a given routing (route, route_scored, or the caller's own): (y [T, emb] bf16, saved dict
     or None). save: None, "full" (the set ffn_bwd takes; keep_h as in ffn_fwd) or "int8" (the set ffn_bwd_ckpt
-    takes). workspace: uint8 of at least workspace_bytes_routed(...) bytes."""
+    takes); a set holds topk_idx and topk_w themselves, not copies. workspace: uint8 of at least workspace_bytes_routed(...) bytes."""
     if save not in (None, "full", "int8"):
         raise ValueError(f'save must be None, "full" or "int8", got {save!r}')
     _need_rank2(x, "x", torch.bfloat16, None)

@@ -107,7 +107,8 @@ __global__ __launch_bounds__(256) void swiglu_bwd_ckpt_kernel(int64_t M, int mlp
                                                               float* __restrict__ dscale) {
   const int lane = threadIdx.x & (LPR - 1);
   const int nch = mlp / 8;
-  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
+  // (a launch holds 2^32 lanes of x at most)
+  const int64_t r = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x) / LPR;
   if (r >= M) return;  // whole rows leave together; the sum below stays within a row's lanes
   const int64_t q = row_slot ? row_slot[r] : r;
   const bool inside = q >= 0 && q < M;
@@ -192,7 +193,9 @@ hipError_t launch_swiglu_bwd_ckpt(int64_t M, int mlp, const uint16_t* da, const 
   int lpr = 64, idle = (64 - nch % 64) % 64;
   for (int l = 32; l >= 8; l /= 2)
     if ((l - nch % l) % l < idle) lpr = l, idle = (l - nch % l) % l;
-  const dim3 grid((unsigned)((M * lpr + 255) / 256)), block(256);
+  const int64_t blocks = (M * lpr + 255) / 256;
+  const unsigned gx = grid_of(blocks, 1);
+  const dim3 grid(gx, (unsigned)((blocks + gx - 1) / gx)), block(256);
 #define MOE_SWIGLU_BWD(L)                                                                                       \
   swiglu_bwd_ckpt_kernel<L><<<grid, block, 0, stream>>>(M, mlp, da, h_codes, h_scales, row_slot, slot_scale, dh, a, \
                                                         dslot_scale)

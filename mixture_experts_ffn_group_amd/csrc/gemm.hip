@@ -1400,7 +1400,8 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
     for (int s = 0; s < NST; ++s)
       if (s < nk) issue_a(s);
   };
-  // codes of k-slice kt -> operand tile kt % 2: lane's 8 elements of row 4 wave + lane / 16
+  // codes of k-slice kt -> operand tile kt % 2: lane's 8 elements of row 4 wave + lane / 16. (Codes as unsigned
+  // bytes with -128 steps in the multiplication's addend take as long and leave fp32 at the largest step.)
   const int crow = wave * 4 + (lane >> 4), cch = lane & 15;
   u32x2_t cv;
   uint32_t cs;
@@ -1410,14 +1411,13 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_ckpt_kernel(WgradCkptP p) {
   };
   auto conv_write = [&](int kt) {
     const float held = ckpt_step(cs);
-    const float step = crow < n - kt * GBK ? held : 0.0f, bias = -128.0f * step;
+    const float step = crow < n - kt * GBK ? held : 0.0f;
     u32x4_t o;
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
-      const uint32_t b = cv[d] ^ 0x80808080u;  // code + 128 in each byte
       float f[4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) f[m] = __builtin_fmaf((float)((b >> (8 * m)) & 0xffu), step, bias);
+      for (int m = 0; m < 4; ++m) f[m] = (float)((int32_t)(cv[d] << (24 - 8 * m)) >> 24) * step;
       o[2 * d] = pack_bf16x2(f[0], f[1]);
       o[2 * d + 1] = pack_bf16x2(f[2], f[3]);
     }

@@ -200,6 +200,27 @@ def test_swiglu_bwd_ckpt_slots_out_of_range():
     assert (dh[1::2] == 0).all()
 
 
+def test_swiglu_bwd_ckpt_more_rows_than_one_launch_takes():
+    """2^29 + 5 rows, past 2^32 lanes: the first and the last rows as in a call of their own."""
+    M, mlp, n = 2 ** 29 + 5, 32, 300
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info(DEV)[0] < 180 << 30:
+        pytest.skip("needs 140 GB of device memory")
+    rng = torch.Generator().manual_seed(1)
+    da = torch.zeros((M, mlp), dtype=torch.bfloat16, device=DEV)
+    codes = torch.zeros((M, 2 * mlp), dtype=torch.int8, device=DEV)
+    scales = torch.full((M, 2), 127, dtype=torch.uint8, device=DEV)
+    for r in (slice(0, n), slice(M - n, M)):
+        da[r] = torch.randn((n, mlp), generator=rng).to(torch.bfloat16)
+        codes[r] = torch.randint(-127, 128, (n, 2 * mlp), generator=rng, dtype=torch.int8)
+    dh, _, ds = moe.swiglu_bwd_ckpt(da, codes, scales, want_a=False)
+    for r in (slice(0, n), slice(M - n, M)):
+        small, _, dss = moe.swiglu_bwd_ckpt(*(t[r].clone() for t in (da, codes, scales)), want_a=False)
+        assert torch.equal(dh[r], small) and torch.equal(ds[r], dss)
+    del da, codes, scales, dh, ds
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ weight gradient
 
 def _wgrad_case(T, k, E, P, Q, seed, sizes=None):
@@ -294,6 +315,21 @@ def test_wgrad_ckpt_rows_of_other_groups_never_enter():
                                       row_slot=_np_dev(slot), slot_div=1)
     assert torch.isfinite(out[0].float()).all() and torch.isfinite(out[2].float()).all()
     assert torch.isnan(out[1].float()).all()
+
+
+def test_wgrad_ckpt_ends_of_the_scale_range():
+    """Blocks at both ends of the scale codes (2^127 and more in magnitude; values that are subnormal), a code a
+    group, with D scaled so that the sums stay in range; and codes of -128, which the quantizer never writes."""
+    rng = np.random.default_rng(8)
+    cs, n, P, Q = [254, 253, 247, 127, 8, 7, 2, 1], 40, 96, 72
+    E, M = len(cs), len(cs) * n
+    codes = rng.integers(-128, 128, (M, P)).astype(np.int8)
+    codes[:n] = np.maximum(codes[:n], -127)  # -128 of the largest step is past bf16
+    scales = np.repeat(np.array(cs, np.uint8), n)[:, None].repeat(P // 32, axis=1)
+    d = rng.integers(1, 8, (M, Q)) * np.ldexp(1.0, np.minimum(137 - scales[:, :1].astype(np.int64), 120))
+    D = torch.from_numpy(d).to(torch.bfloat16)
+    off = (np.arange(E + 1) * n).astype(np.int32)
+    _check_wgrad(codes, np.ascontiguousarray(scales), np.arange(M, dtype=np.int32), off, D, 1, E)
 
 
 def test_wgrad_ckpt_no_rows():

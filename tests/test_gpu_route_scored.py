@@ -262,6 +262,22 @@ def test_route_scored_bwd_against_differences(score, renorm):
     assert np.abs(d - num).max() < 2e-6
 
 
+def test_arguments_held_in_tensors_are_read_at_each_call():
+    """k and scale as 0-dim tensors that change between the calls."""
+    logits = torch.randn((5, 16), generator=torch.Generator().manual_seed(2)).to(DEV)
+    k, scale = torch.tensor(4), torch.tensor(2.0)
+    i4, w4 = moe.route_scored(k, logits, scale=scale)
+    k.fill_(2)
+    scale.fill_(1.0)
+    i2, w2 = moe.route_scored(k, logits, scale=scale)
+    ri, rw = moe.route_scored(2, logits)
+    assert i4.shape == (5, 4) and torch.equal(i2, ri) and torch.equal(w2, rw)
+    d = moe.route_scored_bwd(logits, ri, rw, torch.ones_like(rw), score="sigmoid", renorm=False, scale=scale)
+    scale.fill_(3.0)
+    d3 = moe.route_scored_bwd(logits, ri, rw, torch.ones_like(rw), score="sigmoid", renorm=False, scale=scale)
+    assert torch.equal(d, d3)  # the factor is in the weights
+
+
 def test_no_tokens():
     l = torch.zeros((0, 16), device=DEV)
     idx, w = moe.route_scored(3, l)

@@ -265,3 +265,45 @@ def test_bad_routings_stay_inside_the_buffers():
     moe.ffn_bwd_ckpt(d["dy"], saved, d["wi"], d["wo"])
     torch.cuda.synchronize()
     assert (guard == 0x5a).all()
+
+
+def test_bad_routings_leave_neighbouring_memory():
+    """The same routings and an index set written over by hand, every output and scratch in a larger buffer."""
+    import ctypes as C
+
+    from mixture_experts_ffn_group_amd import _lib
+
+    T, emb, mlp, E, k = 40, 64, 64, 4, 2
+    S = T * k
+    d = _case(T, emb, mlp, E, k, 2)
+    idx, w = moe.route(k, d["x"], d["wr"])
+    idx[3] = torch.tensor([-1, 2**31 - 1], dtype=torch.int32)
+    idx[7] = torch.tensor([1, 1], dtype=torch.int32)
+    guards = []
+
+    def buf(n):
+        b = torch.full((n + 8192,), 0x5a, dtype=torch.uint8, device=DEV)
+        guards.append((b, n))
+        return b[4096:4096 + n]
+
+    sizes = dict(group_sizes=4 * E, group_offsets=4 * (E + 1), sorted_slot=4 * S, slot_row=4 * S, x_codes=T * emb,
+                 x_scales=T * emb // 32, h_codes=S * 2 * mlp, h_scales=S * mlp // 16)
+    saved = {n: buf(v) for n, v in sizes.items()}
+    y = buf(T * emb * 2)
+    out = [buf(n) for n in (T * emb * 2, E * emb * 2 * mlp * 2, E * mlp * emb * 2, S * 4)]
+    s = _lib.shape(T, emb, mlp, E, k)
+    wf, wb = moe.workspace_bytes_routed(T, emb, mlp, E, k), moe.workspace_bytes_routed(T, emb, mlp, E, k, True)
+    ws_f, ws_b = buf(wf), buf(wb)
+    s8 = _lib.MoeSaved8(*[saved[n].data_ptr() for n in sizes])
+    dev = torch.device(DEV)
+    moe._call("moe_ffn_fwd_routed", dev, C.byref(s), d["x"], idx, w, d["wi"], d["wo"], y, None, C.byref(s8), ws_f, wf)
+    for offsets in (None, [0, 70, 20, 2**31 - 1, -5]):
+        if offsets:
+            saved["group_offsets"].view(torch.int32).copy_(torch.tensor(offsets, dtype=torch.int32))
+            for n in ("sorted_slot", "slot_row"):
+                saved[n].view(torch.int32)[::3] = 2**31 - 1
+                saved[n].view(torch.int32)[1::3] = -7
+        moe._call("moe_ffn_bwd_ckpt", dev, C.byref(s), d["dy"], w, C.byref(s8), d["wi"], d["wo"], *out, ws_b, wb)
+    torch.cuda.synchronize()
+    for b, n in guards:
+        assert (b[:4096] == 0x5a).all() and (b[4096 + n:] == 0x5a).all()
