@@ -21,7 +21,10 @@
 namespace moe {
 namespace {
 
-// Eight consecutive elements of a row per thread; four threads share a block.
+// Eight consecutive elements of a row per thread; four threads share a block, whose maximum takes two lane
+// exchanges. Bound by memory, so the source is read past the caches (it is not read again here) and the codes,
+// which the backward reads, are stored through them. 58.7 M bf16 values: 32 us, 5.5 TB/s; 100.7 M fp32 values:
+// 87 us, 5.8 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restrict__ src, int64_t n8,
                                                             int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -58,6 +61,8 @@ __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restri
   }
 }
 
+// Bound by memory: 58.7 M values to bf16 in 28 us (6.4 TB/s, the codes partly from the Infinity Cache), 100.7 M
+// in 46 us.
 // Eight elements per thread of destination row r, from source row row_index[r] / row_div (clamped) or r.
 template <bool BF16>
 __global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __restrict__ codes,
@@ -95,7 +100,7 @@ __global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __re
 // SwiGLU backward from the 8-bit h = [gate | up] of row r, LPR lanes a row (64 / LPR rows a wave), 8 columns a
 // lane and round. q = row_slot[r] (or r), w = slot_scale[q] (or 1), s = sigmoid(g):
 //   a = g s u,  dh = [w da u s (1 + g (1 - s)) | w da g s],  dslot_scale[q] = sum_m da a (a unrounded)
-// Bound by memory: 4 bytes read and 6 written a column. The outputs are read by other kernels much later and the
+// Bound by memory: 4 bytes read and 6 written a column; 262144 rows of 768 take 357 us, 5.7 TB/s. The outputs are read by other kernels much later and the
 // inputs not again: both go past the caches.
 template <int LPR>
 __global__ __launch_bounds__(256) void swiglu_bwd_ckpt_kernel(int64_t M, int mlp, const uint16_t* __restrict__ da,
@@ -188,7 +193,9 @@ hipError_t launch_swiglu_bwd_ckpt(int64_t M, int mlp, const uint16_t* da, const 
                                   const uint8_t* h_scales, const int32_t* row_slot, const float* slot_scale,
                                   uint16_t* dh, uint16_t* a, float* dslot_scale, hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  // lanes a row: the largest of 64, 32, 16, 8 that leaves the fewest lanes idle in the last round
+  // lanes a row: the largest of 64, 32, 16, 8 that leaves the fewest lanes idle in the last round. Against 64
+  // lanes throughout: 2^20 rows of 64 columns 671 -> 135 us, of 128 668 -> 250, 2^18 of 768 363 -> 359, of 320
+  // 196 -> 182
   const int nch = mlp / 8;
   int lpr = 64, idle = (64 - nch % 64) % 64;
   for (int l = 32; l >= 8; l /= 2)

@@ -211,11 +211,17 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __
 // left goes to route_row_exact: a pick that is disabled, values out of the
 // integers' range, more close values than candidates, close softmax scores
 // (their 64-bit sum runs over all experts). Groups too close at the edge of
-// those that stay are ranked the same way, by the exact scores of their two best. bf16 logits without a bias leave 16 bits for the
-// expert itself: those keys are exact, ties included.
+// those that stay are ranked the same way, by the exact scores of their two
+// best. bf16 logits without a bias leave 16 bits for the expert itself: those
+// keys are exact, ties included.
 //
-// Per four tokens of 128 experts about 400 vector instructions and no LDS
-// without groups, against some 4000 of the 64-bit form.
+// Bound by the issue of vector instructions: per four tokens of 128 experts
+// some 480 (of them 190 in the k = 8 rounds, 80 in the 64-bit weights) and no
+// LDS without groups, against some 4000 of the 64-bit form a token. Measured:
+// 32768 tokens x 128, softmax: 9.3 us (49 us with a token a wave in 64 bits);
+// 8192 x 256, sigmoid, bias, 4 of 8 groups: 9.6 us (40 us); 4 tokens x 256:
+// 5.9 us (18 us), the latency of one wave. Their logits alone, at a copy's rate, take
+// 4.0 and 1.9 us.
 constexpr int kHalf28 = 1 << 27;
 
 template <class V, int N>
@@ -612,8 +618,10 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(RouteBwdP p, cons
 }
 
 // The same, four tokens a wave on 16 lanes each (k <= 16), the row assembled in
-// LDS and stored 4 elements a lane where E is a multiple of 4. A wave a token
-// left most lanes idle at 60 experts (32749 x 60 bf16: 12.9 us).
+// LDS and stored 4 elements a lane where E is a multiple of 4. Latency bounds
+// it (2 us of memory at a copy's rate): 32749 x 60 bf16, every logit with a
+// gradient, 5.0 us (12.8 us with a wave a token, most lanes idle); 8192 x 256
+// fp32, picks only, 4.4 us (5.0 us).
 template <class V, int N>
 __global__ __launch_bounds__(256) void route_scored_bwd16_kernel(RouteBwdP p, const V* __restrict__ logits,
                                                                  V* __restrict__ dlogits) {
@@ -717,6 +725,8 @@ hipError_t launch_route_scored(int64_t T, int E, int k, int score, int n_group, 
   const RouteP p{T, E, k, score, n_group, topk_group, group_top, renorm, scale, bias, topk_idx, topk_w};
   const bool groups = topk_group < n_group;
   const bool choice = bias != nullptr || (groups && group_top == 2);
+  // k <= 16: a pick a lane; groups: one a lane, of whole runs of four experts. The rest takes the 64-bit form,
+  // three to five times as long (figures above).
   if (k <= 16 && (!groups || (n_group <= 16 && (E / n_group) % 4 == 0))) {
     if (logits_bf16) {
       const uint16_t* l = static_cast<const uint16_t*>(logits);
