@@ -414,12 +414,11 @@ int moe_swiglu_bwd_ckpt(int64_t M, int32_t mlp, const moe_bf16_t* da, const int8
  *  without row_slot (a_rows must be M). D [M, Q] bf16, C [E, P, Q] bf16,
  *  fp32 accumulate; the values of X enter the products unrounded. An empty
  *  group gives exact zeros. P % 32 == 0, Q % 8 == 0, Q < 2^25,
- *  a_rows * P < 2^31, M < 2^31.
+ *  a_rows * P < 2^31, M < 2^31 - 64.
  *  ws: scratch of moe_wgrad_ckpt_workspace_bytes(E, M, P, Q) bytes, or less, or
- *  NULL. With it an expert that holds more rows than a workgroup's mean load is
- *  cut along its rows and the pieces' sums are added in row order; with less,
- *  fewer are cut, and without, none, which changes no more than the order of
- *  the fp32 additions.
+ *  NULL. With it long experts may be cut along their rows and the pieces' sums
+ *  added in row order; with less, fewer are cut, and without, none, which
+ *  changes no more than the order of the fp32 additions.
  */
 size_t moe_wgrad_ckpt_workspace_bytes(int32_t E, int64_t M, int32_t P, int32_t Q);
 int moe_grouped_gemm_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int64_t a_rows,

@@ -48,6 +48,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "lanes.h"
 
 namespace moe {
 namespace {
@@ -1114,11 +1115,10 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_kernel(WgradP p) {
 // 1500 rows of 12 experts, 256 x 384: 12.5 us, the latency of one tile on 24 workgroups.
 //
 // Work list, made for skewed loads, which routers have in practice: the tiles are dealt longest first, in turns
-// of one a workgroup, every second turn backwards, an expert's tiles (which share its rows) to one XCD. Where the
-// caller gives a workspace, an expert longer than half the mean load of a workgroup is cut along its rows into
-// pieces of at most that; they leave fp32 partial tiles in the workspace, which a second kernel adds in
-// row order. Dealt by expert, as wgrad_kernel does, a hot expert holds one XCD, and each of its tiles one
-// workgroup, for its whole length.
+// of one a workgroup, every second turn backwards, a turn's neighbours (which share an expert's rows) to one XCD.
+// Where the caller gives a workspace, long experts may be cut along their rows (ckpt_plan); the pieces leave fp32
+// partial tiles in the workspace, which a second kernel adds in row order. Dealt by expert, as wgrad_kernel does, a
+// hot expert holds one XCD, and each of its tiles one workgroup, for its whole length.
 struct WgradCkptP {
   const int8_t* A;
   const uint8_t* S;  // step codes [a_rows, P / 32]
@@ -1162,7 +1162,7 @@ __device__ __forceinline__ void g2lds1(const void* sbase, uint32_t voff, uint32_
 constexpr size_t kCkCutBytes = 8192;   // holds a WgradCkptCuts
 static_assert(sizeof(WgradCkptCuts) <= kCkCutBytes, "the list fits its place");
 constexpr int kCkPart = kCkP * kCkQ;  // floats of a partial tile
-constexpr int kCkMinCut = 32;         // k-slices below which an expert is not cut
+constexpr int kCkMinCut = 12;         // k-slices below which an expert is not cut
 constexpr int kCkNoCut = 0x3fffffff;
 constexpr int kCkMinRows = 2048;      // rows in all below which none is
 
@@ -1184,22 +1184,61 @@ struct WgradCkptPlan {
   int order[kMaxExperts];     // experts in list order
   int unit[kMaxExperts + 1];  // first unit of the i-th of them; a unit is a piece, all its tiles
   int part[kMaxExperts];      // first partial tile of a cut expert
-  __attribute__((aligned(16))) uint32_t key[kMaxExperts];
+  float time[GTHR / 64];      // what each wave's list would take
   int cut;                    // k-slices of the longest piece
 };
 // Exclusive sums over the experts 4 lane + u, and their total.
 __device__ __forceinline__ int plan_scan(const int (&v)[4], int (&before)[4]) {
-  const int lane = threadIdx.x & 63;
   int incl = v[0] + v[1] + v[2] + v[3];
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
+  // row_shr 1, 2, 4, 8 within each 16 lanes, then the broadcasts of lanes 15 and 31
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xa, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xc, 0xf, false);
   before[0] = incl - (v[0] + v[1] + v[2] + v[3]);
 #pragma unroll
   for (int u = 1; u < 4; ++u) before[u] = before[u - 1] + v[u - 1];
   return __builtin_amdgcn_readlane(incl, 63);
+}
+// Keys 4 lane + u in falling order (a bitonic network over the first n, a power of two; the rest are 0).
+__device__ __forceinline__ void plan_sort(uint32_t (&key)[4], int n) {
+  const int lane = threadIdx.x & 63;
+  for (int k = 2; k <= n; k <<= 1) {
+    for (int j = k >> 1; j >= 4; j >>= 1) {
+      const bool high = (4 * lane & k) == 0 ? (4 * lane & j) == 0 : (4 * lane & j) != 0;  // keeps the larger
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)key[u], j >> 2);
+        key[u] = high ? max(key[u], o) : min(key[u], o);
+      }
+    }
+    auto pair = [&](int x, int y) {
+      const bool down = ((4 * lane + x) & k) == 0;
+      const uint32_t hi = max(key[x], key[y]), lo = min(key[x], key[y]);
+      key[x] = down ? hi : lo;
+      key[y] = down ? lo : hi;
+    };
+    if (k > 2) pair(0, 2), pair(1, 3);
+    pair(0, 1), pair(2, 3);
+  }
+}
+// The cut decides how even the workgroups' loads are, how many tiles each starts and ends, and how many partial
+// tiles are written and added, and a workgroup's load goes in whole tiles: no multiple of the mean load comes near
+// the best cut for all. So each of the eight waves works out the list and the time of one cut (0.6 to 4 times the
+// mean load, or the longest expert if that is shorter; or none), and the fastest list is used. Times are in
+// k-slices: a tile takes 8 besides its own, one that leaves a partial tile 10, the joining launch 6 and 1/18 a
+// partial tile, fitted to 47 timings of lists of eight loads. Against a cut at half the mean load: 32768 rows of 16
+// experts, Zipf(1.1), 1024 x 1024, 128 -> 98 us; 16384 of 5, the same, 80 -> 65; 8192 of one, 2048 x 1536,
+// 101 -> 79; 262144 of 128, Zipf(1.1), 2048 x 1536, 1.80 -> 1.73 ms (one box; 1.67 -> 1.63 on a faster one); 16384
+// of 32, 1024 x 1024, and equal experts, the same. It adds about 1 us.
+__device__ __forceinline__ float plan_factor(int wave) {
+  constexpr float f[7] = {0.6f, 0.9f, 1.1f, 1.25f, 1.5f, 2.5f, 4.0f};
+  float r = f[0];
+#pragma unroll
+  for (int i = 1; i < 7; ++i) r = wave == i ? f[i] : r;
+  return r;
 }
 __device__ __forceinline__ void ckpt_plan(const WgradCkptP& p, int tt, WgradCkptPlan& pl) {
   const int tid = threadIdx.x;
@@ -1212,28 +1251,85 @@ __device__ __forceinline__ void ckpt_plan(const WgradCkptP& p, int tt, WgradCkpt
     return;
   }
   __syncthreads();
-  const int lane = tid & 63;
-  if (tid < 64) {
-    int ns[4], count[4], len[4], v[4], parts[4];
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  auto slices = [&](int e) { return (max(0, pl.off[e + 1] - pl.off[e]) + GBK - 1) / GBK; };
+  int ns[4], count[4], len[4], v[4], parts[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) ns[u] = 4 * lane + u < p.E ? slices(4 * lane + u) : 0;
+  const float mean = (float)plan_scan(ns, parts) * (float)tt / (float)p.grid;  // load of a workgroup
+  const int longest = (int)wave_max_u32((uint32_t)max(max(ns[0], ns[1]), max(ns[2], ns[3])));
+  // (lengths of pieces stay below 2^24: the key's)
+  const bool may = p.cap > 0 && longest >= 2 * kCkMinCut && mean < 4e6f;
+  const int cut = may && wave < 7 ? max(kCkMinCut, (int)(plan_factor(wave) * fminf(mean, (float)longest))) : kCkNoCut;
+  uint32_t key[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    ckpt_pieces(ns[u], cut, &count[u], &len[u]);
+    v[u] = count[u] > 1 ? (int)min((int64_t)count[u] * tt, (int64_t)(1 << 22)) : 0;  // sums stay in an int
+    const int e = 4 * lane + u;  // the key orders by length, then expert
+    key[u] = e < p.E ? ((uint32_t)min(len[u], (1 << 24) - 1) << 8) | (uint32_t)(255 - e) : 0u;
+  }
+  const int partials = plan_scan(v, parts);
+  int n = 4;
+  while (n < p.E) n <<= 1;
+  plan_sort(key, n);
+  // units of the experts in list order
+  int first[4], num[4];
+  float cost[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    num[u] = 0;
+    cost[u] = 0.0f;
+    if (4 * lane + u < p.E) {
+      const int l = (int)(key[u] >> 8), s = slices(255 - (int)(key[u] & 255u));
+      num[u] = s <= cut ? 1 : (s + l - 1) / l;
+      cost[u] = (float)l + (num[u] > 1 ? 10.0f : 8.0f);
+    }
+  }
+  const int units = plan_scan(num, first);
+  // the longest of three workgroups' loads: the one that starts with the longest items, the one that starts with
+  // the shortest of the first turn, and the last to have an item in the last turn
+  float time = 0.0f;
+  if (may) {
+    // (quotients in fp32: one that is off by one changes an estimate)
+    const int g = p.grid, items = (int)((uint32_t)units * (uint32_t)tt), tail = items - (int)((float)items * (1.0f / (float)g)) * g;
+    int q[5], r[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int x = (int)((uint32_t)(i < 4 ? first[i] : first[3] + num[3]) * (uint32_t)tt);
+      q[i] = (int)((float)x * (1.0f / (float)g));
+      r[i] = x - q[i] * g;
+    }
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+      const int at = c == 0 ? 0 : (c == 1 || tail <= 0 ? g - 1 : tail - 1);
+      // items of this workgroup before item x: one a turn, at `at` of it or, in odd turns, at g - 1 - at
+      int before[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) before[i] = q[i] + ((q[i] & 1 ? g - 1 - at : at) < r[i]);
+      float load = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load += cost[u] * (float)(before[u + 1] - before[u]);
+      time = fmaxf(time, wave_sum(load));
+    }
+    if (partials > 0) time += 6.0f + (float)partials * (1.0f / 18.0f);
+    if (partials > p.cap) time = INFINITY;
+  }
+  if (lane == 0) pl.time[wave] = time;
+  __syncthreads();
+  int best = 7;  // without cuts, always possible
+#pragma unroll
+  for (int i = 6; i >= 0; --i)
+    if (pl.time[i] < pl.time[best]) best = i;
+  if (wave == best) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = 4 * lane + u;
-      ns[u] = e < p.E ? (max(0, pl.off[e + 1] - pl.off[e]) + GBK - 1) / GBK : 0;
-    }
-    const float mean = (float)plan_scan(ns, parts) * (float)tt / (float)p.grid;  // load of a workgroup
-    int cut = p.cap > 0 && mean < 1e9f ? max(kCkMinCut, (int)(0.5f * mean)) : kCkNoCut;
-    for (;;) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        ckpt_pieces(ns[u], cut, &count[u], &len[u]);
-        v[u] = count[u] > 1 ? (int)min((int64_t)count[u] * tt, (int64_t)(1 << 22)) : 0;  // sums stay in an int
+      if (e < p.E) {
+        pl.part[e] = parts[u];
+        pl.order[e] = 255 - (int)(key[u] & 255u);
+        pl.unit[e] = first[u];
       }
-      if (plan_scan(v, parts) <= p.cap || cut == kCkNoCut) break;
-      cut = cut < (1 << 28) ? 2 * cut : kCkNoCut;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = 4 * lane + u;
       if (p.cuts && blockIdx.x == 0) {  // one workgroup leaves the list for the joining kernel
         const bool is = e < p.E && count[u] > 1;
         const uint64_t cuts = __ballot(is);
@@ -1245,45 +1341,11 @@ __device__ __forceinline__ void ckpt_plan(const WgradCkptP& p, int tt, WgradCkpt
         }
         if (lane == 0) p.cuts->sum[u] = __popcll(cuts);
       }
-      if (e < p.E) {
-        pl.part[e] = parts[u];
-        // count and length are recomputed where they are needed; the key orders by length, then expert
-        pl.key[e] = ((uint32_t)min(len[u], (1 << 24) - 1) << 8) | (uint32_t)(255 - e);
-      } else if (e < kMaxExperts) {
-        pl.key[e] = 0;
-      }
     }
-    if (lane == 0) pl.cut = cut;
-  }
-  __syncthreads();
-  if (tid < p.E) {
-    const uint32_t mine = pl.key[tid];
-    int rank = 0;
-    for (int i = 0; i < (p.E + 3) / 4; ++i) {
-      const u32x4_t o = *reinterpret_cast<const u32x4_t*>(&pl.key[4 * i]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) rank += o[u] > mine;
+    if (lane == 0) {
+      pl.unit[p.E] = units;
+      pl.cut = cut;
     }
-    pl.order[rank] = tid;
-  }
-  __syncthreads();
-  if (tid < 64) {
-    int v[4], first[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      v[u] = 0;
-      if (4 * lane + u < p.E) {
-        const int e = pl.order[4 * lane + u];
-        int count, len;
-        ckpt_pieces((max(0, pl.off[e + 1] - pl.off[e]) + GBK - 1) / GBK, pl.cut, &count, &len);
-        v[u] = count;
-      }
-    }
-    const int units = plan_scan(v, first);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (4 * lane + u < p.E) pl.unit[4 * lane + u] = first[u];
-    if (lane == 0) pl.unit[p.E] = units;
   }
   __syncthreads();
 }
@@ -1737,12 +1799,12 @@ hipError_t launch_wgrad(const uint16_t* A, const uint16_t* D, const int32_t* gro
 }
 
 size_t wgrad_ckpt_workspace(int E, int64_t M, int P, int Q) {
-  // An expert is cut into pieces of at least the mean load of a workgroup, and at least kCkMinCut k-slices, so
-  // there are at most twice the workgroups, or 2 / kCkMinCut of all k-slices, of them.
+  // Two partial tiles a workgroup, or one per 16 k-slices where there are fewer: lists that would need more are
+  // hardly ever the fastest.
   const int64_t tt = (int64_t)((P + kCkP - 1) / kCkP) * ((Q + kCkQ - 1) / kCkQ);
   const int64_t slices = (M / GBK + E) * tt;
   if (M < kCkMinRows) return 0;
-  const int64_t n = std::min<int64_t>(2 * persistent_grid(), 2 * slices / kCkMinCut + 2 * tt);
+  const int64_t n = std::min<int64_t>(2 * persistent_grid(), slices / 16 + 2 * tt);
   return kCkCutBytes + (size_t)n * kCkPart * sizeof(float);
 }
 

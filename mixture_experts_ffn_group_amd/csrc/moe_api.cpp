@@ -169,6 +169,7 @@ int check_ckpt(int64_t rows, int32_t K) {
 
 int check_wgrad_ckpt(int64_t a_rows, bool gather, int32_t slot_div, int32_t E, int64_t M, int32_t P, int32_t Q) {
   if (int rc = check_wgrad(E, M, P, Q)) return rc;
+  if (M >= (int64_t(1) << 31) - 64) return fail(MOE_ERR_UNSUPPORTED, "M >= 2^31 - 64");  // rows rounded up to k-slices
   if (P % 32) return fail(MOE_ERR_UNSUPPORTED, "P (%d) is not a multiple of 32", P);
   if (a_rows < 0) return fail(MOE_ERR_SHAPE, "need a_rows >= 0");
   if (M > 0 && !gather && a_rows != M) return fail(MOE_ERR_SHAPE, "without row_slot, a_rows must equal M");

@@ -303,6 +303,21 @@ def test_wgrad_ckpt_long_groups_cut_along_their_rows(sizes, P, Q):
         assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("E,M,P,Q,power", [(256, 6000, 32, 8, 1.5), (255, 9000, 64, 520, 1.1), (61, 12000, 96, 72, 2.0),
+                                           (17, 20000, 160, 1032, 1.1), (64, 5000, 1056, 40, 0.0), (2, 9001, 288, 8, 3.0)])
+def test_wgrad_ckpt_skewed_loads(E, M, P, Q, power):
+    """Work lists of many and few experts in shuffled order of load, some cut, with the workspace asked for."""
+    rng = np.random.default_rng(E + M)
+    w = np.arange(1, E + 1) ** -power
+    sizes = rng.permutation(rng.multinomial(M, w / w.sum()))
+    case = _wgrad_case(M, 1, E, P, Q, M, sizes=sizes)
+    n = moe._lib.lib().moe_wgrad_ckpt_workspace_bytes(E, M, P, Q)
+    ws = torch.full((n + 4096,), 0x5a, dtype=torch.uint8, device=DEV)
+    out = _check_wgrad(*case, 1, E, workspace=ws[:n])
+    assert (ws[n:] == 0x5a).all()
+    assert torch.equal(out, _check_wgrad(*case, 1, E, workspace=ws[:n]))
+
+
 def test_wgrad_ckpt_rows_of_other_groups_never_enter():
     """NaN in a row of another group, in rows behind the last group and in a token no row reads."""
     k, E, P, Q = 1, 3, 64, 64
