@@ -523,11 +523,13 @@ def route_scored_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch
     ty = _need_typed(logits, "logits", 2)
     dev = logits.device
     T, E = logits.shape
-    _need_rank2(topk_idx, "topk_idx", torch.int32, dev)
-    k = topk_idx.shape[1]
-    for t, n, d in ((topk_idx, "topk_idx", torch.int32), (topk_w, "topk_w", torch.float32),
-                    (dtopk_w, "dtopk_w", torch.float32)):
-        _need_like(t, n, (T, k), d, dev)
+    if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
+        _need_rank2(topk_idx, "topk_idx", torch.int32, dev)
+    shape = (T, topk_idx.shape[1])
+    _need_like(topk_idx, "topk_idx", shape, torch.int32, dev)
+    _need_like(topk_w, "topk_w", shape, torch.float32, dev)
+    _need_like(dtopk_w, "dtopk_w", shape, torch.float32, dev)
+    k = shape[1]
     d = torch.empty_like(logits)
     _call("moe_route_scored_bwd", dev, _route_shape(T, E, k), _router(score, 1, 1, 1, bool(renorm), float(scale)), logits, ty,
           topk_idx, topk_w, dtopk_w, d)
@@ -582,15 +584,14 @@ def swiglu_bwd_ckpt(da: torch.Tensor, h_codes: torch.Tensor, h_scales: torch.Ten
     _need_rank2(da, "da", torch.bfloat16, None)
     dev = da.device
     M, mlp = da.shape
-    for t, n, sh, d in ((h_codes, "h_codes", (M, 2 * mlp), torch.int8),
-                        (h_scales, "h_scales", (M, mlp // 16), torch.uint8)):
-        if t is None:
-            raise ValueError(f"{n} is missing")
-        _need_like(t, n, sh, d, dev)
+    if h_codes is None or h_scales is None:
+        raise ValueError("h_codes or h_scales is missing")
+    _need_like(h_codes, "h_codes", (M, 2 * mlp), torch.int8, dev)
+    _need_like(h_scales, "h_scales", (M, mlp // 16), torch.uint8, dev)
     _need_like(row_slot, "row_slot", (M,), torch.int32, dev)
     _need_like(slot_scale, "slot_scale", (M,), torch.float32, dev)
     dh = torch.empty((M, 2 * mlp), dtype=torch.bfloat16, device=dev)
-    a = torch.empty((M, mlp), dtype=torch.bfloat16, device=dev) if want_a else None
+    a = torch.empty_like(da) if want_a else None
     ds = torch.empty(M, dtype=torch.float32, device=dev) if want_dscale else None
     _call("moe_swiglu_bwd_ckpt", dev, M, mlp, da, h_codes, h_scales, row_slot, slot_scale, dh, a, ds)
     return dh, a, ds
