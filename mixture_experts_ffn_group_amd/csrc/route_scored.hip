@@ -197,7 +197,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __
   if (t < p.T) route_row_exact(p, t, logits + t * p.E, s_s[wave], s_k[wave], s_g[wave]);
 }
 
-// Four tokens a wave, token g of the group on lanes 16g .. 16g+15, for k <= 16.
+// Four tokens a wave, token g of the group on lanes 16g .. 16g+15, for k <= 32.
 //
 // The choice runs on 28-bit integers: lane r holds experts 4 (r + 16 q) + i as
 // keys value << 4 | (15 - (4 q + i)), so a sort is min and max only and a pick's
@@ -295,8 +295,9 @@ __device__ __forceinline__ int count_before(double v, int id) {
   return c;
 }
 
-// CHOICE: the order is that of c (a bias, or group values that are sums of scores), else of the logits.
-template <class V, int N, bool CHOICE>
+// CHOICE: the order is that of c (a bias, or group values that are sums of scores), else of the logits. NP picks a
+// lane, pick 16 i + r on lane r; with two, close values go to the 64-bit form.
+template <class V, int N, bool CHOICE, int NP>
 __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* __restrict__ logits) {
   constexpr bool EXACT16 = sizeof(V) == 2 && !CHOICE;
   // a wave's row in the 64-bit form (scores, keys), or its four rows of 32-bit group values or keys
@@ -450,8 +451,10 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
       }
     }
     sort_desc(key);
-    uint32_t my = 0, prev = 0xffffffffu;
-    int my_r = 0;
+    uint32_t my[NP], prev = 0xffffffffu;
+    int my_r[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) my[i] = 0, my_r[i] = 0;
     bool near = false;
     constexpr uint32_t kFirst = EXACT16 ? 0x10000u : 16u;  // smallest key of an enabled expert
     // round j: the row's largest key goes to lane j (of its holders the lowest lane's; equal keys are near)
@@ -459,10 +462,12 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
       const uint32_t m = row_max_fused(key[0]);
       const uint64_t wins = __ballot(key[0] == m);
       const int first = __builtin_ctz((uint32_t)(wins >> (16 * g)) & 0xffffu);
-      if (r == j) {
-        my = m;
-        my_r = first;
-      }
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        if (16 * i + r == j) {
+          my[i] = m;
+          my_r[i] = first;
+        }
       // the winner's keys move up by one: a bitwise select on an opaque mask, which the compiler cannot
       // turn into a choice of registers at run time
       uint32_t pop = 0u - (uint32_t)(r == first);
@@ -482,58 +487,70 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
       const bool close = m >= kFirst && ((prev >> 4) - (m >> 4)) <= thr;
       near |= close;
       flag |= close && k == 16;
-      if (CHOICE && p.bias && p.score == 0) {
+      if (NP > 1 || (CHOICE && p.bias && p.score == 0)) {
         flag |= near;
         near = false;
       }
     }
-    auto expert = [&]() -> int {
-      if (EXACT16) return (int)(0xffffu - (my & 0xffffu));
-      const int i = 15 - (int)(my & 15u);
-      return 4 * (my_r + 16 * (i >> 2)) + (i & 3);
+    auto expert = [&](int pick) -> int {
+      if (EXACT16) return (int)(0xffffu - (my[pick] & 0xffffu));
+      const int i = 15 - (int)(my[pick] & 15u);
+      return 4 * (my_r[pick] + 16 * (i >> 2)) + (i & 3);
     };
-    int e = expert();
-    if (!EXACT16 && __ballot(near) != 0) {
+    int e[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) e[i] = expert(i);
+    if (!EXACT16 && NP == 1 && __ballot(near) != 0) {
       // Close values: the 16 best candidates, one a lane, ranked by their exact choice values. The order
       // stands if none beyond them can reach the picks.
       for (int j = k; j < 16; ++j) {
         const uint32_t m = round(j);
         if (j == 15) flag |= near && m >= kFirst && ((prev >> 4) - (m >> 4)) <= thr;
       }
-      e = expert();
+      e[0] = expert(0);
       double o = -(double)INFINITY;
       int id = 0x10000 + r;  // no candidate: after all others
-      if (my >= kFirst) {
-        id = e;
-        o = (double)load_logit(row + e);
-        if (p.bias) o = 1.0 / (1.0 + exp(-o)) + (double)p.bias[e];
+      if (my[0] >= kFirst) {
+        id = e[0];
+        o = (double)load_logit(row + e[0]);
+        if (p.bias) o = 1.0 / (1.0 + exp(-o)) + (double)p.bias[e[0]];
       }
       const int rank = count_before<1>(o, id);
-      e = __builtin_amdgcn_ds_permute((16 * g + rank) << 2, e);
+      e[0] = __builtin_amdgcn_ds_permute((16 * g + rank) << 2, e[0]);
     }
     const uint64_t flags = __ballot(flag);
     const bool slow = ((flags >> (16 * g)) & 0xffffull) != 0;
-    // weights in 64 bits, a lane a pick
-    double s = 0.0;
-    if (r < k && !slow) {
-      const double x = (double)load_logit(row + e);
-      s = p.score == 0 ? exp(x - (double)mx) : 1.0 / (1.0 + exp(-x));
+    // weights in 64 bits
+    double s[NP], tot = 0.0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      s[i] = 0.0;
+      if (16 * i + r < k && !slow) {
+        const double x = (double)load_logit(row + e[i]);
+        s[i] = p.score == 0 ? exp(x - (double)mx) : 1.0 / (1.0 + exp(-x));
+      }
+      tot += s[i];
     }
     if (p.renorm) {
-      const double tot = row_sum_f64(s);
-      s = tot > 0.0 ? s / tot : 0.0;
+      tot = row_sum_f64(tot);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) s[i] = tot > 0.0 ? s[i] / tot : 0.0;
     } else if (p.score == 0) {
       double sum = 0.0;
       // (a bias may have disabled experts that count in the sum: their logits are read again)
       if (CHOICE) load_row16<V, N>(row, E, r, l);
 #pragma unroll
       for (int i = 0; i < N; ++i) sum += (double)expf(fmaxf(l[i], -INFINITY) - mx);
-      s /= row_sum_f64(sum);
+      sum = row_sum_f64(sum);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) s[i] /= sum;
     }
-    if (r < k && !slow && t0 + g < p.T) {
-      p.idx[t * k + r] = e;
-      p.w[t * k + r] = (float)(s * (double)p.scale);
-    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      if (16 * i + r < k && !slow && t0 + g < p.T) {
+        p.idx[t * k + 16 * i + r] = e[i];
+        p.w[t * k + 16 * i + r] = (float)(s[i] * (double)p.scale);
+      }
     if (flags != 0) {
       for (int h = 0; h < 4; ++h) {
         if (((flags >> (16 * h)) & 0xffffull) == 0 || t0 + h >= p.T) continue;
@@ -617,12 +634,12 @@ __global__ __launch_bounds__(256) void route_scored_bwd_kernel(RouteBwdP p, cons
   }
 }
 
-// The same, four tokens a wave on 16 lanes each (k <= 16), the row assembled in
+// The same, four tokens a wave on 16 lanes each (k <= 32), the row assembled in
 // LDS and stored 4 elements a lane where E is a multiple of 4. Latency bounds
 // it (2 us of memory at a copy's rate): 32749 x 60 bf16, every logit with a
 // gradient, 5.0 us (12.8 us with a wave a token, most lanes idle); 8192 x 256
 // fp32, picks only, 4.4 us (5.0 us).
-template <class V, int N>
+template <class V, int N, int NP>
 __global__ __launch_bounds__(256) void route_scored_bwd16_kernel(RouteBwdP p, const V* __restrict__ logits,
                                                                  V* __restrict__ dlogits) {
   __shared__ __attribute__((aligned(16))) float s_row[4][4][16 * N];
@@ -634,23 +651,31 @@ __global__ __launch_bounds__(256) void route_scored_bwd16_kernel(RouteBwdP p, co
   const int64_t t = min(t0 + g, p.T - 1);
   const V* lt = logits + t * E;
   float* row = s_row[wave][g];
-  int e = -1;
-  float w = 0.0f, gr = 0.0f;
-  if (r < k) {
-    e = p.idx[t * k + r];
-    w = p.w[t * k + r];
-    gr = p.g[t * k + r];
-    if ((unsigned)e >= (unsigned)E || w == 0.0f) e = -1;
+  int e[NP];
+  float w[NP], gr[NP], wg[NP], tot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    e[i] = -1;
+    w[i] = gr[i] = 0.0f;
+    if (16 * i + r < k) {
+      e[i] = p.idx[t * k + 16 * i + r];
+      w[i] = p.w[t * k + 16 * i + r];
+      gr[i] = p.g[t * k + 16 * i + r];
+      if ((unsigned)e[i] >= (unsigned)E || w[i] == 0.0f) e[i] = -1;
+    }
+    wg[i] = e[i] >= 0 ? w[i] * gr[i] : 0.0f;
+    tot += wg[i];
   }
   float l[N];
   const bool dense = p.score == 0 && !p.renorm;
   if (dense) load_row16<V, N>(lt, E, r, l);
-  float wg = e >= 0 ? w * gr : 0.0f;
-  const float tot = row_sum(wg);
-  if (e >= 0) {
-    if (p.renorm) wg = w * (gr - tot / p.scale);
-    if (p.score == 1) wg *= 1.0f / (1.0f + expf(load_logit(lt + e)));
-  }
+  tot = row_sum(tot);
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    if (e[i] >= 0) {
+      if (p.renorm) wg[i] = w[i] * (gr[i] - tot / p.scale);
+      if (p.score == 1) wg[i] *= 1.0f / (1.0f + expf(load_logit(lt + e[i])));
+    }
   float base[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) base[i] = 0.0f;
@@ -678,7 +703,9 @@ __global__ __launch_bounds__(256) void route_scored_bwd16_kernel(RouteBwdP p, co
     *reinterpret_cast<f32x4_t*>(row + 4 * (r + 16 * q)) =
         f32x4_t{base[4 * q], base[4 * q + 1], base[4 * q + 2], base[4 * q + 3]};
   wave_lds_fence();
-  if (e >= 0) row[e] += wg;
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    if (e[i] >= 0) row[e[i]] += wg[i];
   wave_lds_fence();
   if (t0 + g >= p.T) return;
   V* out = dlogits + t * E;
@@ -698,22 +725,35 @@ __global__ __launch_bounds__(256) void route_scored_bwd16_kernel(RouteBwdP p, co
   }
 }
 
-template <class V, int N>
+template <class V, int N, int NP>
 void launch16(const RouteP& p, const V* logits, bool choice, hipStream_t stream) {
   const dim3 grid((unsigned)((p.T + 15) / 16));  // T * 64 < 2^31: the shape check of the call
-  if (choice) route_scored16_kernel<V, N, true><<<grid, dim3(256), 0, stream>>>(p, logits);
-  else route_scored16_kernel<V, N, false><<<grid, dim3(256), 0, stream>>>(p, logits);
+  if (choice) route_scored16_kernel<V, N, true, NP><<<grid, dim3(256), 0, stream>>>(p, logits);
+  else route_scored16_kernel<V, N, false, NP><<<grid, dim3(256), 0, stream>>>(p, logits);
+}
+
+template <class V, int NP>
+void launch16_np(const RouteP& p, const V* l, bool choice, hipStream_t stream) {
+  if (p.E <= 64) launch16<V, 4, NP>(p, l, choice, stream);
+  else if (p.E <= 128) launch16<V, 8, NP>(p, l, choice, stream);
+  else launch16<V, 16, NP>(p, l, choice, stream);
 }
 
 dim3 row_grid(int64_t T) { return dim3((unsigned)((T + 3) / 4)); }
 
+template <class V, int NP>
+void launch_bwd16(const RouteBwdP& p, const V* l, V* d, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.T + 15) / 16)), block(256);
+  if (p.E <= 64) route_scored_bwd16_kernel<V, 4, NP><<<grid, block, 0, stream>>>(p, l, d);
+  else if (p.E <= 128) route_scored_bwd16_kernel<V, 8, NP><<<grid, block, 0, stream>>>(p, l, d);
+  else route_scored_bwd16_kernel<V, 16, NP><<<grid, block, 0, stream>>>(p, l, d);
+}
+
 template <class V>
 void launch_bwd(const RouteBwdP& p, const V* l, V* d, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.T + 15) / 16)), block(256);
-  if (p.k > 16) route_scored_bwd_kernel<V><<<row_grid(p.T), block, 0, stream>>>(p, l, d);
-  else if (p.E <= 64) route_scored_bwd16_kernel<V, 4><<<grid, block, 0, stream>>>(p, l, d);
-  else if (p.E <= 128) route_scored_bwd16_kernel<V, 8><<<grid, block, 0, stream>>>(p, l, d);
-  else route_scored_bwd16_kernel<V, 16><<<grid, block, 0, stream>>>(p, l, d);
+  if (p.k <= 16) launch_bwd16<V, 1>(p, l, d, stream);
+  else if (p.k <= 32) launch_bwd16<V, 2>(p, l, d, stream);
+  else route_scored_bwd_kernel<V><<<row_grid(p.T), dim3(256), 0, stream>>>(p, l, d);
 }
 
 }  // namespace
@@ -725,19 +765,18 @@ hipError_t launch_route_scored(int64_t T, int E, int k, int score, int n_group, 
   const RouteP p{T, E, k, score, n_group, topk_group, group_top, renorm, scale, bias, topk_idx, topk_w};
   const bool groups = topk_group < n_group;
   const bool choice = bias != nullptr || (groups && group_top == 2);
-  // k <= 16: a pick a lane; groups: one a lane, of whole runs of four experts. The rest takes the 64-bit form,
-  // three to five times as long (figures above).
-  if (k <= 16 && (!groups || (n_group <= 16 && (E / n_group) % 4 == 0))) {
+  // k <= 32: one or two picks a lane; groups: one a lane, of whole runs of four experts. The rest takes the 64-bit
+  // form, three to five times as long (figures above; k = 24, 32768 x 128, softmax: 110 us against 19, and with a
+  // bias, where close values are frequent, 107 against 43).
+  if (k <= 32 && (!groups || (n_group <= 16 && (E / n_group) % 4 == 0))) {
     if (logits_bf16) {
       const uint16_t* l = static_cast<const uint16_t*>(logits);
-      if (E <= 64) launch16<uint16_t, 4>(p, l, choice, stream);
-      else if (E <= 128) launch16<uint16_t, 8>(p, l, choice, stream);
-      else launch16<uint16_t, 16>(p, l, choice, stream);
+      if (k <= 16) launch16_np<uint16_t, 1>(p, l, choice, stream);
+      else launch16_np<uint16_t, 2>(p, l, choice, stream);
     } else {
       const float* l = static_cast<const float*>(logits);
-      if (E <= 64) launch16<float, 4>(p, l, choice, stream);
-      else if (E <= 128) launch16<float, 8>(p, l, choice, stream);
-      else launch16<float, 16>(p, l, choice, stream);
+      if (k <= 16) launch16_np<float, 1>(p, l, choice, stream);
+      else launch16_np<float, 2>(p, l, choice, stream);
     }
   } else if (logits_bf16) {
     route_scored_kernel<uint16_t><<<row_grid(T), dim3(256), 0, stream>>>(p, static_cast<const uint16_t*>(logits));

@@ -71,6 +71,30 @@ def test_route_scored_groups(E, n_group, topk_group, k, group_top, score, biased
                renorm=True, scale=2.5)
 
 
+@pytest.mark.parametrize("T,E,k", [(130, 128, 24), (50, 37, 20), (41, 256, 32), (33, 64, 17), (21, 160, 31)])
+@pytest.mark.parametrize("cfg", CONFIGS, ids=lambda c: f"{c['score']}-{'renorm' if c['renorm'] else 'raw'}")
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_scored_17_to_32_picks(T, E, k, cfg, biased, bf16):
+    g = torch.Generator().manual_seed(E)
+    bias = torch.randn(E, generator=g) * 0.05 if biased else None
+    l = _logits(T, E, T + E, bf16)
+    _check(l, bias, k, **cfg)
+    l[3] = -float("inf")
+    l[5, ::2] = float("nan")
+    l[6, :] = 0.5
+    _check(l, bias, k, **cfg)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group,k", [(256, 8, 4, 24), (96, 4, 2, 32), (200, 5, 3, 20), (256, 16, 2, 32)])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_groups_of_17_to_32_picks(E, n_group, topk_group, k, group_top, score, biased):
+    bias = torch.randn(E, generator=torch.Generator().manual_seed(E)) * 0.1 if biased else None
+    _check(_logits(70, E, 70 + k), bias, k, score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+
+
 def test_group_of_one_expert():
     _check(_logits(50, 32, 3), None, 5, score="sigmoid", n_group=32, topk_group=9, group_top=1)
 
@@ -166,6 +190,20 @@ def test_many_tokens_match_the_64_bit_choice(T):
     assert ((w.cpu().double() - ref).abs() <= 4 * 2.0 ** -24 * ref).all()
 
 
+@pytest.mark.parametrize("k", [17, 32])
+def test_many_tokens_and_picks_match_the_64_bit_choice(k):
+    T = 8191
+    g = torch.Generator().manual_seed(k)
+    l = torch.randn((T, 256), generator=g)
+    b = torch.randn(256, generator=g) * 0.05
+    idx, w = moe.route_scored(k, l.to(DEV), balance_bias=b.to(DEV), score="sigmoid")
+    c = torch.sigmoid(l.double()) + b.double()
+    assert torch.equal(idx.cpu().long(), c.topk(k, dim=1).indices)
+    s = torch.sigmoid(l.double()).gather(1, idx.cpu().long())
+    ref = s / s.sum(1, keepdim=True)
+    assert ((w.cpu().double() - ref).abs() <= 4 * 2.0 ** -24 * ref).all()
+
+
 # ------------------------------------------------------------------ gradient
 
 def _bwd_ref(l, idx, w, g, score, renorm, scale):
@@ -219,6 +257,17 @@ def _check_bwd(l, k, score, renorm, scale, seed, bias=None):
 @pytest.mark.parametrize("bf16", [False, True])
 def test_route_scored_bwd(T, E, k, score, renorm, scale, bf16):
     _check_bwd(_logits(T, E, T, bf16), k, score, renorm, scale, seed=T + 1)
+
+
+@pytest.mark.parametrize("T,E,k", [(130, 128, 24), (35, 37, 20), (50, 256, 32), (33, 60, 17)])
+@pytest.mark.parametrize("score,renorm,scale", [("softmax", True, 1.0), ("softmax", False, 2.5),
+                                                ("sigmoid", True, 2.5), ("sigmoid", False, 1.0)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_scored_bwd_17_to_32_picks(T, E, k, score, renorm, scale, bf16):
+    l = _logits(T, E, T, bf16)
+    _check_bwd(l, k, score, renorm, scale, seed=T + 1)
+    l[2, 5:] = -float("inf")  # fewer enabled than picks
+    _check_bwd(l, k, score, renorm, scale, seed=T + 1)
 
 
 @pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True),
