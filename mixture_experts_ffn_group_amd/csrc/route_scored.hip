@@ -207,10 +207,10 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __
 // less than `thr` / 2 units. The picks stand if every pick and the first expert
 // not picked differ from the next by more than thr. Otherwise (about one token
 // in 1000 with a bias) the 16 best candidates are ranked by their exact values,
-// one a lane; that needs 64-bit scores of 16 experts rather than all. What is
-// left goes to route_row_exact: a pick that is disabled, values out of the
-// integers' range, more close values than candidates, close softmax scores
-// (their 64-bit sum runs over all experts). Groups too close at the edge of
+// one a lane; that needs 64-bit scores of 16 experts rather than all (softmax:
+// and the 64-bit sum, 16 lanes a row). What is left goes to route_row_exact: a
+// pick that is disabled, values out of the integers' range, more close values
+// than candidates. Groups too close at the edge of
 // those that stay are ranked the same way, by the exact scores of their two
 // best. bf16 logits without a bias leave 16 bits for the expert itself: those
 // keys are exact, ties included.
@@ -219,9 +219,10 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __
 // some 480 (of them 190 in the k = 8 rounds, 80 in the 64-bit weights) and no
 // LDS without groups, against some 4000 of the 64-bit form a token. Measured:
 // 32768 tokens x 128, softmax: 9.3 us (49 us with a token a wave in 64 bits);
-// 8192 x 256, sigmoid, bias, 4 of 8 groups: 9.6 us (40 us); 4 tokens x 256:
-// 5.9 us (18 us), the latency of one wave. Their logits alone, at a copy's rate, take
-// 4.0 and 1.9 us.
+// with a bias, where close values are frequent, 15.5 us; 8192 x 256, sigmoid,
+// bias, 4 of 8 groups: 9.8 us (40 us), softmax, 13 to 17 us; 4 tokens x 256:
+// 6.0 us (18 us), the latency of one wave. Their logits alone, at a copy's
+// rate, take 4.0 and 1.9 us.
 constexpr int kHalf28 = 1 << 27;
 
 template <class V, int N>
@@ -374,6 +375,21 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
         key[i] = v > 0 && l[i] > -INFINITY ? ((uint32_t)v << 4) | (uint32_t)(15 - i) : 0u;
       }
     }
+    // exact score and choice value of an expert; softmax's sum over the row, logits read again, in 64 bits
+    auto exact_sum = [&]() -> double {
+      double sum = 0.0;
+#pragma unroll 1
+      for (int e = r; e < E; e += 16) {
+        const float x = load_logit(row + e);
+        if (x > -INFINITY) sum += exp((double)x - (double)mx);
+      }
+      return row_sum_f64(sum);
+    };
+    auto exact_choice = [&](int e, double sum) -> double {
+      const double x = (double)load_logit(row + e);
+      const double s = p.score == 0 ? exp(x - (double)mx) / sum : 1.0 / (1.0 + exp(-x));
+      return s + (p.bias ? (double)p.bias[e] : 0.0);
+    };
     if (groups) {
       // the two largest values of each run of four experts, then of each group on its own lane
       const int gs = E / p.n_group, nq = gs >> 2;
@@ -406,8 +422,7 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
       const bool edge = __builtin_popcount(mask) != p.topk_group || lo <= hi + 2 * thr;
       if (!EXACT16 && __ballot(edge) != 0) {
         // Groups too close at the edge: ranked by their exact values, from the two best experts of each,
-        // scored in 64 bits on the group's lane. That needs both certain (the third further off than thr),
-        // and scores that do not hang on the row's sum.
+        // scored in 64 bits on the group's lane. That needs both certain (the third further off than thr).
         uint32_t* const all = reinterpret_cast<uint32_t*>(s_x[wave]) + g * 256;
         wave_lds_fence();
 #pragma unroll
@@ -426,16 +441,10 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
             ka = fa ? kk : ka;
           }
         flag |= edge && (kc >= 16u && ((kb >> 4) - (kc >> 4)) <= thr);
-        if (p.score == 0 && CHOICE) flag |= edge;
+        const double sum = CHOICE && p.score == 0 ? exact_sum() : 1.0;
         double va = -(double)INFINITY, vb = -(double)INFINITY;
-        if (ka >= 16u) {
-          va = (double)load_logit(row + ea);
-          if (CHOICE) va = 1.0 / (1.0 + exp(-va)) + (p.bias ? (double)p.bias[ea] : 0.0);
-        }
-        if (kb >= 16u) {
-          vb = (double)load_logit(row + eb);
-          if (CHOICE) vb = 1.0 / (1.0 + exp(-vb)) + (p.bias ? (double)p.bias[eb] : 0.0);
-        }
+        if (ka >= 16u) va = CHOICE ? exact_choice(ea, sum) : (double)load_logit(row + ea);
+        if (kb >= 16u) vb = CHOICE ? exact_choice(eb, sum) : (double)load_logit(row + eb);
         double v = fmax(va, vb);
         if (p.group_top == 2 && kb >= 16u) v = va > vb ? va + vb : vb + va;
         const int rank = count_before<1>(v, r < p.n_group ? r : 16 + r);
@@ -487,7 +496,7 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
       const bool close = m >= kFirst && ((prev >> 4) - (m >> 4)) <= thr;
       near |= close;
       flag |= close && k == 16;
-      if (NP > 1 || (CHOICE && p.bias && p.score == 0)) {
+      if (NP > 1) {
         flag |= near;
         near = false;
       }
@@ -508,12 +517,12 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
         if (j == 15) flag |= near && m >= kFirst && ((prev >> 4) - (m >> 4)) <= thr;
       }
       e[0] = expert(0);
+      const double sum = p.bias && p.score == 0 ? exact_sum() : 1.0;
       double o = -(double)INFINITY;
       int id = 0x10000 + r;  // no candidate: after all others
       if (my[0] >= kFirst) {
         id = e[0];
-        o = (double)load_logit(row + e[0]);
-        if (p.bias) o = 1.0 / (1.0 + exp(-o)) + (double)p.bias[e[0]];
+        o = p.bias ? exact_choice(id, sum) : (double)load_logit(row + id);
       }
       const int rank = count_before<1>(o, id);
       e[0] = __builtin_amdgcn_ds_permute((16 * g + rank) << 2, e[0]);

@@ -190,6 +190,28 @@ def test_many_tokens_match_the_64_bit_choice(T):
     assert ((w.cpu().double() - ref).abs() <= 4 * 2.0 ** -24 * ref).all()
 
 
+@pytest.mark.parametrize("spread", [0.05, 0.002, 1e-5])
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("E", [256, 100])
+def test_many_tokens_of_softmax_scores_match_the_64_bit_choice(spread, grouped, E):
+    """Biases down to the distance of neighbouring scores: most tokens then have close choice values."""
+    T, k, G, kept = 8191, 7, 4, 2
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn((T, E), generator=g)
+    b = torch.randn(E, generator=g) * spread
+    cfg = dict(n_group=G, topk_group=kept, group_top=2) if grouped else {}
+    idx, w = moe.route_scored(k, l.to(DEV), balance_bias=b.to(DEV), score="softmax", renorm=False, **cfg)
+    s = torch.softmax(l.double(), dim=1)
+    c = s + b.double()
+    if grouped:
+        gv = c.view(T, G, E // G).topk(2, dim=2).values.sum(2)
+        keep = torch.zeros(T, G, dtype=torch.bool).scatter_(1, gv.topk(kept, dim=1).indices, True)
+        c = c.masked_fill(~keep.repeat_interleave(E // G, 1), float("-inf"))
+    assert torch.equal(idx.cpu().long(), c.topk(k, dim=1).indices)
+    ref = s.gather(1, idx.cpu().long())
+    assert ((w.cpu().double() - ref).abs() <= 4 * 2.0 ** -24 * ref).all()
+
+
 @pytest.mark.parametrize("k", [17, 32])
 def test_many_tokens_and_picks_match_the_64_bit_choice(k):
     T = 8191
