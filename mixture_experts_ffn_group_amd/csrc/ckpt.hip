@@ -91,6 +91,7 @@ __global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __re
       __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(dst) + i * 8));
     } else {
       f32x4_t* f = reinterpret_cast<f32x4_t*>(static_cast<float*>(dst) + i * 8);
+      // through the caches, which join the two halves of a lane's 32 bytes: past them 3.5 TB/s instead of 5.6
       f[0] = f32x4_t{x[0], x[1], x[2], x[3]};
       f[1] = f32x4_t{x[4], x[5], x[6], x[7]};
     }
