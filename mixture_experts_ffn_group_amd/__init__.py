@@ -153,6 +153,7 @@ def grouped_gemm(A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Tensor, 
         M = row_slot.numel() if row_slot is not None else A.shape[0]
     E = B.shape[0]
     N = B.shape[2] if op == "nn" else B.shape[1]
+    _lib.need_32_bits(E | K | N | slot_div | grid, "E, K, N, slot_div and grid")
     epi = _EPI[epilogue]
     width = N if epi == MOE_EPI_NONE else (N // 2 if epi == MOE_EPI_SWIGLU else 2 * N)
     C_ = out if out is not None else torch.empty((M, width), dtype=torch.bfloat16, device=dev)
@@ -178,6 +179,7 @@ def grouped_gemm_wgrad(A: torch.Tensor, D: torch.Tensor, group_offsets: torch.Te
     _need(group_offsets, "group_offsets", torch.int32, dev)
     M, P = A.shape
     Q = D.shape[1]
+    _lib.need_32_bits(E | P | Q | grid, "E, P, Q and grid")
     C_ = torch.empty((E, P, Q), dtype=torch.bfloat16, device=dev)
     _lib.check(_lib.lib().moe_grouped_gemm_wgrad_grid(_ptr(A), _ptr(D), _ptr(group_offsets), E, M, P, Q, _ptr(C_),
                                                       grid, _stream(dev)), "moe_grouped_gemm_wgrad")
@@ -194,6 +196,7 @@ def tile_schedule(kind: str, group_offsets, M: int, N: int, grid: int, Q: int = 
 
     off = np.ascontiguousarray(group_offsets, dtype=np.int32)
     E = len(off) - 1
+    _lib.need_32_bits(N | Q | grid, "N, Q and grid")
     count = C.c_int64(0)
     f = _lib.lib().moe_tile_schedule
     _lib.check(f(_SCHED[kind], off.ctypes.data, E, M, N, Q, grid, None, 0, C.byref(count)), "moe_tile_schedule")
@@ -349,6 +352,7 @@ def mx_quantize_rows(src: torch.Tensor, row_index: torch.Tensor | None = None, r
     dev = src.device
     _need(row_index, "row_index", torch.int32, dev)
     R, K = src.shape
+    _lib.need_32_bits(K | row_div, "a row's length and row_div")
     M = rows if rows is not None else (row_index.numel() if row_index is not None else R)
     codes = torch.empty((M, K), dtype=torch.uint8, device=dev)
     scales = torch.empty((K // 64, M, 4), dtype=torch.uint8, device=dev)
@@ -362,6 +366,7 @@ def mx_quantize_weight(w: torch.Tensor):
     (codes [E, N, K] uint8, scales [E, K/64, N, 4] uint8)."""
     _need(w, "w", torch.bfloat16)
     E, K, N = w.shape
+    _lib.need_32_bits(E | K | N, "E, K and N")
     codes = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
     scales = torch.empty((E, K // 64, N, 4), dtype=torch.uint8, device=w.device)
     _lib.check(_lib.lib().moe_mx_quantize_weight(_ptr(w), E, K, N, _ptr(codes), _ptr(scales), _stream(w.device)),
@@ -386,6 +391,7 @@ def grouped_gemm_mx(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torc
     a_rows, K = a_codes.shape
     M = a_rows if row_slot is None else (rows if rows is not None else row_slot.numel())
     E, N, _ = b_codes.shape
+    _lib.need_32_bits(E | K | N | slot_div, "E, K, N and slot_div")
     epi = {"none": 0, "swiglu": 1}[epilogue]
     width = N if epi == 0 else N // 2
     C_ = (out if out is not None else torch.empty((M, width), dtype=torch.bfloat16, device=dev)) if bf16_out \
@@ -492,6 +498,7 @@ def _route_shape(T, E, k):
 def _router(score, n_group, topk_group, group_top, renorm, scale):
     if score not in _SCORE:
         raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
+    _lib.need_32_bits(n_group | topk_group | group_top, "n_group, topk_group and group_top")
     return C.byref(_lib.MoeRouter(_SCORE[score], n_group, topk_group, group_top, renorm, scale))
 
 
@@ -509,10 +516,11 @@ def route_scored(k: int, logits: torch.Tensor, balance_bias: torch.Tensor | None
     k = operator.index(k)
     r = _router(score, operator.index(n_group), operator.index(topk_group), operator.index(group_top), bool(renorm),
                 float(scale))
+    s = _route_shape(T, E, k)
     kk = k if k > 0 else 0  # a k <= 0 is the library's to refuse
     idx = torch.empty((T, kk), dtype=torch.int32, device=dev)
     w = torch.empty((T, kk), dtype=torch.float32, device=dev)
-    _call("moe_route_scored", dev, _route_shape(T, E, k), r, logits, ty, balance_bias, idx, w)
+    _call("moe_route_scored", dev, s, r, logits, ty, balance_bias, idx, w)
     return idx, w
 
 
@@ -542,6 +550,7 @@ def ckpt_quantize(src: torch.Tensor):
     ty = _need_typed(src, "src", 2)
     dev = src.device
     M, K = src.shape
+    _lib.need_32_bits(K, "a row's length")
     codes = torch.empty((M, K), dtype=torch.int8, device=dev)
     scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
     _call("moe_ckpt_quantize", dev, src, ty, M, K, codes, scales)
@@ -566,6 +575,7 @@ def ckpt_dequantize(codes: torch.Tensor, scales: torch.Tensor, row_index: torch.
     if dtype not in _TYPE:
         raise TypeError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
     R, K = codes.shape
+    _lib.need_32_bits(K | row_div, "a row's length and row_div")
     M = R
     if row_index is not None:
         M = row_index.numel()
@@ -584,6 +594,7 @@ def swiglu_bwd_ckpt(da: torch.Tensor, h_codes: torch.Tensor, h_scales: torch.Ten
     _need_rank2(da, "da", torch.bfloat16, None)
     dev = da.device
     M, mlp = da.shape
+    _lib.need_32_bits(mlp, "mlp")
     if h_codes is None or h_scales is None:
         raise ValueError("h_codes or h_scales is missing")
     _need_like(h_codes, "h_codes", (M, 2 * mlp), torch.int8, dev)
@@ -608,6 +619,7 @@ def grouped_gemm_wgrad_ckpt(a_codes: torch.Tensor, a_scales: torch.Tensor, D: to
     _need_rank2(D, "D", torch.bfloat16, dev)
     M, Q = D.shape
     R, P = a_codes.shape
+    _lib.need_32_bits(E | P | Q | slot_div, "E, P, Q and slot_div")
     _need_like(row_slot, "row_slot", (M,), torch.int32, dev)
     if group_offsets is None:
         raise ValueError("group_offsets is missing")

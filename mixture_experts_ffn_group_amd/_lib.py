@@ -131,5 +131,13 @@ def check(status: int, where: str) -> None:
         raise MoeError(status, where, lib().moe_last_error_detail().decode())
 
 
+def need_32_bits(sizes: int, what: str) -> None:
+    """Refuse a number that the library takes in 32 bits and that does not fit (several may come joined by `|`):
+    ctypes keeps the low 32 bits of such a number, so 2^32 + 2 would silently be taken as 2."""
+    if sizes >> 31 not in (0, -1):
+        raise ValueError(f"{what} must fit 32 bits")
+
+
 def shape(T: int, emb: int, mlp: int, E: int, k: int) -> MoeShape:
+    need_32_bits(emb | mlp | E | k, "emb, mlp, E and k")
     return MoeShape(T, emb, mlp, E, k)
