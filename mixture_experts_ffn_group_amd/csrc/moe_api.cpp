@@ -149,12 +149,14 @@ int check_gemm(int op, int epi, int64_t M, int K, int N, int E) {
   return MOE_OK;
 }
 
-int check_wgrad(int32_t E, int64_t M, int32_t P, int32_t Q) {
+int check_wgrad(int32_t E, int64_t M, int32_t P, int32_t Q, int tile = moe::kWgradTile) {
   if (M < 0 || P <= 0 || Q <= 0 || E <= 0) return fail(MOE_ERR_SHAPE, "need M >= 0 and P, Q, E > 0");
   if (E > 256) return fail(MOE_ERR_UNSUPPORTED, "E (%d) > 256", E);
   if (M >= (int64_t(1) << 31)) return fail(MOE_ERR_UNSUPPORTED, "M >= 2^31");
   if (P % 8 || Q % 8) return fail(MOE_ERR_UNSUPPORTED, "P and Q must be multiples of 8");
-  if ((int64_t)E * ((P + 255) / 256) * ((Q + 255) / 256) >= (int64_t(1) << 31))
+  // the last tile's edge, at a multiple of `tile`, stays in 32 bits
+  if (std::max(P, Q) > (int64_t(1) << 31) - tile) return fail(MOE_ERR_UNSUPPORTED, "P or Q > 2^31 - %d", tile);
+  if ((int64_t)E * ((P + 255LL) / 256) * ((Q + 255LL) / 256) >= (int64_t(1) << 31))
     return fail(MOE_ERR_UNSUPPORTED, "tile count too large");
   return MOE_OK;
 }
@@ -168,7 +170,7 @@ int check_ckpt(int64_t rows, int32_t K) {
 }
 
 int check_wgrad_ckpt(int64_t a_rows, bool gather, int32_t slot_div, int32_t E, int64_t M, int32_t P, int32_t Q) {
-  if (int rc = check_wgrad(E, M, P, Q)) return rc;
+  if (int rc = check_wgrad(E, M, P, Q, 128)) return rc;
   if (M >= (int64_t(1) << 31) - 64) return fail(MOE_ERR_UNSUPPORTED, "M >= 2^31 - 64");  // rows rounded up to k-slices
   if (P % 32) return fail(MOE_ERR_UNSUPPORTED, "P (%d) is not a multiple of 32", P);
   if (a_rows < 0) return fail(MOE_ERR_SHAPE, "need a_rows >= 0");
