@@ -197,7 +197,7 @@ int moe_grouped_gemm(int op, int epilogue, const moe_bf16_t* A, const moe_bf16_t
  * gradients of the grouped GEMM, "MoE: fused TensorCore Pallas
  * permute/combine kernels ...", Tests). A [M, P], D [M, Q] bf16;
  * C [E, P, Q] bf16; an empty group gives exact zeros. fp32 accumulate.
- * Needs P % 8 == 0, Q % 8 == 0.
+ * Needs P % 8 == 0, Q % 8 == 0, P and Q < 2^26.
  */
 int moe_grouped_gemm_wgrad(const moe_bf16_t* A, const moe_bf16_t* D, const int32_t* group_offsets, int32_t E,
                            int64_t M, int32_t P, int32_t Q, moe_bf16_t* C, moe_stream_t stream);
@@ -414,7 +414,7 @@ int moe_swiglu_bwd_ckpt(int64_t M, int32_t mlp, const moe_bf16_t* da, const int8
  *  without row_slot (a_rows must be M). D [M, Q] bf16, C [E, P, Q] bf16,
  *  fp32 accumulate; the values of X enter the products unrounded. An empty
  *  group gives exact zeros. P % 32 == 0, Q % 8 == 0, Q < 2^25,
- *  a_rows * P < 2^31, M < 2^31 - 64.
+ *  a_rows * P < 2^31, P <= 2^31 - 128, M < 2^31 - 64.
  *  ws: scratch of moe_wgrad_ckpt_workspace_bytes(E, M, P, Q) bytes, or less, or
  *  NULL. With it long experts may be cut along their rows and the pieces' sums
  *  added in row order; with less, fewer are cut, and without, none, which

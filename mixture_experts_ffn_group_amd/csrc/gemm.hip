@@ -915,8 +915,8 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_kernel(WgradP p) {
   auto issue_loads = [&](int kt) {
     if (!loader) return;
     const int r0 = lo + kt * GBK, rows = min(GBK, n - kt * GBK);
-    const i32x4_t ra = buffer_rsrc(p.A + (int64_t)r0 * p.P, (uint32_t)(rows * p.P * 2));
-    const i32x4_t rd = buffer_rsrc(p.D + (int64_t)r0 * p.Q, (uint32_t)(rows * p.Q * 2));
+    const i32x4_t ra = buffer_rsrc(p.A + (int64_t)r0 * p.P, (uint32_t)rows * p.P * 2u);
+    const i32x4_t rd = buffer_rsrc(p.D + (int64_t)r0 * p.Q, (uint32_t)rows * p.Q * 2u);
     const uint32_t st = (uint32_t)(kt & (NST - 1)) * kOpStage;
 #pragma unroll
     for (int j = 0; j < 4; ++j) b2lds16(ra, a_off[j & 1] + (uint32_t)((j >> 1) * 8 * p.P), lds_a + st + j * 1024);

@@ -384,6 +384,8 @@ int moe_grouped_gemm_wgrad_grid(const moe_bf16_t* A, const moe_bf16_t* D, const 
                                 int64_t M, int32_t P, int32_t Q, moe_bf16_t* C, int32_t grid, moe_stream_t stream) {
   g_detail[0] = 0;
   if (int rc = check_wgrad(E, M, P, Q)) return rc;
+  // a k-slice, 32 rows of A and of D, in 32-bit byte offsets
+  if (M > 0 && std::max(P, Q) >= 1 << 26) return fail(MOE_ERR_UNSUPPORTED, "P or Q >= 2^26");
   if (int rc = check_grid(grid)) return rc;
   NEED(group_offsets);
   NEED(C);
