@@ -346,8 +346,11 @@ int moe_route_bwd(const moe_shape_t* shape, const moe_bf16_t* x, const float* wr
  *   renorm, softmax: dl_j = w_j (g_j - D)       renorm, sigmoid: times (1 - s_j)
  *   sigmoid:         dl_j = w_j (1 - s_j) g_j
  *   softmax:         dl_e = [e picked] w_e g_e - s_e sum_j w_j g_j   (every e)
- *  and 0 elsewhere. Only score, renorm and scale of the router are used. The
- *  logits' own producer goes on from here (x^T dlogits, dlogits wr^T).
+ *  and 0 elsewhere. Only score, renorm and scale of the router are used. A
+ *  pick whose id lies outside [0, E) takes no part either. The logits' own
+ *  producer goes on from here (x^T dlogits, dlogits wr^T): moe_route_bwd is
+ *  of moe_route's softmax and does not take these.
+ *  Both calls check the whole shape; emb and mlp are not used (64 will do).
  */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 typedef struct {

@@ -23,8 +23,8 @@ namespace {
 
 // Eight consecutive elements of a row per thread; four threads share a block, whose maximum takes two lane
 // exchanges. Bound by memory, so the source is read past the caches (it is not read again here) and the codes,
-// which the backward reads, are stored through them. 58.7 M bf16 values: 32 us, 5.5 TB/s; 100.7 M fp32 values:
-// 87 us, 5.8 TB/s.
+// which the backward reads, are stored through them. 58.7 M bf16 values: 33-34 us, 5.2-5.4 TB/s; 100.7 M fp32
+// values: 87 us, 5.8 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restrict__ src, int64_t n8,
                                                             int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -61,8 +61,8 @@ __global__ __launch_bounds__(256) void ckpt_quantize_kernel(const void* __restri
   }
 }
 
-// Bound by memory: 58.7 M values to bf16 in 28 us (6.4 TB/s, the codes partly from the Infinity Cache), 100.7 M
-// in 46 us.
+// Bound by memory: 58.7 M values to bf16 in 29 us (6.1 TB/s, the codes partly from the Infinity Cache), 100.7 M
+// in 48 us (6.4 TB/s).
 // Eight elements per thread of destination row r, from source row row_index[r] / row_div (clamped) or r.
 template <bool BF16>
 __global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __restrict__ codes,
@@ -101,8 +101,8 @@ __global__ __launch_bounds__(256) void ckpt_dequantize_kernel(const int8_t* __re
 // SwiGLU backward from the 8-bit h = [gate | up] of row r, LPR lanes a row (64 / LPR rows a wave), 8 columns a
 // lane and round. q = row_slot[r] (or r), w = slot_scale[q] (or 1), s = sigmoid(g):
 //   a = g s u,  dh = [w da u s (1 + g (1 - s)) | w da g s],  dslot_scale[q] = sum_m da a (a unrounded)
-// Bound by memory: 4 bytes read and 6 written a column; 262144 rows of 768 take 357 us, 5.7 TB/s. The outputs are read by other kernels much later and the
-// inputs not again: both go past the caches.
+// Bound by memory: 4 bytes read and 6 written a column; 262144 rows of 768 take 357-365 us, 5.6-5.7 TB/s by the
+// counters too. The outputs are read by other kernels much later and the inputs not again: both go past the caches.
 template <int LPR>
 __global__ __launch_bounds__(256) void swiglu_bwd_ckpt_kernel(int64_t M, int mlp, const uint16_t* __restrict__ da,
                                                               const int8_t* __restrict__ hc,

@@ -435,7 +435,7 @@ __global__ __launch_bounds__(GTHR, 1) void gemm_kernel(GemmP p) {
     // block), then one A copy of k-slice kt + NST; the B copies follow the last MFMA.
     // Issued as one burst after the barrier (the first form), a copying wave's eight
     // copies held back its MFMAs until the last of them was accepted. Measured,
-    // alternating on one box (32768-token workload, DeepSeek-V3 shape in brackets):
+    // alternating in one run (32768-token workload, DeepSeek-V3 shape in brackets):
     // GEMM1 1.463 -> 1.437 ms (4.66 -> 4.57), GEMM2 0.964 -> 0.954 (2.465 -> 2.43).
     // Spreading the B copies over the MFMAs as well, one per MFMA or across both
     // sub-slices, was slower than the burst form.
@@ -676,8 +676,8 @@ __global__ __launch_bounds__(GTHR, 1) void gemm_kernel(GemmP p) {
           // one block each, half in this lane and half in lane ^ 32. Codes go out as 32-byte row
           // segments through the staging block ([gate | up] x [32 rows][32 B]), the step bytes
           // straight (lanes 0-31 the gate's, 32-63 the up's).
-          // 32768 tokens, top 8, 128 experts, 2048 x 768: the forward takes 2.66-2.75 ms with this and x quantized,
-          // 3.05-3.10 with h in fp32 and the sorted rows kept, 2.43-2.50 with nothing kept.
+          // 32768 tokens, top 8, 128 experts, 2048 x 768: the forward takes 2.75-2.87 ms with this and x quantized,
+          // 3.13-3.25 with h in fp32 and the sorted rows kept, 2.54-2.80 with nothing kept.
           int sc8[2];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -1108,11 +1108,18 @@ __global__ __launch_bounds__(GTHR, 1) void wgrad_kernel(WgradP p) {
 // of kt + 3, and its barrier needs codes and steps kt + 2 and D kt + 1: one
 // iteration's copies (10 a copying wave) may still be in flight.
 //
-// What it takes: 262144 rows of 128 experts, 2048 x 1536: 1.60-1.65 ms, 1.0-1.03 PFLOP/s; wgrad_kernel on rows
-// already read back and sorted takes 1.49-1.53 ms, and reading them back 0.24 ms more. Bound, as wgrad_kernel is, by
-// several units at once: copies, fragment reads, an epilogue a tile, and here the conversion. 16384 rows of 32
-// experts, Zipf(1.1), 1024 x 1024: 63 us and 8-11 us of joining (bf16: 75 us and 10 of reading back).
-// 1500 rows of 12 experts, 256 x 384: 12.5 us, the latency of one tile on 24 workgroups.
+// What it takes, the join included: 262144 rows of 128 equal experts, 2048 x 1536: 1.64-1.80 ms, 0.92-1.0 PFLOP/s.
+// Timed in turn with it (1.71-1.75), wgrad_kernel on rows already read back and sorted takes 1.39-1.43 ms and reading
+// them back 0.25 ms more: 4 % less in all, for 1 GB of rows. Zipf(1.1) experts: 1.76-1.80 ms against 2.09-2.12 and 0.26.
+// 16384 rows of 32 experts, Zipf(1.1), 1024 x 1024: 72-76 us, 8-12 of them the join (bf16: 73-77 us and 9 of reading
+// back). 1500 rows of 12 experts, 256 x 384: 12.5 us, the latency of one tile on 24 workgroups. No one unit bounds
+// it: on the first of these loads the matrix cores are busy 49 % of the cycles (wgrad_kernel 70 %, at a clock that its
+// power pulls down to 1.4 GHz; this one runs at 1.9), LDS 26 %, a wave waits to issue for 40 % of its time and on
+// memory or a barrier for 24 %, and 1.8 TB/s pass the L2.
+//
+// The tile has one width. Columns past Q or P are copied and, but for whole 64-column waves past Q, multiplied: 65536
+// rows of 32 experts, 2048 x 128: 105 us, x 256: 120, x 512: 149, x 640: 231, x 1024: 283 (wgrad_kernel: 71, 74, 132,
+// 191, 259); 64, 128 and 192 x 1536: 74, 76, 76 us (56, 56, 58).
 //
 // Work list, made for skewed loads, which routers have in practice: the tiles are dealt longest first, in turns
 // of one a workgroup, every second turn backwards, a turn's neighbours (which share an expert's rows) to one XCD.
@@ -1164,7 +1171,10 @@ static_assert(sizeof(WgradCkptCuts) <= kCkCutBytes, "the list fits its place");
 constexpr int kCkPart = kCkP * kCkQ;  // floats of a partial tile
 constexpr int kCkMinCut = 12;         // k-slices below which an expert is not cut
 constexpr int kCkNoCut = 0x3fffffff;
-constexpr int kCkMinRows = 2048;      // rows in all below which none is
+// Rows in all below which none is cut and the joining launch (2 to 8 us) is saved. That pays where experts are many
+// and short: 11 experts, 1024 x 1024: 15.7 us at 2047 rows, 20.2 at 2048; four: 23.3 and 27.7. It does not for one long
+// expert, which the number of rows alone does not tell: 57.6 us at 2047 rows, 38.1 at 2048.
+constexpr int kCkMinRows = 2048;
 
 // An expert of ns k-slices in pieces of at most cut: their number and length (none is empty; an expert without
 // rows is one piece of none).
@@ -1231,7 +1241,7 @@ __device__ __forceinline__ void plan_sort(uint32_t (&key)[4], int n) {
 // k-slices: a tile takes 8 besides its own, one that leaves a partial tile 10, the joining launch 6 and 1/18 a
 // partial tile, fitted to 47 timings of lists of eight loads. Against a cut at half the mean load: 32768 rows of 16
 // experts, Zipf(1.1), 1024 x 1024, 128 -> 98 us; 16384 of 5, the same, 80 -> 65; 8192 of one, 2048 x 1536,
-// 101 -> 79; 262144 of 128, Zipf(1.1), 2048 x 1536, 1.80 -> 1.73 ms (one box; 1.67 -> 1.63 on a faster one); 16384
+// 101 -> 79; 262144 of 128, Zipf(1.1), 2048 x 1536, 1.80 -> 1.73 ms (in another run 1.67 -> 1.63); 16384
 // of 32, 1024 x 1024, and equal experts, the same. It adds about 1 us.
 __device__ __forceinline__ float plan_factor(int wave) {
   constexpr float f[7] = {0.6f, 0.9f, 1.1f, 1.25f, 1.5f, 2.5f, 4.0f};
@@ -1817,7 +1827,8 @@ hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int
   while ((uint64_t(1) << L) < (uint64_t)slot_div) ++L;
   const uint32_t mul = (uint32_t)((uint64_t(1) << (31 + L)) / (uint64_t)slot_div + 1);
   const dim3 grid(persistent_grid()), block(GTHR);
-  // with few rows the longest expert is short: not cut, and the second launch (5 us) is saved
+  // (the second launch goes out whether or not the plan cuts: 8192 rows of 128 experts, 1024 x 1024: 78 us, and 70
+  // without a workspace)
   const bool fits = ws && M >= kCkMinRows && ws_bytes >= kCkCutBytes + kCkPart * sizeof(float);
   const int64_t cap = fits ? std::min<int64_t>((ws_bytes - kCkCutBytes) / (kCkPart * sizeof(float)), 1 << 20) : 0;
   const WgradCkptP p{A_codes, A_scales, row_slot, D, group_offsets, C,   E,   (int)M,

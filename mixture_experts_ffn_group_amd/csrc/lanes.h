@@ -42,13 +42,6 @@ __device__ __forceinline__ float wave_sum(float v) {
 // 16-lane (row) reductions with symmetric exchanges: quad swaps, then the
 // half-row and row mirrors. Every lane combines its value with a partner's
 // in the same association, so all 16 lanes end with the identical result.
-__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
-  v = max(v, dpp_u32<0xb1, 0xf>(v));   // quad_perm [1,0,3,2]
-  v = max(v, dpp_u32<0x4e, 0xf>(v));   // quad_perm [2,3,0,1]
-  v = max(v, dpp_u32<0x141, 0xf>(v));  // row_half_mirror
-  v = max(v, dpp_u32<0x140, 0xf>(v));  // row_mirror
-  return v;
-}
 __device__ __forceinline__ float row_sum(float v) {
   v = v + __uint_as_float(dpp_u32<0xb1, 0xf>(__float_as_uint(v)));
   v = v + __uint_as_float(dpp_u32<0x4e, 0xf>(__float_as_uint(v)));

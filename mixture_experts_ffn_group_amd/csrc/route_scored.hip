@@ -223,6 +223,10 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteP p, const V* __
 // bias, 4 of 8 groups: 9.8 us (40 us), softmax, 13 to 17 us; 4 tokens x 256:
 // 6.0 us (18 us), the latency of one wave. Their logits alone, at a copy's
 // rate, take 4.0 and 1.9 us.
+//
+// "Out of the integers' range" is |c| >= 1.99 for any enabled expert of the row, picked or not: with a bias that
+// puts one there, or a soft mask of -1e4 on one expert, every row goes to the 64-bit form: 8192 x 256 in groups 9.7 ->
+// 62 to 81 us. (An expert disabled by a bias of -inf costs nothing.)
 constexpr int kHalf28 = 1 << 27;
 
 template <class V, int N>
@@ -529,7 +533,7 @@ __global__ __launch_bounds__(256) void route_scored16_kernel(RouteP p, const V* 
     }
     const uint64_t flags = __ballot(flag);
     const bool slow = ((flags >> (16 * g)) & 0xffffull) != 0;
-    // weights in 64 bits
+    // weights in 64 bits (the softmax's sum over all experts: 32-bit exponentials added in 64)
     double s[NP], tot = 0.0;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -775,8 +779,9 @@ hipError_t launch_route_scored(int64_t T, int E, int k, int score, int n_group, 
   const bool groups = topk_group < n_group;
   const bool choice = bias != nullptr || (groups && group_top == 2);
   // k <= 32: one or two picks a lane; groups: one a lane, of whole runs of four experts. The rest takes the 64-bit
-  // form, three to five times as long (figures above; k = 24, 32768 x 128, softmax: 110 us against 19, and with a
-  // bias, where close values are frequent, 107 against 43).
+  // form, three to nine times as long (figures above; k = 24, 32768 x 128, softmax: 110 us against 17.5, and with a
+  // bias, where close values are frequent, 107 against 54; k = 33: 140; 32768 x 60, k = 4: 6.2 us without groups, 57
+  // and 46 with 4 and 10, of 15 and 6 experts; 8192 x 256 with 32 groups: 29).
   if (k <= 32 && (!groups || (n_group <= 16 && (E / n_group) % 4 == 0))) {
     if (logits_bf16) {
       const uint16_t* l = static_cast<const uint16_t*>(logits);
