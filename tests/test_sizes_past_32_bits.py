@@ -21,7 +21,7 @@ def test_layer_shapes(i, v):
         moe.query_support(*sizes)
 
 
-def test_shapes_that_fit_are_the_library_s_to_judge():
+def test_shapes_that_fit_go_to_the_library():
     assert _lib.shape(B, B // 2 - 1, 64, 8, 2).emb == B // 2 - 1  # T has 64 bits
     assert _lib.shape(1, 64, 64, 8, -B // 2).k == -B // 2
     for k in (0, -1, 9):
