@@ -591,6 +591,110 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* shape, const moe_bf16_t* dy, const float
                      const moe_bf16_t* wi, const moe_bf16_t* wo, moe_bf16_t* dx, moe_bf16_t* dwi, moe_bf16_t* dwo,
                      float* dtopk_w, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * moe_ffn_fwd_few -- the whole layer for a few tokens (a decode step), T <= 64:
+ *  router, experts and combine in four kernels (two on a given routing) that read the weights of
+ *  each expert that has a token once, with no permute and no copy of rows.
+ *  wr [emb, E] fp32: the layer routes x itself; bias [E] fp32 or NULL (may
+ *  hold -inf to disable an expert); topk_idx [T, k] int32 and topk_w [T, k]
+ *  fp32 are outputs: the k largest of the logits x . wr + bias in descending
+ *  order, ties to the lower id, and their softmax. Logits are summed and
+ *  compared in 64 bits (moe_route's are a chain of fp32 additions, so that
+ *  picks may differ where two logits lie within its rounding). A NaN logit
+ *  counts as -inf; a pick of logit -inf has weight 0.
+ *  wr NULL: topk_idx and topk_w are inputs (from moe_route, moe_route_scored
+ *  or the caller), bias is NULL. A pick whose id lies outside [0, E) takes no
+ *  part. An expert may be picked twice by a token here.
+ *  wi [E, emb, 2*mlp], wo [E, mlp, emb] bf16; y [T, emb] bf16 =
+ *  sum_j topk_w[t, j] (silu(x wi_e[:, :mlp]) * (x wi_e[:, mlp:])) wo_e,
+ *  summed in fp32, the SwiGLU output kept to 16 bits, y rounded once.
+ *  ws: at least moe_workspace_bytes_few(shape) bytes (0: unsupported shape).
+ *
+ * moe_ffn_fwd_few_mx -- the same on MXFP8 weights (wi_codes, wi_scales, wo_codes and
+ *  wo_scales as in moe_ffn_fwd_mx). x and the SwiGLU output are not
+ *  quantized, the weights enter at the values their codes stand for, and sums
+ *  are fp32, so the result differs from moe_ffn_fwd_mx's by that one's
+ *  activation quantization. Scale codes above 246 (weights past 2^119) are unspecified.
+ */
+size_t moe_workspace_bytes_few(const moe_shape_t* shape);
+int moe_ffn_fwd_few(const moe_shape_t* shape, const moe_bf16_t* x, const float* wr, const float* bias,
+                    int32_t* topk_idx, float* topk_w, const moe_bf16_t* wi, const moe_bf16_t* wo, moe_bf16_t* y,
+                    void* ws, size_t ws_bytes, moe_stream_t stream);
+int moe_ffn_fwd_few_mx(const moe_shape_t* shape, const moe_bf16_t* x, const float* wr, const float* bias,
+                       int32_t* topk_idx, float* topk_w, const uint8_t* wi_codes, const uint8_t* wi_scales,
+                       const uint8_t* wo_codes, const uint8_t* wo_scales, moe_bf16_t* y, void* ws, size_t ws_bytes,
+                       moe_stream_t stream);
+
+/*
+ * The norms around the layer, N(v; w) = v * r(v) * (offset + w) with
+ * r(v) = (mean(v^2) + eps)^-1/2 over a row (w NULL: v * r(v)). Rows have emb
+ * elements, emb % 8 == 0, 8 <= emb <= 16384; 0 <= T < 2^31. Sums are fp32: the
+ * squares of a row must not overflow. weight_type, x_type: MOE_F32 or
+ * MOE_BF16. eps > 0.
+ *
+ * moe_norm -- y [T, emb] bf16 = N(x; weight), x [T, emb] of x_type, weight [emb]
+ *  of weight_type or NULL: the layer's input from the residual stream.
+ *
+ * moe_norm_bwd -- from dy [T, emb] bf16: dx [T, emb] = dres + the gradient of
+ *  x (dres of x_type or NULL; dx of x_type, may be dres itself);
+ *  dweight [emb] fp32 = sum_t dy x r(x) (NULL: not wanted).
+ *  ws: at least moe_norm_bwd_workspace_bytes(T, emb) bytes; without dweight none.
+ *  The order of the sums over rows depends on T and emb alone.
+ */
+int moe_norm(int64_t T, int32_t emb, const void* x, int32_t x_type, const void* weight, int32_t weight_type,
+             float offset, float eps, moe_bf16_t* y, moe_stream_t stream);
+size_t moe_norm_bwd_workspace_bytes(int64_t T, int32_t emb);
+int moe_norm_bwd(int64_t T, int32_t emb, const moe_bf16_t* dy, const void* x, int32_t x_type, const void* weight,
+                 int32_t weight_type, float offset, float eps, const void* dres, void* dx, float* dweight, void* ws,
+                 size_t ws_bytes, moe_stream_t stream);
+
+/* How the layer's output joins the residual stream (moe_block_out). */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };
+typedef struct {
+  int32_t x_type;          /* MOE_F32 or MOE_BF16: the residual stream (res, out, dout, dres) */
+  int32_t weight_type;     /* of post_weight and next_weight */
+  int32_t gate_mode;       /* MOE_GATE_*: gate is [emb] (CHANNEL), [T] (TOKEN) or [T, emb] (FULL) */
+  int32_t gate_type;       /* MOE_F32 or MOE_BF16 */
+  int32_t post;            /* nonzero: a norm after the layer */
+  float offset, eps;       /* of both norms */
+  float scale, res_scale;  /* finite */
+  const void* post_weight; /* [emb] or NULL; NULL without post */
+  const void* next_weight; /* [emb] or NULL: of the next norm */
+  const void* gate;        /* NULL for MOE_GATE_NONE */
+} moe_block_t;
+
+/*
+ * moe_block_out -- what follows the layer in a transformer block:
+ *   out = res_scale * res + scale * gate * z, z = N(y; post_weight) or y,
+ *   xn  = N(out; next_weight), the next layer's input (NULL: not wanted),
+ *  with gate broadcast over rows or columns. out and res [T, emb] of x_type
+ *  (out may be res itself), xn bf16; xn is taken from out before its rounding.
+ *  y [T, emb] bf16, or NULL: then y[t] = sum_j topk_w[t, j] ys[slot_row[t*k + j]]
+ *  as in moe_combine (1 <= k <= 64, ys [T*k, emb] bf16, topk_w NULL: unit
+ *  weights), not rounded before its use; y_out [T, emb] bf16 or NULL receives
+ *  its rounded values, which the backward takes. A slot_row outside [0, T*k)
+ *  adds nothing. With y given, ys, slot_row, topk_w and y_out are NULL.
+ *
+ * moe_block_out_bwd -- from dout [T, emb] of x_type (NULL: 0) and dxn [T, emb] bf16
+ *  (NULL: xn took no part; then out is NULL too), at y as above and the stored
+ *  out [T, emb], d = dout + the gradient of out through xn:
+ *   dres = res_scale * d                    x_type, may be dout itself
+ *   dy                                      bf16: through z, from scale * gate * d
+ *   dpost_weight, dnext_weight              fp32 [emb]
+ *   dgate = scale * d * z, summed over the gate's broadcast axis: fp32 [emb]
+ *           (CHANNEL), fp32 [T] (TOKEN), [T, emb] of gate_type (FULL)
+ *  each NULL if not wanted. y may be NULL where neither post nor a gate needs it.
+ *  ws: at least moe_block_out_bwd_workspace_bytes(T, emb) bytes, where a column
+ *  sum (dpost_weight, dnext_weight, a CHANNEL dgate) is wanted.
+ */
+int moe_block_out(int64_t T, int32_t emb, const moe_block_t* block, const void* res, const moe_bf16_t* y, int32_t k,
+                  const moe_bf16_t* ys, const int32_t* slot_row, const float* topk_w, void* out, moe_bf16_t* xn,
+                  moe_bf16_t* y_out, moe_stream_t stream);
+size_t moe_block_out_bwd_workspace_bytes(int64_t T, int32_t emb);
+int moe_block_out_bwd(int64_t T, int32_t emb, const moe_block_t* block, const void* dout, const moe_bf16_t* y,
+                      const void* out, const moe_bf16_t* dxn, void* dres, moe_bf16_t* dy, float* dpost_weight,
+                      float* dnext_weight, void* dgate, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,9 @@ the C ABI in include/moe_ffn.h:
     activations kept in 8 bits between the passes
     ffn_fwd_routed, ffn_bwd_ckpt: the layer on a given routing, and its
     backward from the 8-bit saved set
+    ffn_fwd_few, ffn_fwd_few_mx: the layer for a few tokens (a decode step)
+    norm, norm_bwd, block_out, block_out_bwd: the norms around the layer, with
+    the gate and the residual sum
 
 Tensors: bf16 activations/weights, fp32 router weights/logits/top-k weights,
 int32 indices, all contiguous and on one CUDA (HIP) device.
@@ -30,7 +33,8 @@ from ._lib import (MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_BWD, MOE_NN, MOE
 
 __all__ = ["route", "permute", "grouped_gemm", "grouped_gemm_wgrad", "combine", "combine_bwd", "ffn_fwd", "ffn_bwd",
            "route_scored", "route_scored_bwd", "ckpt_quantize", "ckpt_dequantize", "swiglu_bwd_ckpt",
-           "grouped_gemm_wgrad_ckpt", "ffn_fwd_routed", "ffn_bwd_ckpt", "query_support", "workspace_bytes", "MoeError"]
+           "grouped_gemm_wgrad_ckpt", "ffn_fwd_routed", "ffn_bwd_ckpt",
+           "ffn_fwd_few", "ffn_fwd_few_mx", "norm", "norm_bwd", "block_out", "block_out_bwd", "query_support", "workspace_bytes", "MoeError"]
 
 _EPI = {"none": MOE_EPI_NONE, "swiglu": MOE_EPI_SWIGLU, "swiglu_bwd": MOE_EPI_SWIGLU_BWD}
 _OP = {"nn": MOE_NN, "nt": MOE_NT}
@@ -745,3 +749,238 @@ def workspace_bytes_routed(T: int, emb: int, mlp: int, E: int, k: int, backward:
     """Workspace bytes of ffn_fwd_routed, or of ffn_bwd_ckpt with backward."""
     s = _lib.shape(T, emb, mlp, E, k)
     return int(_lib.lib().moe_workspace_bytes_routed(C.byref(s), int(backward)))
+
+
+FEW_MAX_TOKENS = 64  # most tokens of ffn_fwd_few and ffn_fwd_few_mx
+
+
+@functools.lru_cache(maxsize=256)
+def _few_plan(T, emb, mlp, E, k):
+    """The shape structure and the workspace bytes of a few-token call."""
+    s = _lib.shape(T, emb, mlp, E, k)
+    n = int(_lib.lib().moe_workspace_bytes_few(C.byref(s)))
+    return C.byref(s), n
+
+
+def workspace_bytes_few(T: int, emb: int, mlp: int, E: int, k: int) -> int:
+    """Workspace bytes of ffn_fwd_few and ffn_fwd_few_mx (0: unsupported shape)."""
+    return _few_plan(T, emb, mlp, E, k)[1]
+
+
+def _few(fn, x, weights, mlp, E, k, wr, bias, topk_idx, topk_w, workspace, out):
+    dev = x.device
+    T, emb = x.shape
+    if wr is not None:
+        if topk_idx is not None or topk_w is not None:
+            raise ValueError("either wr or topk_idx and topk_w must be given, not both")
+        if k is None:
+            raise ValueError("k is missing")
+        k = operator.index(k)
+        _need_like(wr, "wr", (emb, E), torch.float32, dev)
+        _need_like(bias, "bias", (E,), torch.float32, dev)
+        topk_idx = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+        topk_w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    else:
+        if topk_idx is None or topk_w is None:
+            raise ValueError("wr, or topk_idx and topk_w, must be given")
+        if bias is not None:
+            raise ValueError("bias is the router's: with topk_idx and topk_w it must be None")
+        _need_rank2(topk_idx, "topk_idx", torch.int32, dev)
+        if k is not None and k != topk_idx.shape[1]:
+            raise ValueError(f"k is {k}, topk_idx has {topk_idx.shape[1]} picks")
+        k = topk_idx.shape[1]
+        _need_like(topk_idx, "topk_idx", (T, k), torch.int32, dev)
+        _need_like(topk_w, "topk_w", (T, k), torch.float32, dev)
+    _need_like(out, "out", (T, emb), torch.bfloat16, dev)
+    s, n = _few_plan(T, emb, mlp, E, k)
+    ws = _workspace(workspace, n, dev)
+    y = out if out is not None else torch.empty((T, emb), dtype=torch.bfloat16, device=dev)
+    _call(fn, dev, s, x, wr, bias, topk_idx, topk_w, *weights, y, ws, ws.numel())
+    return y, topk_idx, topk_w
+
+
+def ffn_fwd_few(x: torch.Tensor, wi: torch.Tensor, wo: torch.Tensor, k: int | None = None,
+                wr: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                topk_idx: torch.Tensor | None = None, topk_w: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """The whole layer for a few tokens, at most FEW_MAX_TOKENS (see moe_ffn_fwd_few): (y [T, emb] bf16, topk_idx
+    [T, k] int32, topk_w [T, k] fp32). Either k and wr [emb, E] fp32 (+ bias [E] fp32), or a routing topk_idx,
+    topk_w, which then comes back as it is. workspace: uint8 of at least workspace_bytes_few(...) bytes."""
+    _need_rank2(x, "x", torch.bfloat16, None)
+    E, mlp = _layer_sizes(wi, wo, x.shape[1], x.device)
+    return _few("moe_ffn_fwd_few", x, (wi, wo), mlp, E, k, wr, bias, topk_idx, topk_w, workspace, out)
+
+
+def ffn_fwd_few_mx(x: torch.Tensor, wq: dict, k: int | None = None, wr: torch.Tensor | None = None,
+                   bias: torch.Tensor | None = None, topk_idx: torch.Tensor | None = None,
+                   topk_w: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None):
+    """ffn_fwd_few on MXFP8 weights wq from mx_quantize_expert_weights (see moe_ffn_fwd_few_mx): x and the SwiGLU
+    output are not quantized."""
+    _need_rank2(x, "x", torch.bfloat16, None)
+    dev, emb, mlp = x.device, x.shape[1], operator.index(wq["mlp"])
+    _need(wq["wi_codes"], "wi_codes", torch.uint8, dev)
+    E = wq["wi_codes"].shape[0]
+    for n, shape in (("wi_codes", (E, 2 * mlp, emb)), ("wi_scales", (E, emb // 64, 2 * mlp, 4)),
+                     ("wo_codes", (E, emb, mlp)), ("wo_scales", (E, mlp // 64, emb, 4))):
+        if wq[n] is None:
+            raise ValueError(f"{n} is missing")
+        _need_like(wq[n], n, shape, torch.uint8, dev)
+    return _few("moe_ffn_fwd_few_mx", x, (wq["wi_codes"], wq["wi_scales"], wq["wo_codes"], wq["wo_scales"]), mlp, E, k,
+                wr, bias, topk_idx, topk_w, workspace, out)
+
+
+def _weight_type(t, name, emb, dev):
+    """MOE_* type of a norm's weight [emb] (fp32 without one)."""
+    if t is None:
+        return _lib.MOE_F32
+    ty = _need_typed(t, name, 1)
+    _need_like(t, name, (emb,), t.dtype, dev)
+    return ty
+
+
+def norm(x: torch.Tensor, weight: torch.Tensor | None = None, offset: float = 0.0, eps: float = 1e-6,
+         out: torch.Tensor | None = None) -> torch.Tensor:
+    """x / sqrt(mean(x^2) + eps) * (offset + weight) over rows [T, emb] fp32 or bf16, as bf16 (see moe_norm);
+    weight [emb] fp32 or bf16, or None."""
+    ty = _need_typed(x, "x", 2)
+    dev = x.device
+    T, emb = x.shape
+    _lib.need_32_bits(emb, "emb")
+    wt = _weight_type(weight, "weight", emb, dev)
+    _need_like(out, "out", (T, emb), torch.bfloat16, dev)
+    y = out if out is not None else torch.empty((T, emb), dtype=torch.bfloat16, device=dev)
+    _call("moe_norm", dev, T, emb, x, ty, weight, wt, offset, eps, y)
+    return y
+
+
+def norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = None, offset: float = 0.0,
+             eps: float = 1e-6, dres: torch.Tensor | None = None, want_dweight: bool = True,
+             workspace: torch.Tensor | None = None):
+    """Gradients of norm from dy [T, emb] bf16 (see moe_norm_bwd): (dx of x's type, dweight [emb] fp32 or None).
+    dres, of x's type, is the gradient that reaches x on the residual stream: it is added."""
+    ty = _need_typed(x, "x", 2)
+    dev = x.device
+    T, emb = x.shape
+    _lib.need_32_bits(emb, "emb")
+    wt = _weight_type(weight, "weight", emb, dev)
+    if dy is None:
+        raise ValueError("dy is missing")
+    _need_like(dy, "dy", (T, emb), torch.bfloat16, dev)
+    _need_like(dres, "dres", (T, emb), x.dtype, dev)
+    dx = torch.empty_like(x)
+    dw = ws = None
+    if weight is not None and want_dweight:
+        dw = torch.empty(emb, dtype=torch.float32, device=dev)
+        ws = _workspace(workspace, int(_lib.lib().moe_norm_bwd_workspace_bytes(T, emb)), dev)
+    _call("moe_norm_bwd", dev, T, emb, dy, x, ty, weight, wt, offset, eps, dres, dx, dw, ws,
+          0 if ws is None else ws.numel())
+    return dx, dw
+
+
+def _block(x_type, T, emb, dev, post_norm, post_weight, gate, scale, res_scale, next_weight, offset, eps):
+    """The structure of a block_out call, and the gate's mode."""
+    _lib.need_32_bits(emb, "emb")
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight without post_norm")
+    wt = _weight_type(post_weight, "post_weight", emb, dev)
+    nt = _weight_type(next_weight, "next_weight", emb, dev)
+    if post_weight is not None and next_weight is not None and wt != nt:
+        raise TypeError("post_weight and next_weight must have one type")
+    mode, gt = _lib.MOE_GATE_NONE, _lib.MOE_F32
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        gt = _need_typed(gate, "gate", 1 if gate.dim() == 1 else 2)
+        shape = tuple(gate.shape)
+        mode = {(emb,): _lib.MOE_GATE_CHANNEL, (T, 1): _lib.MOE_GATE_TOKEN, (T, emb): _lib.MOE_GATE_FULL}.get(shape)
+        if mode is None:
+            raise ValueError(f"gate must have shape ({emb},), ({T}, 1) or ({T}, {emb}), got {shape}")
+        _need_like(gate, "gate", shape, gate.dtype, dev)
+    p = [None if t is None else t.data_ptr() for t in (post_weight, next_weight, gate)]
+    return C.byref(_lib.MoeBlock(x_type, nt if post_weight is None else wt, mode, gt, int(bool(post_norm)), offset,
+                                 eps, scale, res_scale, *p)), mode
+
+
+def block_out(res: torch.Tensor, y: torch.Tensor | None = None, ys: torch.Tensor | None = None,
+              slot_row: torch.Tensor | None = None, topk_w: torch.Tensor | None = None, post_norm: bool = False,
+              post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None, scale: float = 1.0,
+              res_scale: float = 1.0, next_norm: bool = False, next_weight: torch.Tensor | None = None,
+              offset: float = 0.0, eps: float = 1e-6, want_y: bool = False, out: torch.Tensor | None = None) -> dict:
+    """What follows the layer in a block (see moe_block_out): dict(out = res_scale * res + scale * gate * z, of res's
+    type; xn = norm(out) bf16 with next_norm, else None; y bf16 with want_y, else None), z = norm(y) with post_norm,
+    else y. The layer's output is y [T, emb] bf16, or the weighted sum of its expert rows ys [T*k, emb] through
+    slot_row [T*k] and topk_w [T, k] (as combine). gate: [emb], [T, 1] or [T, emb], fp32 or bf16. out may be res."""
+    ty = _need_typed(res, "res", 2)
+    dev = res.device
+    T, emb = res.shape
+    if next_weight is not None and not next_norm:
+        raise ValueError("next_weight without next_norm")
+    b, _ = _block(ty, T, emb, dev, post_norm, post_weight, gate, float(scale), float(res_scale), next_weight,
+                  float(offset), float(eps))
+    k = 0
+    if y is not None:
+        if ys is not None or slot_row is not None or topk_w is not None or want_y:
+            raise ValueError("either y or ys, slot_row and topk_w must be given, not both (nor want_y with y)")
+        _need_like(y, "y", (T, emb), torch.bfloat16, dev)
+    else:
+        if ys is None or slot_row is None or topk_w is None:
+            raise ValueError("y, or ys, slot_row and topk_w, must be given")
+        _need_rank2(topk_w, "topk_w", torch.float32, dev)
+        k = topk_w.shape[1]
+        _need_like(topk_w, "topk_w", (T, k), torch.float32, dev)
+        _need_like(ys, "ys", (T * k, emb), torch.bfloat16, dev)
+        _need_like(slot_row, "slot_row", (T * k,), torch.int32, dev)
+    _need_like(out, "out", (T, emb), res.dtype, dev)
+    o = out if out is not None else torch.empty_like(res)
+    xn = torch.empty((T, emb), dtype=torch.bfloat16, device=dev) if next_norm else None
+    yo = torch.empty((T, emb), dtype=torch.bfloat16, device=dev) if want_y else None
+    _call("moe_block_out", dev, T, emb, b, res, y, k, ys, slot_row, topk_w, o, xn, yo)
+    return dict(out=o, xn=xn, y=yo)
+
+
+def block_out_bwd(dout: torch.Tensor | None, y: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  dxn: torch.Tensor | None = None, post_norm: bool = False, post_weight: torch.Tensor | None = None,
+                  gate: torch.Tensor | None = None, scale: float = 1.0, res_scale: float = 1.0,
+                  next_norm: bool = False, next_weight: torch.Tensor | None = None, offset: float = 0.0,
+                  eps: float = 1e-6, need=("dres", "dy", "dpost_weight", "dgate", "dnext_weight"),
+                  workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of block_out (see moe_block_out_bwd) from dout (of the residual's type, or None) and, with next_norm,
+    dxn [T, emb] bf16 at the stored out: dict of dres, dy, dpost_weight, dgate, dnext_weight, None where not needed or
+    not there. y as given to, or returned by, block_out. dgate: fp32 for a gate [emb] or [T, 1], else the gate's
+    type."""
+    lead = out if out is not None else dout
+    if lead is None:
+        raise ValueError("dout, or dxn and out, must be given")
+    ty = _need_typed(lead, "dout" if out is None else "out", 2)
+    dev = lead.device
+    T, emb = lead.shape
+    if next_norm != (dxn is not None) or next_norm != (out is not None):
+        raise ValueError("next_norm goes with dxn and out")
+    if next_weight is not None and not next_norm:
+        raise ValueError("next_weight without next_norm")
+    b, mode = _block(ty, T, emb, dev, post_norm, post_weight, gate, float(scale), float(res_scale), next_weight,
+                     float(offset), float(eps))
+    _need_like(dout, "dout", (T, emb), lead.dtype, dev)
+    _need_like(dxn, "dxn", (T, emb), torch.bfloat16, dev)
+    if y is None and (post_norm or gate is not None):
+        raise ValueError("y is missing")
+    _need_like(y, "y", (T, emb), torch.bfloat16, dev)
+
+    def new(name, have, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=dev) if have and name in need else None
+
+    f32 = torch.float32
+    dres = new("dres", True, (T, emb), lead.dtype)
+    dy = new("dy", True, (T, emb), torch.bfloat16)
+    dpw = new("dpost_weight", post_weight is not None, (emb,), f32)
+    dnw = new("dnext_weight", next_weight is not None, (emb,), f32)
+    dgate = None
+    if gate is not None:
+        dgate = new("dgate", True, tuple(gate.shape), gate.dtype if mode == _lib.MOE_GATE_FULL else f32)
+    ws = None
+    if dpw is not None or dnw is not None or (dgate is not None and mode == _lib.MOE_GATE_CHANNEL):
+        ws = _workspace(workspace, int(_lib.lib().moe_block_out_bwd_workspace_bytes(T, emb)), dev)
+    _call("moe_block_out_bwd", dev, T, emb, b, dout, y, out, dxn, dres, dy, dpw, dnw, dgate, ws,
+          0 if ws is None else ws.numel())
+    return dict(dres=dres, dy=dy, dpost_weight=dpw, dgate=dgate, dnext_weight=dnw)

@@ -20,11 +20,12 @@ MOE_NN, MOE_NT = 0, 1
 MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_BWD = 0, 1, 2
 MOE_F32, MOE_BF16 = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 MOE_SCHED_GEMM, MOE_SCHED_GEMM_SWIGLU, MOE_SCHED_WGRAD = 0, 1, 2
 
 # Every function the header declares, with its ctypes signature.
 _p = C.c_void_p
-_i32, _i64, _sz = C.c_int32, C.c_int64, C.c_size_t
+_i32, _i64, _sz, _f32 = C.c_int32, C.c_int64, C.c_size_t, C.c_float
 
 
 class MoeShape(C.Structure):
@@ -51,7 +52,14 @@ class MoeRouter(C.Structure):
                [("scale", C.c_float)]
 
 
+class MoeBlock(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("x_type", "weight_type", "gate_mode", "gate_type", "post")] + \
+               [(n, C.c_float) for n in ("offset", "eps", "scale", "res_scale")] + \
+               [(n, C.c_void_p) for n in ("post_weight", "next_weight", "gate")]
+
+
 _SHP = C.POINTER(MoeShape)
+_BLK = C.POINTER(MoeBlock)
 _RTR = C.POINTER(MoeRouter)
 SIGNATURES = {
     "moe_status_str": ([C.c_int], C.c_char_p),
@@ -93,6 +101,15 @@ SIGNATURES = {
     "moe_ffn_fwd_routed": ([_SHP, _p, _p, _p, _p, _p, _p, C.POINTER(MoeSaved), C.POINTER(MoeSaved8), _p, _sz, _p],
                            C.c_int),
     "moe_ffn_bwd_ckpt": ([_SHP, _p, _p, C.POINTER(MoeSaved8), _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
+    "moe_workspace_bytes_few": ([_SHP], _sz),
+    "moe_ffn_fwd_few": ([_SHP, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
+    "moe_ffn_fwd_few_mx": ([_SHP, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
+    "moe_norm": ([_i64, _i32, _p, _i32, _p, _i32, _f32, _f32, _p, _p], C.c_int),
+    "moe_norm_bwd_workspace_bytes": ([_i64, _i32], _sz),
+    "moe_norm_bwd": ([_i64, _i32, _p, _p, _i32, _p, _i32, _f32, _f32, _p, _p, _p, _p, _sz, _p], C.c_int),
+    "moe_block_out": ([_i64, _i32, _BLK, _p, _p, _i32, _p, _p, _p, _p, _p, _p, _p], C.c_int),
+    "moe_block_out_bwd_workspace_bytes": ([_i64, _i32], _sz),
+    "moe_block_out_bwd": ([_i64, _i32, _BLK, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
     "moe_route_bwd": ([_SHP, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p], C.c_int),
 }
 

@@ -92,4 +92,34 @@ hipError_t launch_wgrad_ckpt(const int8_t* A_codes, const uint8_t* A_scales, int
                              int slot_div, const uint16_t* D, const int32_t* group_offsets, int E, int64_t M, int P,
                              int Q, uint16_t* C, void* ws, size_t ws_bytes, hipStream_t stream);
 
+// The layer for a few tokens (few.hip). T <= kFewMaxTokens; wr NULL: topk_idx and topk_w are given.
+constexpr int kFewMaxTokens = 64;
+struct FewWeights {
+  const uint16_t *wi, *wo;               // bf16 [E, emb, 2*mlp], [E, mlp, emb], or NULL:
+  const uint8_t *wic, *wis, *woc, *wos;  // MXFP8 codes [E, N, K] and scales [E][K/64][N][4]
+};
+size_t few_workspace(int64_t T, int emb, int mlp, int E, int k);
+hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t* x, const float* wr, const float* bias,
+                      int32_t* topk_idx, float* topk_w, const FewWeights& wt, uint16_t* y, void* ws,
+                      hipStream_t stream);
+
+// The norms around the layer (norm.hip). emb <= kNormMaxEmb, a multiple of 8.
+constexpr int kNormMaxEmb = 16384;
+enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
+struct BlockArgs {
+  bool x_f32, w_f32, gate_f32, post;
+  int gate_mode;
+  float offset, eps, scale, res_scale;
+  const void *post_weight, *next_weight, *gate;
+};
+// y and ys NULL: the norm of res alone, into xn. xn NULL: no next norm.
+hipError_t launch_block_out(int64_t T, int emb, const BlockArgs& b, const void* res, const uint16_t* y, int k,
+                            const uint16_t* ys, const int32_t* slot_row, const float* topk_w, void* out, uint16_t* xn,
+                            uint16_t* y_out, hipStream_t st);
+// part NULL: no column sums. `sums`: how many the call can take (next norm, post norm, channel gate). has_y false: the next norm's gradient alone.
+size_t block_bwd_workspace(int64_t T, int emb, int sums);
+hipError_t launch_block_out_bwd(int64_t T, int emb, const BlockArgs& b, bool has_y, const void* dout, const uint16_t* y,
+                                const void* out, const uint16_t* dxn, void* dres, uint16_t* dy, float* dpost,
+                                float* dnext, void* dgate, float* part, hipStream_t st);
+
 }  // namespace moe

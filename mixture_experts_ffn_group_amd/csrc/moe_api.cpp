@@ -1099,4 +1099,239 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* s, const moe_bf16_t* dy, const float* to
   return MOE_OK;
 }
 
+// ---- the layer for a few tokens
+
+static int check_few(const moe_shape_t* s) {
+  if (int rc = check_shape(s)) return rc;
+  if (s->T > moe::kFewMaxTokens)
+    return fail(MOE_ERR_UNSUPPORTED, "T (%lld) > %d tokens", (long long)s->T, moe::kFewMaxTokens);
+  return MOE_OK;
+}
+
+size_t moe_workspace_bytes_few(const moe_shape_t* shape) {
+  if (check_few(shape) != MOE_OK) return 0;
+  return moe::few_workspace(shape->T, shape->emb, shape->mlp, shape->E, shape->k);
+}
+
+static int few(const char* what, const moe_shape_t* s, const moe_bf16_t* x, const float* wr, const float* bias,
+               int32_t* topk_idx, float* topk_w, const moe::FewWeights& wt, moe_bf16_t* y, void* ws, size_t ws_bytes,
+               moe_stream_t stream) {
+  if (s->T == 0) return MOE_OK;
+  NEED(x);
+  MAYBE(wr);
+  MAYBE(bias);
+  if (bias && !wr) return fail(MOE_ERR_SHAPE, "bias without wr: the routing is given");
+  NEED(topk_idx);
+  NEED(topk_w);
+  NEED(y);
+  NEED_WS(moe::few_workspace(s->T, s->emb, s->mlp, s->E, s->k));
+  return hip_status(moe::launch_few(s->T, s->emb, s->mlp, s->E, s->k, x, wr, bias, topk_idx, topk_w, wt, y, ws,
+                                    (hipStream_t)stream),
+                    what);
+}
+
+int moe_ffn_fwd_few(const moe_shape_t* s, const moe_bf16_t* x, const float* wr, const float* bias, int32_t* topk_idx,
+                    float* topk_w, const moe_bf16_t* wi, const moe_bf16_t* wo, moe_bf16_t* y, void* ws,
+                    size_t ws_bytes, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_few(s)) return rc;
+  if (s->T > 0) {
+    NEED(wi);
+    NEED(wo);
+  }
+  moe::FewWeights wt{};
+  wt.wi = wi;
+  wt.wo = wo;
+  return few("moe_ffn_fwd_few", s, x, wr, bias, topk_idx, topk_w, wt, y, ws, ws_bytes, stream);
+}
+
+int moe_ffn_fwd_few_mx(const moe_shape_t* s, const moe_bf16_t* x, const float* wr, const float* bias,
+                       int32_t* topk_idx, float* topk_w, const uint8_t* wi_codes, const uint8_t* wi_scales,
+                       const uint8_t* wo_codes, const uint8_t* wo_scales, moe_bf16_t* y, void* ws, size_t ws_bytes,
+                       moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_few(s)) return rc;
+  if (s->T > 0) {
+    NEED(wi_codes);
+    NEED(wi_scales);
+    NEED(wo_codes);
+    NEED(wo_scales);
+  }
+  moe::FewWeights wt{};
+  wt.wic = wi_codes;
+  wt.wis = wi_scales;
+  wt.woc = wo_codes;
+  wt.wos = wo_scales;
+  return few("moe_ffn_fwd_few_mx", s, x, wr, bias, topk_idx, topk_w, wt, y, ws, ws_bytes, stream);
+}
+
+// ---- the norms around the layer
+
+static int check_rows(int64_t T, int32_t emb) {
+  if (T < 0 || emb <= 0) return fail(MOE_ERR_SHAPE, "need T >= 0 and emb > 0");
+  if (emb % 8) return fail(MOE_ERR_UNSUPPORTED, "emb (%d) is not a multiple of 8", emb);
+  if (emb > moe::kNormMaxEmb) return fail(MOE_ERR_UNSUPPORTED, "emb (%d) > %d", emb, moe::kNormMaxEmb);
+  if (T >= int64_t(1) << 31) return fail(MOE_ERR_UNSUPPORTED, "T >= 2^31");
+  return MOE_OK;
+}
+
+static int check_norm(float offset, float eps) {
+  if (!std::isfinite(offset)) return fail(MOE_ERR_SHAPE, "offset must be finite");
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_SHAPE, "eps must be finite and > 0");
+  return MOE_OK;
+}
+
+static int check_block(const moe_block_t* b) {
+  if (!b) return fail(MOE_ERR_NULL, "block is NULL");
+  if (int rc = check_type("x_type", b->x_type)) return rc;
+  if (int rc = check_norm(b->offset, b->eps)) return rc;
+  if (!std::isfinite(b->scale) || !std::isfinite(b->res_scale))
+    return fail(MOE_ERR_SHAPE, "scale and res_scale must be finite");
+  if (b->gate_mode < MOE_GATE_NONE || b->gate_mode > MOE_GATE_FULL)
+    return fail(MOE_ERR_SHAPE, "unknown gate_mode %d", b->gate_mode);
+  if (b->gate_mode == MOE_GATE_NONE) {
+    if (b->gate) return fail(MOE_ERR_SHAPE, "gate given with MOE_GATE_NONE");
+  } else {
+    if (int rc = check_type("gate_type", b->gate_type)) return rc;
+  }
+  if (b->post_weight && !b->post) return fail(MOE_ERR_SHAPE, "post_weight without post");
+  if (b->post_weight || b->next_weight) {
+    if (int rc = check_type("weight_type", b->weight_type)) return rc;
+  }
+  MAYBE(b->post_weight);
+  MAYBE(b->next_weight);
+  return MOE_OK;
+}
+
+static moe::BlockArgs block_args(const moe_block_t* b) {
+  moe::BlockArgs a{};
+  a.x_f32 = b->x_type == MOE_F32;
+  a.w_f32 = b->weight_type == MOE_F32;
+  a.gate_f32 = b->gate_type == MOE_F32;
+  a.post = b->post != 0;
+  a.gate_mode = b->gate_mode;
+  a.offset = b->offset;
+  a.eps = b->eps;
+  a.scale = b->scale;
+  a.res_scale = b->res_scale;
+  a.post_weight = b->post_weight;
+  a.next_weight = b->next_weight;
+  a.gate = b->gate;
+  return a;
+}
+
+int moe_norm(int64_t T, int32_t emb, const void* x, int32_t x_type, const void* weight, int32_t weight_type,
+             float offset, float eps, moe_bf16_t* y, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_rows(T, emb)) return rc;
+  moe_block_t b{};
+  b.x_type = x_type;
+  b.weight_type = weight_type;
+  b.offset = offset;
+  b.eps = eps;
+  b.next_weight = weight;
+  if (int rc = check_block(&b)) return rc;
+  if (T == 0) return MOE_OK;
+  NEED(x);
+  NEED(y);
+  return hip_status(moe::launch_block_out(T, emb, block_args(&b), x, nullptr, 0, nullptr, nullptr, nullptr, nullptr, y,
+                                          nullptr, (hipStream_t)stream),
+                    "moe_norm");
+}
+
+size_t moe_norm_bwd_workspace_bytes(int64_t T, int32_t emb) {
+  return check_rows(T, emb) == MOE_OK ? moe::block_bwd_workspace(T, emb, 1) : 0;
+}
+
+int moe_norm_bwd(int64_t T, int32_t emb, const moe_bf16_t* dy, const void* x, int32_t x_type, const void* weight,
+                 int32_t weight_type, float offset, float eps, const void* dres, void* dx, float* dweight, void* ws,
+                 size_t ws_bytes, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_rows(T, emb)) return rc;
+  moe_block_t b{};
+  b.x_type = x_type;
+  b.weight_type = weight_type;
+  b.offset = offset;
+  b.eps = eps;
+  b.res_scale = 1.0f;
+  b.next_weight = weight;
+  if (int rc = check_block(&b)) return rc;
+  MAYBE(dweight);
+  if (T > 0) {
+    NEED(dy);
+    NEED(x);
+    MAYBE(dres);
+    NEED(dx);
+  }
+  NEED_WS(dweight ? moe::block_bwd_workspace(T, emb, 1) : 0);
+  return hip_status(moe::launch_block_out_bwd(T, emb, block_args(&b), false, dres, nullptr, x, dy, dx, nullptr, nullptr,
+                                              dweight, nullptr, dweight ? static_cast<float*>(ws) : nullptr,
+                                              (hipStream_t)stream),
+                    "moe_norm_bwd");
+}
+
+int moe_block_out(int64_t T, int32_t emb, const moe_block_t* block, const void* res, const moe_bf16_t* y, int32_t k,
+                  const moe_bf16_t* ys, const int32_t* slot_row, const float* topk_w, void* out, moe_bf16_t* xn,
+                  moe_bf16_t* y_out, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_rows(T, emb)) return rc;
+  if (int rc = check_block(block)) return rc;
+  if (y && (ys || slot_row || topk_w || y_out))
+    return fail(MOE_ERR_SHAPE, "with y, ys, slot_row, topk_w and y_out must be NULL");
+  if (T == 0) return MOE_OK;
+  if (!y) {
+    if (k < 1) return fail(MOE_ERR_SHAPE, "need k >= 1");
+    if (k > 64) return fail(MOE_ERR_UNSUPPORTED, "k (%d) > 64", k);
+    if (T * k >= int64_t(1) << 31) return fail(MOE_ERR_UNSUPPORTED, "T*k >= 2^31");
+    NEED(ys);
+    NEED(slot_row);
+    MAYBE(topk_w);
+    MAYBE(y_out);
+  } else {
+    NEED(y);
+  }
+  if (block->gate_mode != MOE_GATE_NONE) NEED(block->gate);
+  NEED(res);
+  NEED(out);
+  MAYBE(xn);
+  return hip_status(moe::launch_block_out(T, emb, block_args(block), res, y, k, ys, slot_row, topk_w, out, xn, y_out,
+                                          (hipStream_t)stream),
+                    "moe_block_out");
+}
+
+size_t moe_block_out_bwd_workspace_bytes(int64_t T, int32_t emb) {
+  return check_rows(T, emb) == MOE_OK ? moe::block_bwd_workspace(T, emb, 3) : 0;
+}
+
+int moe_block_out_bwd(int64_t T, int32_t emb, const moe_block_t* block, const void* dout, const moe_bf16_t* y,
+                      const void* out, const moe_bf16_t* dxn, void* dres, moe_bf16_t* dy, float* dpost_weight,
+                      float* dnext_weight, void* dgate, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  g_detail[0] = 0;
+  if (int rc = check_rows(T, emb)) return rc;
+  if (int rc = check_block(block)) return rc;
+  if (T > 0 && !dxn && (out || dnext_weight)) return fail(MOE_ERR_SHAPE, "out or dnext_weight without dxn");
+  if (dpost_weight && !block->post) return fail(MOE_ERR_SHAPE, "dpost_weight without post");
+  if (dgate && block->gate_mode == MOE_GATE_NONE) return fail(MOE_ERR_SHAPE, "dgate without a gate");
+  MAYBE(dpost_weight);
+  MAYBE(dnext_weight);
+  MAYBE(dgate);
+  if (T > 0) {
+    if (block->gate_mode != MOE_GATE_NONE) NEED(block->gate);
+    if (!dout && !dxn) return fail(MOE_ERR_NULL, "dout and dxn are both NULL");
+    MAYBE(dout);
+    MAYBE(dxn);
+    if (dxn) NEED(out);
+    if (block->post || block->gate_mode != MOE_GATE_NONE) NEED(y);
+    else MAYBE(y);
+    MAYBE(dres);
+    MAYBE(dy);
+  }
+  const bool sums = dpost_weight || dnext_weight || (dgate && block->gate_mode == MOE_GATE_CHANNEL);
+  NEED_WS(sums ? moe::block_bwd_workspace(T, emb, 3) : 0);
+  return hip_status(moe::launch_block_out_bwd(T, emb, block_args(block), true, dout, y, out, dxn, dres, dy, dpost_weight,
+                                              dnext_weight, dgate, sums ? static_cast<float*>(ws) : nullptr,
+                                              (hipStream_t)stream),
+                    "moe_block_out_bwd");
+}
+
 }  // extern "C"
