@@ -24,6 +24,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import operator
+import struct
 
 import torch
 
@@ -834,9 +835,17 @@ def _weight_type(t, name, emb, dev):
     """MOE_* type of a norm's weight [emb] (fp32 without one)."""
     if t is None:
         return _lib.MOE_F32
+    if type(t) is torch.Tensor and t.device == dev and t.is_contiguous() and t.shape == (emb,):
+        ty = _TYPE.get(t.dtype)
+        if ty is not None:
+            return ty
     ty = _need_typed(t, name, 1)
     _need_like(t, name, (emb,), t.dtype, dev)
     return ty
+
+
+def _bf16_like(t):
+    return torch.empty_like(t) if t.dtype is torch.bfloat16 else torch.empty_like(t, dtype=torch.bfloat16)
 
 
 def norm(x: torch.Tensor, weight: torch.Tensor | None = None, offset: float = 0.0, eps: float = 1e-6,
@@ -849,7 +858,7 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, offset: float = 0.
     _lib.need_32_bits(emb, "emb")
     wt = _weight_type(weight, "weight", emb, dev)
     _need_like(out, "out", (T, emb), torch.bfloat16, dev)
-    y = out if out is not None else torch.empty((T, emb), dtype=torch.bfloat16, device=dev)
+    y = out if out is not None else _bf16_like(x)
     _call("moe_norm", dev, T, emb, x, ty, weight, wt, offset, eps, y)
     return y
 
@@ -878,6 +887,9 @@ def norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = No
     return dx, dw
 
 
+_BLOCK = struct.Struct("@5i4f3P")  # moe_block_t (packed: a third of the time that filling a ctypes structure takes)
+
+
 def _block(x_type, T, emb, dev, post_norm, post_weight, gate, scale, res_scale, next_weight, offset, eps):
     """The structure of a block_out call, and the gate's mode."""
     _lib.need_32_bits(emb, "emb")
@@ -897,9 +909,9 @@ def _block(x_type, T, emb, dev, post_norm, post_weight, gate, scale, res_scale, 
         if mode is None:
             raise ValueError(f"gate must have shape ({emb},), ({T}, 1) or ({T}, {emb}), got {shape}")
         _need_like(gate, "gate", shape, gate.dtype, dev)
-    p = [None if t is None else t.data_ptr() for t in (post_weight, next_weight, gate)]
-    return C.byref(_lib.MoeBlock(x_type, nt if post_weight is None else wt, mode, gt, int(bool(post_norm)), offset,
-                                 eps, scale, res_scale, *p)), mode
+    return _BLOCK.pack(x_type, nt if post_weight is None else wt, mode, gt, 1 if post_norm else 0, offset, eps, scale,
+                       res_scale, 0 if post_weight is None else post_weight.data_ptr(),
+                       0 if next_weight is None else next_weight.data_ptr(), 0 if gate is None else gate.data_ptr()), mode
 
 
 def block_out(res: torch.Tensor, y: torch.Tensor | None = None, ys: torch.Tensor | None = None,
@@ -933,8 +945,8 @@ def block_out(res: torch.Tensor, y: torch.Tensor | None = None, ys: torch.Tensor
         _need_like(slot_row, "slot_row", (T * k,), torch.int32, dev)
     _need_like(out, "out", (T, emb), res.dtype, dev)
     o = out if out is not None else torch.empty_like(res)
-    xn = torch.empty((T, emb), dtype=torch.bfloat16, device=dev) if next_norm else None
-    yo = torch.empty((T, emb), dtype=torch.bfloat16, device=dev) if want_y else None
+    xn = _bf16_like(res) if next_norm else None
+    yo = _bf16_like(res) if want_y else None
     _call("moe_block_out", dev, T, emb, b, res, y, k, ys, slot_row, topk_w, o, xn, yo)
     return dict(out=o, xn=xn, y=yo)
 

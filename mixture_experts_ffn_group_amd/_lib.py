@@ -59,7 +59,7 @@ class MoeBlock(C.Structure):
 
 
 _SHP = C.POINTER(MoeShape)
-_BLK = C.POINTER(MoeBlock)
+_BLK = C.c_void_p  # a MoeBlock by reference, or its bytes
 _RTR = C.POINTER(MoeRouter)
 SIGNATURES = {
     "moe_status_str": ([C.c_int], C.c_char_p),

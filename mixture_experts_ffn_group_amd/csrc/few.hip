@@ -22,112 +22,145 @@ namespace {
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 16;   // rows of a tile: the matrix instruction's side
-constexpr int kFewMaxSlice = 256;  // most mlp columns of a workgroup
-constexpr int kCols = 64;   // mlp columns of a sub-slice: 64 gate and 64 up columns are the 128 columns of a load step
+constexpr int kWaves = 8;           // waves of a workgroup of the experts' kernels
+constexpr int kFewMaxSlice = 128;  // most mlp columns of a workgroup
 
 // ---------------------------------------------------------------- router
 
 // logits[split][t][e] = sum over the split's rows of x[t, i] wr[i, e]. The products (8 + 24 bits) are exact in
 // fp64 and the sums are off by 2^-53 a step, so picks are those of exact arithmetic but for ties to 2^-40.
-// A wave takes 16 experts and a run of emb; v_mfma_f64_16x16x4 has A[i = lane%16][k = lane/16],
-// B[k = lane/16][j = lane%16] and D[i = 4r + lane/16][j = lane%16].
-constexpr int kLogitWaves = 8;
+// A wave takes 16 experts and 64 rows of emb at a time, all of whose loads are in flight at once (the kernel is one
+// memory latency long). v_mfma_f64_16x16x4 has A[i = lane%16][k = lane/16], B[k = lane/16][j = lane%16] and
+// D[i = 4r + lane/16][j = lane%16]; step i of the 16 takes row 16 (lane/16) + i of the 64.
+constexpr int kLogitWaves = 4;
 
 template <int NT>
 __global__ __launch_bounds__(kLogitWaves * 64) void few_logits_kernel(int T, int emb, int E, int run,
                                                                      const uint16_t* __restrict__ x,
                                                                      const float* __restrict__ wr,
                                                                      double* __restrict__ out) {
-  __shared__ double red[kLogitWaves][NT * 16][16];
+  __shared__ double red[kLogitWaves][16][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.x * 16 + (lane & 15);
+  const int c = lane & 15, g = lane >> 4;
+  const int e = blockIdx.x * 16 + c;
   const int ec = e < E ? e : E - 1;  // columns past E are computed on the last one and not stored
   const int k0 = (blockIdx.y * kLogitWaves + wave) * run;
   const int k1 = min(k0 + run, emb);
-  const int kl = lane >> 4;
   f64x4_t acc[NT];
-  const uint16_t* xr[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = f64x4_t{0, 0, 0, 0};
+  for (int k = k0 + 16 * g; k < k1; k += 64) {  // emb and run are multiples of 64
+    float b[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = wr[(int64_t)(k + i) * E + ec];
+    u32x4_t v[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = n * 16 + c;
+      const uint16_t* xr = x + (int64_t)(t < T ? t : T - 1) * emb + k;
+      v[n][0] = ld16(xr);
+      v[n][1] = ld16(xr + 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const double w = (double)b[i];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t d = v[n][i >> 3][(i >> 1) & 3];
+        acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)((i & 1) ? bf16_hi(d) : bf16_lo(d)), w, acc[n], 0, 0, 0);
+      }
+    }
+  }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    acc[n] = f64x4_t{0, 0, 0, 0};
-    const int t = n * 16 + (lane & 15);
-    xr[n] = x + (int64_t)(t < T ? t : T - 1) * emb + kl;
-  }
-  const float* wp = wr + (int64_t)kl * E + ec;
-#pragma unroll 4
-  for (int k = k0; k < k1; k += 4) {  // emb and run are multiples of 4
-    const double b = (double)wp[(int64_t)k * E];
+    if (n) __syncthreads();
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)bf16_to_f32(xr[n][k]), b, acc[n], 0, 0, 0);
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave][n * 16 + 4 * r + kl][lane & 15] = acc[n][r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < NT * 256; i += kLogitWaves * 64) {
-    const int t = i >> 4, ee = blockIdx.x * 16 + (i & 15);
+    for (int r = 0; r < 4; ++r) red[wave][4 * r + g][c] = acc[n][r];
+    __syncthreads();
+    const int i = threadIdx.x;  // 256 of them
+    const int t = n * 16 + (i >> 4), ee = blockIdx.x * 16 + (i & 15);
     if (t >= T || ee >= E) continue;
     double s = 0;
 #pragma unroll
-    for (int w = 0; w < kLogitWaves; ++w) s += red[w][t][i & 15];
+    for (int w = 0; w < kLogitWaves; ++w) s += red[w][i >> 4][i & 15];
     out[((int64_t)blockIdx.y * T + t) * E + ee] = s;
   }
 }
 
-// Order-preserving 64-bit key: larger logit, larger key; -0 like +0; NaN 1, below every number; 0 is "taken".
-__device__ __forceinline__ uint64_t key64(double v) {
-  if (v != v) return 1;
+// Order-preserving 64-bit key of expert e's logit: larger logit, larger key, -0 like +0, NaN like -inf; the low 8 bits
+// give equal logits (to 2^-44) to the lower id. 0 is no key.
+__device__ __forceinline__ uint64_t pick_key(double v, int e) {
+  if (v != v) v = -__builtin_inf();
   if (v == 0) v = 0;
   const uint64_t u = (uint64_t)__double_as_longlong(v);
-  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+  return (((u >> 63) ? ~u : (u | 0x8000000000000000ull)) & ~0xffull) | (uint64_t)(255 - e);
 }
-__device__ __forceinline__ double key64_value(uint64_t k) {
-  if (k == 1) return -__builtin_inf();
-  return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+__device__ __forceinline__ double pick_value(uint64_t k) {
+  return __longlong_as_double((long long)(((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k) & ~0xffull));
+}
+// Largest value of the wave, in every lane: the rows' maxima meet in scalar registers.
+__device__ __forceinline__ uint32_t wave_max_fused(uint32_t v) {
+  v = row_max_fused(v);
+  const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0), b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
+  const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32), d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+  return max(max(a, b), max(c, d));
 }
 
-// One wave picks token t's experts: lane j ends with pick j's expert and weight (lanes past k: unspecified).
+// One wave picks token t's experts: lane j gets pick j and its logit (lanes past k: 0 and -inf).
 __device__ __forceinline__ void few_pick(int T, int E, int k, int splits, int t, const double* __restrict__ logits,
-                                         const float* __restrict__ bias, int lane, int& pick, float& weight) {
+                                         const float* __restrict__ bias, int lane, int& pick, double& logit) {
+  // all of the cuts' sums in flight at once, in batches of 8 (cuts and experts that are not there load others')
+  double sum[4] = {0, 0, 0, 0};
+  const double* p = logits + (int64_t)t * E;
+  const int64_t cut = (int64_t)T * E;
+  for (int c0 = 0; c0 < splits; c0 += 8) {
+    double v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (64 * i >= E) continue;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[i][c] = p[min(c0 + c, splits - 1) * cut + min(lane + 64 * i, E - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (64 * i >= E) continue;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[i] += c0 + c < splits ? v[i][c] : 0;
+    }
+  }
   uint64_t key[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = lane + 64 * i;
-    key[i] = 0;
-    if (e < E) {
-      double s = 0;
-      for (int c = 0; c < splits; ++c) s += logits[((int64_t)c * T + t) * E + e];
-      if (bias) s += (double)bias[e];
-      key[i] = key64(s);
-    }
+    key[i] = e < E ? pick_key(bias ? sum[i] + (double)bias[e] : sum[i], e) : 0;
   }
-  pick = 0;
-  double l = -__builtin_inf();
+  sort_desc(key);
+  uint64_t mine = 0;
   for (int j = 0; j < k; ++j) {
-    uint64_t best = key[0];
-    int bi = 0;
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-      if (key[i] > best) best = key[i], bi = i;
-    const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
-    const uint32_t mh = wave_max_u32(hi);
-    const uint32_t ml = wave_max_u32(hi == mh ? lo : 0u);
-    const bool top = hi == mh && lo == ml;
-    // equal values: the lowest id
-    const int e = 0xffff - (int)wave_max_u32(top ? 0xffffu - (uint32_t)(lane + 64 * bi) : 0u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i == e) key[i] = 0;
-    if (lane == j) pick = e, l = key64_value((uint64_t)mh << 32 | ml);
+    const uint32_t hi = (uint32_t)(key[0] >> 32), lo = (uint32_t)key[0];
+    const uint32_t mh = wave_max_fused(hi);
+    uint64_t m = __ballot(hi == mh);
+    if (m & (m - 1)) {  // several lanes, seldom: the low halves differ, if only in the id
+      const uint32_t ml = wave_max_fused(hi == mh ? lo : 0u);
+      m = __ballot(hi == mh && lo == ml);
+    }
+    const int l = __builtin_ctzll(m);
+    const uint32_t ml = (uint32_t)__builtin_amdgcn_readlane((int)lo, l);
+    if (lane == l) key[0] = key[1], key[1] = key[2], key[2] = key[3], key[3] = 0;
+    if (lane == j) mine = (uint64_t)mh << 32 | ml;
   }
-  const double l0 = __shfl(l, 0);
-  double w = lane < k && l != -__builtin_inf() ? exp(l - l0) : 0.0;  // a disabled expert's weight is 0
+  pick = lane < k ? 255 - (int)(mine & 0xff) : 0;
+  logit = lane < k ? pick_value(mine) : -__builtin_inf();
+}
+
+// Weight of pick `lane`: the softmax over the k picks; a disabled expert's is 0.
+__device__ __forceinline__ float few_weight(int k, double logit, int lane) {
+  const double l0 = __shfl(logit, 0);
+  const double w = lane < k && logit != -__builtin_inf() ? exp(logit - l0) : 0.0;
   double s = w;
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m);
-  weight = s == 0 ? 0.0f : (float)(w / s);
+  return s == 0 ? 0.0f : (float)(w / s);
 }
 
 __global__ __launch_bounds__(64) void few_topk_kernel(int T, int E, int k, int splits, const double* __restrict__ logits,
@@ -135,96 +168,115 @@ __global__ __launch_bounds__(64) void few_topk_kernel(int T, int E, int k, int s
                                                       float* __restrict__ topk_w) {
   const int lane = threadIdx.x, t = blockIdx.x;
   int pick;
-  float weight;
-  few_pick(T, E, k, splits, t, logits, bias, lane, pick, weight);
+  double logit;
+  few_pick(T, E, k, splits, t, logits, bias, lane, pick, logit);
+  const float w = few_weight(k, logit, lane);
   if (lane < k) {
     topk_idx[t * k + lane] = pick;
-    topk_w[t * k + lane] = weight;
+    topk_w[t * k + lane] = w;
   }
 }
 
 // ---------------------------------------------------------------- experts
 
-// Both weight forms are read in steps of 8 KB a wave (8 loads of 16 bytes a lane) over 128 columns, and both give the
-// matrix instruction (v_mfma_f32_16x16x32_bf16: A[row lane%16][k 8*(lane/16) + i], B[k][column lane%16], D[row
-// 4*(lane/16) + r][column lane%16]) its B operand straight from the registers they were loaded into.
-//
-// bf16, row-major [K, N], a step is 32 rows: lane (g = lane/16, c = lane%16) loads columns 8c..8c+7 of rows 8g..8g+7.
-// Product j takes column 8c + j of every lane c; its 8 values along K lie in the lane's 8 rows, and one byte permute
-// puts two of them into a register.
-struct StepBf16 {
-  static constexpr int kK = 32;
-  u32x4_t v[8];
-  __device__ __forceinline__ void load(const uint16_t* p, int64_t ld) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = ld16(p + i * ld);
-  }
-  __device__ __forceinline__ bf16x8_t frag(int j) const {
-    const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
-    u32x4_t r;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) r[p] = __builtin_amdgcn_perm(v[2 * p + 1][j >> 1], v[2 * p][j >> 1], sel);
-    return __builtin_bit_cast(bf16x8_t, r);
-  }
-};
-
-// MXFP8, K-contiguous rows [N, K], a step is 64 values of K: of column 16j + c lane (g, c) loads codes 16g..16g+15 and
-// the dword with the scales of the step's two 32-blocks. They convert to bf16 exactly (3 bits of mantissa; a scale
-// code below 3, which only blocks of subnormal weights have, or above 246 leaves bf16's range), 8 values an operand.
-struct StepMx {
-  static constexpr int kK = 64;
-  u32x4_t v[8];
-  uint32_t sc[8];
-  __device__ __forceinline__ void load(int j, const uint8_t* code, const uint8_t* scale) {
-    v[j] = ld16(code);
-    sc[j] = *reinterpret_cast<const uint32_t*>(scale);
-  }
-  __device__ __forceinline__ bf16x8_t frag(int j, int h, int g) const {
-    // the conversion's scale operand is a float of which it takes the exponent
-    const float s = __uint_as_float(((g & 2) ? (sc[j] >> 8) & 0xffu : sc[j] & 0xffu) << 23);
-    u32x4_t r;
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      r[2 * p] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j][2 * h + p], s, false));
-      r[2 * p + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j][2 * h + p], s, true));
-    }
-    return __builtin_bit_cast(bf16x8_t, r);
-  }
-};
+// Weights are read once and not again: non-temporal loads (a plain read of 4 GiB ran at 6.2 TB/s, a non-temporal one
+// at 7.2).
+__device__ __forceinline__ u32x4_t ldw16(const void* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+}
 
 __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+__device__ __forceinline__ bf16x8_t as_bf16(u32x4_t v) { return __builtin_bit_cast(bf16x8_t, v); }
 
-// Workgroup (tile, slice): up to 16 rows (slots t*k + j) of one expert, and `slice` of its mlp columns. The waves share
-// the contraction of the first product (emb) and add up through LDS; of the second (the slice's columns) each takes
-// output columns. part[slot][slice][emb] receives the slice's share of the slot's output row.
-template <bool MX, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void few_experts_kernel(int S, int k, int emb, int mlp, int E, int slice, int ns,
-                                                                 const uint16_t* __restrict__ x,
-                                                                 const int32_t* __restrict__ topk_idx, FewWeights wt,
-                                                                 float* __restrict__ part) {
-  constexpr int kLdA = kFewMaxSlice + 8;
-  __shared__ __align__(16) float red[NW][kRows][128];
-  __shared__ __align__(16) uint16_t a_hi[kRows][kLdA], a_lo[kRows][kLdA];
-  __shared__ int cnt[kMaxExperts];
-  __shared__ int found[2];
-  __shared__ int rows[kRows];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int c = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x / ns, sl = blockIdx.x - tile * ns;
+// A wave reads weights in steps of 8 KB whose every load covers whole 128-byte lines (8 to a load: half-line requests
+// cost half the rate, 3.7 against 6.7 TB/s). The matrix instruction is v_mfma_f32_16x16x32_bf16: A[row lane%16]
+// [k 8*(lane/16) + i], B[k][column lane%16], D[row 4*(lane/16) + r][column lane%16]; g = lane/16, c = lane%16. The rows'
+// part (x, the A operand) is loaded with the weights, so that waiting for it does not wait for the loads issued after it.
+//
+// bf16, row-major [K, N], 128 columns by 32 rows: the lane loads columns 8c..8c+7 of rows 8g..8g+7 (of the first
+// product, c < 8 gate and c >= 8 up columns). Product j takes column 8c + j of every lane; its 8 values along K lie in
+// the lane's 8 rows, and one byte permute puts two of them into a register: the B operand comes straight from the
+// registers that were loaded.
+struct StepBf16 {
+  u32x4_t x, v[8];
+  __device__ __forceinline__ void load(const char* p, int64_t ld, uint32_t lane, const char* xp, uint32_t xlane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = ldw16(p + i * ld + lane);
+    x = ld16(xp + xlane);
+  }
+  __device__ __forceinline__ bf16x8_t col(int j) const {
+    const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
+    u32x4_t r;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) r[p] = __builtin_amdgcn_perm(v[2 * p + 1][j >> 1], v[2 * p][j >> 1], sel);
+    return as_bf16(r);
+  }
+};
 
-  // which expert (tiles go by expert, then by row), and which of its rows
-  for (int i = tid; i < kMaxExperts; i += NW * 64) cnt[i] = 0;
-  if (tid < kRows) rows[tid] = -1;
+// MXFP8, K-contiguous [N, K], 64 columns by 128 values of K: load j covers columns 8j..8j+7, 16 codes a lane. In that
+// order the lanes of a column hold its K side by side, where the matrix instruction wants columns side by side: the
+// step goes through the wave's own 8 KB of LDS, from where lane (g, c) reads codes 16(4p + g).. of column 16t + c.
+// Within a column the 16-byte units are stored at u ^ (column & 7), so that both the writes and the reads spread over
+// the banks; the swizzle is in the address the lane loads from. `scale` holds the dwords of the 64 columns for the
+// step's two 64-blocks. Codes convert to bf16 exactly (3 bits of mantissa; a scale code below 3, which only blocks of
+// subnormal weights have, or above 246 leaves bf16's range).
+// Slices of 64 mlp columns give the second product rows of 64 bytes: 128 columns by 64 values of K then, in the
+// operand's own order (v[j]: column 16j + c, codes 16g..), through plain loads.
+struct StepMx {
+  u32x4_t x[4], v[8];
+  uint32_t scale[2];
+};
+
+__device__ __forceinline__ bf16x8_t mx_values(u32x4_t codes, int h, uint32_t code) {
+  // the conversion's scale operand is a float of which it takes the exponent
+  const float s = __uint_as_float((code & 0xffu) << 23);
+  u32x4_t r;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    r[2 * p] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[2 * h + p], s, false));
+    r[2 * p + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[2 * h + p], s, true));
+  }
+  return as_bf16(r);
+}
+
+// Finds tile `tile`: up to 16 slots (t*k + j) of one expert, in slot order. Lane r < 16 gets row r's slot.
+
+// Up to 64 slots, slot l's expert in lane l: every wave by itself, in registers. A slot whose rank among its expert's
+// is a multiple of 16 starts a tile.
+__device__ __forceinline__ void find_tile64(int S, int E, int tile, int e, int lane, int& te, int& tn,
+                                            int& slot) {
+  const bool valid = lane < S && (unsigned)e < (unsigned)E;
+  for (int j = 0; j < S; ++j) {
+    const int ej = __builtin_amdgcn_readlane(e, j);
+    if ((unsigned)ej >= (unsigned)E) continue;
+    const uint64_t m = __ballot(valid && e == ej);
+    const int rank = popc64(m & ((1ull << j) - 1));
+    if (rank % kRows || tile--) continue;
+    const int r = popc64(m & ((1ull << lane) - 1)) - rank;
+    const bool in = valid && e == ej && r >= 0 && r < kRows;
+    // lanes outside send to lane 63, which is no row's
+    slot = __builtin_amdgcn_ds_permute((in ? r : 63) * 4, lane);
+    te = ej;
+    tn = min(kRows, popc64(m) - rank);
+    break;
+  }
+}
+
+// Any number of slots, through LDS; tiles go by expert. Called by the whole workgroup.
+__device__ __forceinline__ void find_tile(int S, int E, int tile, const int32_t* __restrict__ idx, int* cnt, int* found,
+                                          int* rows, int& te, int& tn, int& slot) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int i = tid; i < kMaxExperts; i += kWaves * 64) cnt[i] = 0;
   if (tid == 0) found[0] = -1;
   __syncthreads();
-  for (int i = tid; i < S; i += NW * 64) {
-    const int e = topk_idx[i];
+  for (int i = tid; i < S; i += kWaves * 64) {
+    const int e = idx[i];
     if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
-  if (wave == 0) {
+  if (tid < 64) {
     int base = 0;
     for (int q = 0; q < E; q += 64) {
       const int n = (cnt[q + lane] + kRows - 1) / kRows;
@@ -243,10 +295,10 @@ __global__ __launch_bounds__(NW * 64, 2) void few_experts_kernel(int S, int k, i
   const int e = found[0];
   if (e < 0) return;
   const int r0 = found[1] * kRows;
-  if (wave == 0) {
+  if (tid < 64) {
     int base = 0;
     for (int q = 0; q < S; q += 64) {
-      const bool mine = q + lane < S && topk_idx[q + lane] == e;
+      const bool mine = q + lane < S && idx[q + lane] == e;
       const uint64_t m = __ballot(mine);
       const int r = base + popc64(m & ((1ull << lane) - 1)) - r0;
       if (mine && r >= 0 && r < kRows) rows[r] = q + lane;
@@ -254,141 +306,403 @@ __global__ __launch_bounds__(NW * 64, 2) void few_experts_kernel(int S, int k, i
     }
   }
   __syncthreads();
-  const int nrows = min(kRows, cnt[e] - r0);
-  // lanes past the last row compute on the first one; their rows of the results are not used
-  const uint16_t* xr = x + (int64_t)((c < nrows ? rows[c] : rows[0]) / k) * emb;
+  te = e;
+  tn = min(kRows, cnt[e] - r0);
+  slot = rows[lane < tn ? lane : 0];
+}
 
-  const int m0 = sl * slice;
-  const int width = min(slice, mlp - m0);
-  for (int s0 = 0; s0 < width; s0 += kCols) {
-    // first product: 64 gate and the 64 up columns from m0 + s0
-    f32x4_t acc[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
-    if constexpr (!MX) {
-      const int64_t ld = 2 * (int64_t)mlp;
-      const uint16_t* p = wt.wi + ((int64_t)e * emb + 8 * g) * ld + m0 + s0 + (c < 8 ? 8 * c : mlp + 8 * (c - 8));
-#pragma unroll 2
-      for (int kk = wave * StepBf16::kK; kk < emb; kk += NW * StepBf16::kK) {
-        StepBf16 st;
-        st.load(p + kk * ld, ld);
-        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, ld16(xr + kk + 8 * g));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = mfma(a, st.frag(j), acc[j]);
-      }
-    } else {
-      const int64_t row = (int64_t)e * 2 * mlp + m0 + s0 + c;
-      const uint8_t* p = wt.wic + row * emb + 16 * g;
-      const uint8_t* q = wt.wis + ((int64_t)e * (emb / 64) * 2 * mlp + m0 + s0 + c) * 4;
-#pragma unroll 2
-      for (int kk = wave * StepMx::kK; kk < emb; kk += NW * StepMx::kK) {
-        StepMx st;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int n = j < 4 ? 16 * j : mlp + 16 * (j - 4);
-          st.load(j, p + (int64_t)n * emb + kk, q + ((int64_t)(kk / 64) * 2 * mlp + n) * 4);
+struct FewArgs {
+  int T, k, emb, mlp, E, slice, ns, blocks, splits;
+  const uint16_t* x;
+  const double* logits;  // PICK: the picks are made here
+  const float* bias;
+  int32_t* topk_idx;
+  float* topk_w;
+  FewWeights wt;
+  float* part;
+};
+
+// Workgroup (tile, slice): the tile's rows, and `slice` (64 or 128) of its expert's mlp columns, 64 at a time in the
+// first product. The waves share the contraction of the first product (emb) and add up through LDS; of the second (over
+// the slice's columns) each takes output columns. part[slot][slice][emb] receives the slice's share of the slot's
+// output row.
+//
+// A wave's weight steps, those of the first product and then those of the second, form one sequence of which two are
+// always in flight, over the barriers between the products too: the second product's first weights arrive while the
+// first one's sums go through LDS.
+// PICK (T <= kWaves, T*k <= 64): every workgroup first picks the experts from the logits, a wave a token, instead of
+// waiting for another kernel to do it; workgroup 0 writes the routing.
+struct FewLds {
+  union {
+    float red[kWaves][kRows][128];  // first product: each wave's sums; MXFP8: before and after, the wave's step
+    struct {                    // before both: the search for the tile
+      int cnt[kMaxExperts], found[2], picks[64];
+    };
+  };
+  uint16_t a_hi[kRows][kFewMaxSlice + 8], a_lo[kRows][kFewMaxSlice + 8];
+  int rows[kRows];
+  int64_t share[kRows];  // where each row's share starts in part
+};
+
+// Which rows, of which expert. False: the routing has no such tile.
+template <bool PICK>
+__device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds& lds, int lane, int wave, int& e, int& nrows,
+                                         int& slot) {
+  e = -1;
+  nrows = slot = 0;
+  const int S = q.T * q.k;
+  if constexpr (PICK) {
+    if (wave < q.T) {
+      int pick;
+      double logit;
+      few_pick(q.T, q.E, q.k, q.splits, wave, q.logits, q.bias, lane, pick, logit);
+      if (lane < q.k) lds.picks[wave * q.k + lane] = pick;
+      if (blockIdx.x == 0) {
+        const float w = few_weight(q.k, logit, lane);
+        if (lane < q.k) {
+          q.topk_idx[wave * q.k + lane] = pick;
+          q.topk_w[wave * q.k + lane] = w;
         }
-        bf16x8_t a[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) a[h] = __builtin_bit_cast(bf16x8_t, ld16(xr + kk + 16 * g + 8 * h));
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) acc[j] = mfma(a[h], st.frag(j, h, g), acc[j]);
-      }
-    }
-    if (s0) __syncthreads();  // the previous sub-slice's sums have been read
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (4 * g + r >= nrows) continue;
-      float* d = red[wave][4 * g + r];
-      if constexpr (!MX) {
-        *reinterpret_cast<f32x4_t*>(d + 8 * c) = f32x4_t{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
-        *reinterpret_cast<f32x4_t*>(d + 8 * c + 4) = f32x4_t{acc[4][r], acc[5][r], acc[6][r], acc[7][r]};
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[16 * j + c] = acc[j][r];
       }
     }
     __syncthreads();
-    for (int i = tid; i < kRows * kCols; i += NW * 64) {
-      const int r = i / kCols, q = i % kCols;
-      float gate = 0, up = 0;
-      if (r < nrows) {
+    find_tile64(S, q.E, tile, lane < S ? lds.picks[lane] : -1, lane, e, nrows, slot);
+  } else if (S <= 64) {
+    find_tile64(S, q.E, tile, lane < S ? q.topk_idx[lane] : -1, lane, e, nrows, slot);
+  } else {
+    find_tile(S, q.E, tile, q.topk_idx, lds.cnt, lds.found, lds.rows, e, nrows, slot);
+  }
+  __syncthreads();  // the search is over, its LDS free
+  e = __builtin_amdgcn_readfirstlane(e);
+  nrows = __builtin_amdgcn_readfirstlane(nrows);
+  return e >= 0;
+}
+
+// The waves' sums of 64 gate and 64 up columns -> SwiGLU -> a's columns s0...
+__device__ __forceinline__ void few_swiglu(FewLds& lds, int nrows, int s0) {
+  for (int i = threadIdx.x; i < kRows * 64; i += kWaves * 64) {
+    const int r = i >> 6, n = i & 63;
+    float gate = 0, up = 0;
+    if (r < nrows) {
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          gate += red[w][r][q];
-          up += red[w][r][kCols + q];
-        }
+      for (int w = 0; w < kWaves; ++w) {
+        gate += lds.red[w][r][n];
+        up += lds.red[w][r][64 + n];
       }
-      // The product enters the second one as the sum of two bf16 numbers, 16 bits of it: the matrix cores are idle most
-      // of the time, so the layer's bf16 rounding of a is not needed here.
-      const float a = silu_f(gate) * up;
-      const uint16_t hi = (uint16_t)pack_bf16x2(a, 0.0f);
-      a_hi[r][s0 + q] = hi;
-      a_lo[r][s0 + q] = (uint16_t)pack_bf16x2(a - bf16_to_f32(hi), 0.0f);
     }
+    // The product enters the second one as the sum of two bf16 numbers, 16 bits of it: the matrix cores are idle most
+    // of the time, so the layer's bf16 rounding of a is not needed here.
+    const float a = silu_f(gate) * up;
+    const uint16_t hi = (uint16_t)pack_bf16x2(a, 0.0f);
+    lds.a_hi[r][s0 + n] = hi;
+    lds.a_lo[r][s0 + n] = (uint16_t)pack_bf16x2(a - bf16_to_f32(hi), 0.0f);
+  }
+}
+
+__device__ __forceinline__ const char* bytes(const void* p) { return static_cast<const char*>(p); }
+
+template <bool WIDE, bool PICK>
+__global__ __launch_bounds__(kWaves * 64, WIDE ? 2 : 4) void few_experts_kernel(FewArgs q) {
+  __shared__ __align__(16) FewLds lds;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int emb = q.emb, mlp = q.mlp;
+  const int tile = blockIdx.x / q.ns, sl = blockIdx.x - tile * q.ns;
+  int e, nrows, slot;
+  if (!few_tile<PICK>(q, tile, lds, lane, wave, e, nrows, slot)) return;
+  const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
+  // lanes past the last row compute on the first one; their rows of the results are not used
+  const uint32_t xrow = (uint32_t)__shfl(slot, c < nrows ? c : 0) / (uint32_t)q.k;
+  // read after the first product's barrier
+  if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb;
+
+  // The sequence of a wave's steps: n1 pairs of the first product (WIDE: a step for each 64 of the slice's 128 columns;
+  // else two steps of its 64), then one step per 32 columns of the slice for each of its output blocks of 128 columns.
+  // Steps past the wave's share, and past the end, load the same few words over and over: loads are never skipped, so
+  // that the wait for a step counts on those behind.
+  constexpr int kPair = WIDE ? 32 : 64;  // rows of emb in a pair
+  const int n1 = (emb + kWaves * kPair - 1) / (kWaves * kPair);
+  int lw = 0, ln = wave * 128, lk = 0;
+  const int64_t ld1 = 4 * (int64_t)mlp, ld2 = 2 * (int64_t)emb;  // bytes from row to row
+  const uint32_t lane1 = 8 * g * (uint32_t)ld1 + 2 * (c < 8 ? 8 * c : mlp + 8 * (c - 8));
+  const uint32_t lane2 = 8 * g * (uint32_t)ld2 + 16 * c;
+  const uint32_t xlane = 2 * (xrow * (uint32_t)emb + 8 * g);
+  const auto load = [&](StepBf16& st, int u) {  // u: which of the pair
+    const bool first = lw < n1;
+    const int k1 = (lw * kWaves + wave) * kPair + (WIDE ? 0 : 32 * u);
+    const bool real = first ? k1 < emb && (!WIDE || 64 * u < width) : ln < emb;
+    // emb is a multiple of 64: the last block may have 64 columns, the other half then takes the first ones
+    const uint32_t l2 = ln + 64 >= emb && c >= 8 ? lane2 - 128 : lane2;
+    const char* p1 = bytes(q.wt.wi) + ((int64_t)e * emb + k1) * ld1 + 2 * (m0 + (WIDE ? 64 * u : 0));
+    const char* p2 = bytes(q.wt.wo) + ((int64_t)e * mlp + m0 + lk) * ld2 + 2 * ln;
+    st.load(real ? first ? p1 : p2 : bytes(q.x), real ? first ? ld1 : ld2 : 0, real ? first ? lane1 : l2 : 0,
+            bytes(q.x) + (first && real ? 2 * k1 : 0), xlane);
+    const bool wrap = lk + 32 >= width;
+    lk = first ? lk : wrap ? 0 : lk + 32;
+    ln = !first && wrap ? ln + kWaves * 128 : ln;
+    lw = u == 1 && first ? lw + 1 : lw;
+  };
+
+  StepBf16 st[2];
+  load(st[0], 0);
+  load(st[1], 1);
+  f32x4_t sum[WIDE ? 2 : 1][8];
+#pragma unroll
+  for (int u = 0; u < (WIDE ? 2 : 1); ++u)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[u][j] = f32x4_t{0, 0, 0, 0};
+  for (int w = 0; w < n1; ++w) {
+    const bool on = (w * kWaves + wave) * kPair < emb;  // emb is a multiple of 64: both steps of a pair or none
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (on) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[WIDE ? u : 0][j] = mfma(as_bf16(st[u].x), st[u].col(j), sum[WIDE ? u : 0][j]);
+      }
+      load(st[u], u);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < (WIDE ? 2 : 1); ++u) {
+    if (64 * u >= width) continue;
+    if (u) __syncthreads();  // the first columns' sums have been read
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (4 * g + r >= nrows) continue;
+      float* d = &lds.red[wave][4 * g + r][8 * c];
+      *reinterpret_cast<f32x4_t*>(d) = f32x4_t{sum[u][0][r], sum[u][1][r], sum[u][2][r], sum[u][3][r]};
+      *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{sum[u][4][r], sum[u][5][r], sum[u][6][r], sum[u][7][r]};
+    }
+    __syncthreads();
+    few_swiglu(lds, nrows, 64 * u);
   }
   __syncthreads();
 
-  float* po[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) po[r] = part + ((int64_t)max(rows[4 * g + r], 0) * ns + sl) * emb;
-  for (int n0 = wave * 128; n0 < emb; n0 += NW * 128) {
-    f32x4_t acc[8];
+  f32x4_t acc[8];
+  for (int n0 = wave * 128; n0 < emb; n0 += kWaves * 128) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
-    // emb is a multiple of 64: the last block may have 64 columns, the other half then computes on the first ones
-    if constexpr (!MX) {
-      const int n = n0 + 8 * c;
-      const uint16_t* p = wt.wo + ((int64_t)e * mlp + m0 + 8 * g) * emb + (n < emb ? n : n0);
-#pragma unroll 2
-      for (int kk = 0; kk < width; kk += StepBf16::kK) {
-        StepBf16 st;
-        st.load(p + (int64_t)kk * emb, emb);
-        const bf16x8_t ah = __builtin_bit_cast(bf16x8_t, ld16(&a_hi[c][kk + 8 * g]));
-        const bf16x8_t al = __builtin_bit_cast(bf16x8_t, ld16(&a_lo[c][kk + 8 * g]));
+    for (int kk = 0; kk < width; kk += 64) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bf16x8_t ah = as_bf16(ld16(&lds.a_hi[c][kk + 32 * u + 8 * g]));
+        const bf16x8_t al = as_bf16(ld16(&lds.a_lo[c][kk + 32 * u + 8 * g]));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const bf16x8_t b = st.frag(j);
+          const bf16x8_t b = st[u].col(j);
           acc[j] = mfma(al, b, mfma(ah, b, acc[j]));
         }
+        load(st[u], u);
       }
-      if (n >= emb) continue;
+    }
+    // The lane's place and the rows' addresses are made anew for each block: kept over the loop they would not fit the
+    // 128 registers that two workgroups a compute unit allow, and a spill's reload waits for the weights in flight.
+    int zero = 0;
+    asm volatile("" : "+s"(zero)::"memory");
+    const int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+    const int n = n0 + 8 * (l & 15);
+    if (n >= emb) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (4 * g + r >= nrows) continue;
-        *reinterpret_cast<f32x4_t*>(po[r] + n) = f32x4_t{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
-        *reinterpret_cast<f32x4_t*>(po[r] + n + 4) = f32x4_t{acc[4][r], acc[5][r], acc[6][r], acc[7][r]};
-      }
-    } else {
-      const uint8_t* p = wt.woc + ((int64_t)e * emb + n0 + c) * mlp + m0 + 16 * g;
-      const uint8_t* q = wt.wos + ((int64_t)e * (mlp / 64) * emb + n0 + c) * 4;
-#pragma unroll 2
-      for (int kk = 0; kk < width; kk += StepMx::kK) {
-        StepMx st;
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * (l >> 4) + r;
+      if (row >= nrows) continue;
+      float* d = q.part + lds.share[row] + n;
+      *reinterpret_cast<f32x4_t*>(d) = f32x4_t{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
+      *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{acc[4][r], acc[5][r], acc[6][r], acc[7][r]};
+    }
+  }
+}
+
+// The same on MXFP8 weights.
+template <bool PICK>
+__global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs q) {
+  __shared__ __align__(16) FewLds lds;
+  __shared__ uint32_t scale[kWaves][2][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int emb = q.emb, mlp = q.mlp;
+  int b = blockIdx.x;
+  if (q.slice == 64) {
+    // two slices share each 128-byte line of wo: blocks b and b + 8 run on the same XCD
+    b = (b & ~15) | ((b & 7) << 1) | ((b >> 3) & 1);
+    if (b >= q.blocks) return;
+  }
+  const int tile = b / q.ns, sl = (b - tile * q.ns + (q.slice == 64 ? 0 : tile)) % q.ns;
+  int e, nrows, slot;
+  if (!few_tile<PICK>(q, tile, lds, lane, wave, e, nrows, slot)) return;
+  const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
+  const bool narrow = width == 64;  // of the second product's steps
+  const uint32_t xrow = (uint32_t)__shfl(slot, c < nrows ? c : 0) / (uint32_t)q.k;
+  // read after the first product's barrier
+  if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb;
+
+  // The sequence: for each 64 columns, n1 pairs of steps (gate, up) of 128 values of emb; then output blocks of 128
+  // columns, one narrow or two wide steps each, an even number in all.
+  const int n1 = (emb + kWaves * 128 - 1) / (kWaves * 128);
+  const uint32_t r8 = lane >> 3, unit = (lane & 7) ^ r8;  // wide: the lane's column of each eight, and its unit
+  int ls = 0, lw = 0, ln = wave * 128;
+  const auto load = [&](StepMx& st, int u) {  // u: which of the pair
+    const bool first = ls < width;
+    const int k1 = (lw * kWaves + wave) * 128;
+    const bool real = first ? k1 < emb : ln < emb;
+    const int64_t ld = first ? emb : mlp;
+    // wide: the first column, and the values of K that are there (emb is a multiple of 64)
+    const int n = first ? m0 + ls + (u ? mlp : 0) : ln + (narrow ? 0 : 64 * u);
+    const bool there = first || n < emb;  // the last output block may have 64 columns
+    const bool half = first && k1 + 64 >= emb;
+    const int64_t row = (int64_t)e * (first ? 2 * mlp : emb) + (there ? n : ln);
+    const char* p = (first ? bytes(q.wt.wic) : bytes(q.wt.woc)) + row * ld + (first ? k1 : m0);
+    const int64_t planes = first ? 2 * mlp : emb;
+    const char* s = (first ? bytes(q.wt.wis) : bytes(q.wt.wos)) +
+                    (((int64_t)e * (ld / 64) + (first ? k1 : m0) / 64) * planes + (there ? n : ln)) * 4;
+    const bool direct = !first && narrow;
+    uint32_t lo = direct ? c * (uint32_t)mlp + 16 * g : r8 * (uint32_t)ld + 16 * (half ? unit & 3 : unit);
+    int64_t step = direct ? 16 * ld : 8 * ld;
+    // columns 64..127 of a narrow step may not be there
+    int64_t upper = direct && ln + 64 >= emb ? 0 : 4 * step;
+    int64_t plane = direct ? (ln + 64 >= emb ? 0 : 256) : half ? 0 : 4 * planes;
+    if (!real) p = bytes(q.wt.wic), s = bytes(q.wt.wis), step = upper = plane = 0, lo = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int n = n0 + 16 * j < emb ? 16 * j : 16 * (j - 4);
-          st.load(j, p + (int64_t)n * mlp + kk, q + ((int64_t)((m0 + kk) / 64) * emb + n) * 4);
-        }
+    for (int j = 0; j < 4; ++j) {
+      st.v[j] = ldw16(p + j * step + lo);
+      st.v[4 + j] = ldw16(p + upper + j * step + lo);
+    }
+    st.scale[0] = *reinterpret_cast<const uint32_t*>(s + 4 * lane);
+    st.scale[1] = *reinterpret_cast<const uint32_t*>(s + plane + 4 * lane);
+    const char* xp = bytes(q.x) + 2 * (xrow * (uint32_t)emb + 16 * g) + (first && real ? 2 * k1 : 0);
+    const int xh = half || !real || !first ? 0 : 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bf16x8_t ah = __builtin_bit_cast(bf16x8_t, ld16(&a_hi[c][kk + 16 * g + 8 * h]));
-          const bf16x8_t al = __builtin_bit_cast(bf16x8_t, ld16(&a_lo[c][kk + 16 * g + 8 * h]));
+    for (int h = 0; h < 2; ++h) {
+      st.x[h] = ld16(xp + 16 * h);
+      st.x[2 + h] = ld16(xp + xh + 16 * h);
+    }
+    const bool wrap = lw + 1 == n1;
+    const bool pair = u == 1;
+    ls = first && pair && wrap ? ls + 64 : ls;
+    lw = !first || !pair ? lw : wrap ? 0 : lw + 1;
+    ln = !first && (narrow || pair) ? ln + kWaves * 128 : ln;
+  };
+  // wide step -> LDS; then column tile t's 16 codes (unit 4p + g) and their scale code
+  u32x4_t* my = reinterpret_cast<u32x4_t*>(lds.red[wave]);
+  const auto stage = [&](const StepMx& st) {
+    wave_lds_fence();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const bf16x8_t b = st.frag(j, h, g);
-            acc[j] = mfma(al, b, mfma(ah, b, acc[j]));
+    for (int j = 0; j < 8; ++j) my[64 * j + lane] = st.v[j];
+    scale[wave][0][lane] = st.scale[0];
+    scale[wave][1][lane] = st.scale[1];
+    wave_lds_fence();
+  };
+  const auto codes = [&](int t, int p) { return my[(16 * t + c) * 8 + ((4 * p + g) ^ (c & 7))]; };
+  const auto code_of = [&](uint32_t d) { return (g & 2) ? d >> 8 : d; };
+
+  StepMx st[2];
+  load(st[0], 0);
+  load(st[1], 1);
+  f32x4_t acc[8];
+  for (int s0 = 0; s0 < width; s0 += 64) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
+    for (int w = 0; w < n1; ++w) {
+      const int k1 = (w * kWaves + wave) * 128;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (k1 < emb) {
+          stage(st[u]);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            if (p && k1 + 64 >= emb) continue;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const u32x4_t v = codes(t, p);
+              const uint32_t s = code_of(scale[wave][p][16 * t + c]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                acc[4 * u + t] = mfma(as_bf16(st[u].x[2 * p + h]), mx_values(v, h, s), acc[4 * u + t]);
+            }
           }
         }
+        load(st[u], u);
       }
+    }
+    // the wave's own LDS from here on holds its sums, until all have read them
+    wave_lds_fence();
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (4 * g + r >= nrows) continue;
+    for (int r = 0; r < 4; ++r) {
+      if (4 * g + r >= nrows) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (n0 + 16 * j < emb) po[r][n0 + 16 * j + c] = acc[j][r];
+      for (int j = 0; j < 8; ++j) lds.red[wave][4 * g + r][16 * j + c] = acc[j][r];
+    }
+    __syncthreads();
+    few_swiglu(lds, nrows, s0);
+    __syncthreads();
+  }
+
+  const auto clear = [&]() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
+  };
+  const auto a_of = [&](int k, bf16x8_t& hi, bf16x8_t& lo) {
+    hi = as_bf16(ld16(&lds.a_hi[c][k]));
+    lo = as_bf16(ld16(&lds.a_lo[c][k]));
+  };
+  const auto store = [&](int n0) {
+    wave_lds_fence();  // `share` is read again, not kept in registers
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * g + r;
+      if (row >= nrows) continue;
+      float* d = q.part + lds.share[row] + n0 + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n0 + 16 * j < emb) d[16 * j] = acc[j][r];
+    }
+  };
+  if (!narrow) {
+    for (int n0 = wave * 128; n0 < emb; n0 += kWaves * 128) {
+      clear();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        stage(st[u]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            bf16x8_t ah, al;
+            a_of(64 * p + 16 * g + 8 * h, ah, al);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const bf16x8_t v = mx_values(codes(t, p), h, code_of(scale[wave][p][16 * t + c]));
+              acc[4 * u + t] = mfma(al, v, mfma(ah, v, acc[4 * u + t]));
+            }
+          }
+        }
+        load(st[u], u);
+      }
+      store(n0);
+    }
+  } else {
+    for (int n0 = wave * 128; n0 < emb; n0 += 2 * kWaves * 128) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (n0 + u * kWaves * 128 < emb) {
+          clear();
+          wave_lds_fence();
+          scale[wave][0][lane] = st[u].scale[0];
+          scale[wave][1][lane] = st[u].scale[1];
+          wave_lds_fence();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            bf16x8_t ah, al;
+            a_of(16 * g + 8 * h, ah, al);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const bf16x8_t v = mx_values(st[u].v[j], h, code_of(scale[wave][j >> 2][16 * (j & 3) + c]));
+              acc[j] = mfma(al, v, mfma(ah, v, acc[j]));
+            }
+          }
+          store(n0 + u * kWaves * 128);
+        }
+        load(st[u], u);
       }
     }
   }
@@ -405,27 +719,40 @@ __global__ __launch_bounds__(kSumWaves * 64) void few_sum_kernel(int k, int emb,
                                                                  const float* __restrict__ topk_w,
                                                                  uint16_t* __restrict__ y) {
   __shared__ f32x4_t red[kSumWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.y;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), t = blockIdx.y;
   const int n = blockIdx.x * 256 + 4 * lane;
-  const int nc = n < emb ? n : 0;
+  const float* p = part + (int64_t)t * k * ns * emb + (n < emb ? n : 0);
+  int id = -1;
+  float w = 0;
+  if (lane < k) id = topk_idx[t * k + lane], w = topk_w[t * k + lane];
   f32x4_t acc = {0, 0, 0, 0};
-  const float* p = part + (int64_t)t * k * ns * emb + nc;
-#pragma unroll 8
-  for (int r = wave; r < k * ns; r += kSumWaves) {
-    const int j = t * k + r / ns;
-    // an expert id out of range has no share
-    const float w = (unsigned)topk_idx[j] < (unsigned)E ? topk_w[j] : 0.0f;
-    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + (int64_t)r * emb);
-    if ((unsigned)topk_idx[j] < (unsigned)E) {
+  const int rows = k * ns;
+  constexpr int kBatch = 12;
+  for (int r0 = wave; r0 < rows; r0 += kSumWaves * kBatch) {
+    f32x4_t v[kBatch];
+    const int jl = (r0 + lane * kSumWaves) / ns;  // lane i: the pick of the batch's row i
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = min(r0 + i * kSumWaves, rows - 1);
+      v[i] = *reinterpret_cast<const f32x4_t*>(p + (int64_t)r * emb);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = r0 + i * kSumWaves;
+      const int j = min(__builtin_amdgcn_readlane(jl, i), k - 1);
+      const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+      // an expert id out of range has no share: its rows hold nothing
+      if (r < rows && (unsigned)__builtin_amdgcn_readlane(id, j) < (unsigned)E) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[u] = __builtin_fmaf(wj, v[i][u], acc[u]);
+      }
     }
   }
   red[wave][lane] = acc;
   __syncthreads();
   if (wave) return;
 #pragma unroll
-  for (int w = 1; w < kSumWaves; ++w) acc += red[w][lane];
+  for (int i = 1; i < kSumWaves; ++i) acc += red[i][lane];
   if (n < emb) st8(y + (int64_t)t * emb + n, u32x2_t{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])});
 }
 
@@ -439,20 +766,30 @@ struct FewPlan {
 FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k) {
   FewPlan p;
   const int S = (int)T * k, experts = S < E ? S : E;
-  p.slice = kCols;
-  while (2 * p.slice <= kFewMaxSlice && (int64_t)experts * ((mlp + 2 * p.slice - 1) / (2 * p.slice)) >= 512) p.slice *= 2;
+  p.slice = (int64_t)experts * ((mlp + 127) / 128) >= 512 ? 128 : 64;
   p.ns = (mlp + p.slice - 1) / p.slice;
   const int most = experts + S / kRows;
   p.tiles = most < S ? most : S;
-  // 64 rows a wave, in at most 8 workgroups along emb
-  const int ways = (emb + kLogitWaves * 64 - 1) / (kLogitWaves * 64);
-  const int splits = ways < 8 ? ways : 8;
-  p.run = ((emb + kLogitWaves * splits - 1) / (kLogitWaves * splits) + 3) / 4 * 4;
+  // a router wave takes 64 rows of emb, more where that would cut emb into more than 16
+  p.run = (emb + kLogitWaves * 16 * 64 - 1) / (kLogitWaves * 16 * 64) * 64;
   p.splits = (emb + kLogitWaves * p.run - 1) / (kLogitWaves * p.run);
   return p;
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+template <bool PICK>
+void launch_experts(const FewArgs& q, hipStream_t st) {
+  const dim3 block(kWaves * 64);
+  if (!q.wt.wi) {
+    const dim3 grid(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks);
+    few_experts_mx_kernel<PICK><<<grid, block, 0, st>>>(q);
+  } else if (q.slice == 64) {
+    few_experts_kernel<false, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
+  } else {
+    few_experts_kernel<true, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
+  }
+}
 
 }  // namespace
 
@@ -467,23 +804,20 @@ hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t*
   const FewPlan p = few_plan(T, emb, mlp, E, k);
   double* logits = static_cast<double*>(ws);
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + up256((size_t)p.splits * T * E * 8));
+  const bool pick = wr && T <= kWaves && T * k <= 64;
   if (wr) {
     const dim3 grid((E + 15) / 16, p.splits), block(kLogitWaves * 64);
-    const int nt = ((int)T + 15) / 16;
-    if (nt == 1) few_logits_kernel<1><<<grid, block, 0, stream>>>((int)T, emb, E, p.run, x, wr, logits);
-    else if (nt == 2) few_logits_kernel<2><<<grid, block, 0, stream>>>((int)T, emb, E, p.run, x, wr, logits);
+    if (T <= 16) few_logits_kernel<1><<<grid, block, 0, stream>>>((int)T, emb, E, p.run, x, wr, logits);
+    else if (T <= 32) few_logits_kernel<2><<<grid, block, 0, stream>>>((int)T, emb, E, p.run, x, wr, logits);
     else few_logits_kernel<4><<<grid, block, 0, stream>>>((int)T, emb, E, p.run, x, wr, logits);
-    few_topk_kernel<<<dim3((unsigned)T), dim3(64), 0, stream>>>((int)T, E, k, p.splits, logits, bias, topk_idx, topk_w);
+    if (!pick)
+      few_topk_kernel<<<dim3((unsigned)T), dim3(64), 0, stream>>>((int)T, E, k, p.splits, logits, bias, topk_idx, topk_w);
   }
-  const dim3 grid(p.tiles * p.ns);
-  if (wt.wi)
-    few_experts_kernel<false, 4><<<grid, dim3(256), 0, stream>>>((int)T * k, k, emb, mlp, E, p.slice, p.ns, x, topk_idx, wt,
-                                                                 part);
-  else
-    few_experts_kernel<true, 4><<<grid, dim3(256), 0, stream>>>((int)T * k, k, emb, mlp, E, p.slice, p.ns, x, topk_idx, wt,
-                                                                part);
-  few_sum_kernel<<<dim3((emb + 255) / 256, (unsigned)T), dim3(kSumWaves * 64), 0, stream>>>(k, emb, E, p.ns, part, topk_idx,
-                                                                                          topk_w, y);
+  const FewArgs q{(int)T, k, emb, mlp, E, p.slice, p.ns, p.tiles * p.ns, p.splits, x, logits, bias, topk_idx, topk_w, wt, part};
+  if (pick) launch_experts<true>(q, stream);
+  else launch_experts<false>(q, stream);
+  few_sum_kernel<<<dim3((emb + 255) / 256, (unsigned)T), dim3(kSumWaves * 64), 0, stream>>>(
+      k, emb, E, p.ns, part, topk_idx, topk_w, y);
   return hipGetLastError();
 }
 
