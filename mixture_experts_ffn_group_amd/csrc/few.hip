@@ -22,7 +22,7 @@ namespace {
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kRows = 16;   // rows of a tile: the matrix instruction's side
-constexpr int kWaves = 8;           // waves of a workgroup of the experts' kernels
+constexpr int kWaves = 4;           // waves of a workgroup of the experts' kernels
 constexpr int kFewMaxSlice = 128;  // most mlp columns of a workgroup
 
 // ---------------------------------------------------------------- router
@@ -330,7 +330,7 @@ struct FewArgs {
 // A wave's weight steps, those of the first product and then those of the second, form one sequence of which two are
 // always in flight, over the barriers between the products too: the second product's first weights arrive while the
 // first one's sums go through LDS.
-// PICK (T <= kWaves, T*k <= 64): every workgroup first picks the experts from the logits, a wave a token, instead of
+// PICK (T <= 8, T*k <= 64): every workgroup first picks the experts from the logits, a wave a token, instead of
 // waiting for another kernel to do it; workgroup 0 writes the routing.
 struct FewLds {
   union {
@@ -352,16 +352,16 @@ __device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds& lds
   nrows = slot = 0;
   const int S = q.T * q.k;
   if constexpr (PICK) {
-    if (wave < q.T) {
+    for (int t = wave; t < q.T; t += kWaves) {
       int pick;
       double logit;
-      few_pick(q.T, q.E, q.k, q.splits, wave, q.logits, q.bias, lane, pick, logit);
-      if (lane < q.k) lds.picks[wave * q.k + lane] = pick;
+      few_pick(q.T, q.E, q.k, q.splits, t, q.logits, q.bias, lane, pick, logit);
+      if (lane < q.k) lds.picks[t * q.k + lane] = pick;
       if (blockIdx.x == 0) {
         const float w = few_weight(q.k, logit, lane);
         if (lane < q.k) {
-          q.topk_idx[wave * q.k + lane] = pick;
-          q.topk_w[wave * q.k + lane] = w;
+          q.topk_idx[t * q.k + lane] = pick;
+          q.topk_w[t * q.k + lane] = w;
         }
       }
     }
@@ -402,7 +402,7 @@ __device__ __forceinline__ void few_swiglu(FewLds& lds, int nrows, int s0) {
 __device__ __forceinline__ const char* bytes(const void* p) { return static_cast<const char*>(p); }
 
 template <bool WIDE, bool PICK>
-__global__ __launch_bounds__(kWaves * 64, WIDE ? 2 : 4) void few_experts_kernel(FewArgs q) {
+__global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) {
   __shared__ __align__(16) FewLds lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -495,16 +495,12 @@ __global__ __launch_bounds__(kWaves * 64, WIDE ? 2 : 4) void few_experts_kernel(
         load(st[u], u);
       }
     }
-    // The lane's place and the rows' addresses are made anew for each block: kept over the loop they would not fit the
-    // 128 registers that two workgroups a compute unit allow, and a spill's reload waits for the weights in flight.
-    int zero = 0;
-    asm volatile("" : "+s"(zero)::"memory");
-    const int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
-    const int n = n0 + 8 * (l & 15);
+    wave_lds_fence();  // `share` is read again, not kept in registers
+    const int n = n0 + 8 * c;
     if (n >= emb) continue;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = 4 * (l >> 4) + r;
+      const int row = 4 * g + r;
       if (row >= nrows) continue;
       float* d = q.part + lds.share[row] + n;
       *reinterpret_cast<f32x4_t*>(d) = f32x4_t{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
@@ -763,10 +759,16 @@ struct FewPlan {
   int tiles;           // most tiles of 16 rows that the routing can give
 };
 
-FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k) {
+FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
   FewPlan p;
   const int S = (int)T * k, experts = S < E ? S : E;
-  p.slice = (int64_t)experts * ((mlp + 127) / 128) >= 512 ? 128 : 64;
+  // Slices of 128 columns are read in longer runs and leave half the shares, slices of 64 give twice the workgroups, and
+  // a compute unit reads 46 GB/s at most. us at emb 2048, mlp 768, top-8 of 128, slices of 64 against 128, by the
+  // workgroups that 128 gives: 96: 44 / 56, 144: 67 / 61, 192: 70 / 64, 288: 99 / 108, 384: 105 / 112 (a second
+  // workgroup for some compute units), 576: 136 / 121; on MXFP8 weights, whose rows of wo are only 64 bytes long in slices of
+  // 64: 96: 37 / 48, 144: 50 / 50, 288: 81 / 72, 576: 96 / 82.
+  const int64_t wide = (int64_t)experts * ((mlp + 127) / 128);
+  p.slice = wide >= 144 && (mx || wide <= 256 || wide >= 448) ? 128 : 64;
   p.ns = (mlp + p.slice - 1) / p.slice;
   const int most = experts + S / kRows;
   p.tiles = most < S ? most : S;
@@ -781,30 +783,28 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 template <bool PICK>
 void launch_experts(const FewArgs& q, hipStream_t st) {
   const dim3 block(kWaves * 64);
-  if (!q.wt.wi) {
-    const dim3 grid(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks);
-    few_experts_mx_kernel<PICK><<<grid, block, 0, st>>>(q);
-  } else if (q.slice == 64) {
+  if (!q.wt.wi)
+    few_experts_mx_kernel<PICK><<<dim3(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks), block, 0, st>>>(q);
+  else if (q.slice == 64)
     few_experts_kernel<false, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
-  } else {
+  else
     few_experts_kernel<true, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
-  }
 }
 
 }  // namespace
 
 size_t few_workspace(int64_t T, int emb, int mlp, int E, int k) {
-  const FewPlan p = few_plan(T, emb, mlp, E, k);
-  return up256((size_t)p.splits * T * E * 8) + up256((size_t)T * k * p.ns * emb * 4);
+  const FewPlan p = few_plan(T, emb, mlp, E, k, false), m = few_plan(T, emb, mlp, E, k, true);
+  return up256((size_t)p.splits * T * E * 8) + up256((size_t)T * k * (p.ns > m.ns ? p.ns : m.ns) * emb * 4);
 }
 
 hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t* x, const float* wr, const float* bias,
                       int32_t* topk_idx, float* topk_w, const FewWeights& wt, uint16_t* y, void* ws, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const FewPlan p = few_plan(T, emb, mlp, E, k);
+  const FewPlan p = few_plan(T, emb, mlp, E, k, !wt.wi);
   double* logits = static_cast<double*>(ws);
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + up256((size_t)p.splits * T * E * 8));
-  const bool pick = wr && T <= kWaves && T * k <= 64;
+  const bool pick = wr && T <= 8 && T * k <= 64;
   if (wr) {
     const dim3 grid((E + 15) / 16, p.splits), block(kLogitWaves * 64);
     if (T <= 16) few_logits_kernel<1><<<grid, block, 0, stream>>>((int)T, emb, E, p.run, x, wr, logits);
