@@ -494,6 +494,22 @@ def _call(fn, dev, *args):
         _lib.check(status, fn)
 
 
+def _call_raw(fn, dev, *args):
+    """_call with pointers for tensors already: the short way for the calls of a decode step."""
+    i = dev.index
+    if i != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call_raw(fn, dev, *args)
+    stream = _raw_stream(i) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    status = _entry(fn)(*args, stream)
+    if status != _lib.MOE_OK:
+        _lib.check(status, fn)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 @functools.lru_cache(maxsize=256)
 def _route_shape(T, E, k):
     return C.byref(_lib.shape(T, 64, 64, E, k))
@@ -796,7 +812,8 @@ def _few(fn, x, weights, mlp, E, k, wr, bias, topk_idx, topk_w, workspace, out):
     s, n = _few_plan(T, emb, mlp, E, k)
     ws = _workspace(workspace, n, dev)
     y = out if out is not None else torch.empty((T, emb), dtype=torch.bfloat16, device=dev)
-    _call(fn, dev, s, x, wr, bias, topk_idx, topk_w, *weights, y, ws, ws.numel())
+    _call_raw(fn, dev, s, x.data_ptr(), _at(wr), _at(bias), topk_idx.data_ptr(), topk_w.data_ptr(),
+              *[w.data_ptr() for w in weights], y.data_ptr(), ws.data_ptr(), ws.numel())
     return y, topk_idx, topk_w
 
 
@@ -859,7 +876,7 @@ def norm(x: torch.Tensor, weight: torch.Tensor | None = None, offset: float = 0.
     wt = _weight_type(weight, "weight", emb, dev)
     _need_like(out, "out", (T, emb), torch.bfloat16, dev)
     y = out if out is not None else _bf16_like(x)
-    _call("moe_norm", dev, T, emb, x, ty, weight, wt, offset, eps, y)
+    _call_raw("moe_norm", dev, T, emb, x.data_ptr(), ty, _at(weight), wt, offset, eps, y.data_ptr())
     return y
 
 
@@ -947,7 +964,8 @@ def block_out(res: torch.Tensor, y: torch.Tensor | None = None, ys: torch.Tensor
     o = out if out is not None else torch.empty_like(res)
     xn = _bf16_like(res) if next_norm else None
     yo = _bf16_like(res) if want_y else None
-    _call("moe_block_out", dev, T, emb, b, res, y, k, ys, slot_row, topk_w, o, xn, yo)
+    _call_raw("moe_block_out", dev, T, emb, b, res.data_ptr(), _at(y), k, _at(ys), _at(slot_row), _at(topk_w),
+              o.data_ptr(), _at(xn), _at(yo))
     return dict(out=o, xn=xn, y=yo)
 
 
