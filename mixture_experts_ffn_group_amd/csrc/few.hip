@@ -320,6 +320,10 @@ struct FewArgs {
   float* topk_w;
   FewWeights wt;
   float* part;
+  // the products in kernels of their own: cuts of emb (rows of each) and of the output columns; hpart: the first one's
+  // sums [slot][slice][cut][64 gate, 64 up]
+  int cuts, run;
+  float* hpart;
 };
 
 // Workgroup (tile, slice): the tile's rows, and `slice` (64 or 128) of its expert's mlp columns, 64 at a time in the
@@ -330,8 +334,13 @@ struct FewArgs {
 // A wave's weight steps, those of the first product and then those of the second, form one sequence of which two are
 // always in flight, over the barriers between the products too: the second product's first weights arrive while the
 // first one's sums go through LDS.
+// PART: kFused, both products; or, where that gives less than a workgroup a compute unit, kFirst and kSecond in kernels
+// of their own, the first one's contraction (emb) and the second one's columns cut over blockIdx.y.
 // PICK (T <= 8, T*k <= 64): every workgroup first picks the experts from the logits, a wave a token, instead of
 // waiting for another kernel to do it; workgroup 0 writes the routing.
+enum { kFused = 0, kFirst = 1, kSecond = 2 };
+constexpr int kMaxCuts = 4;
+
 struct FewLds {
   union {
     float red[kWaves][kRows][128];  // first product: each wave's sums; MXFP8: before and after, the wave's step
@@ -357,7 +366,7 @@ __device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds& lds
       double logit;
       few_pick(q.T, q.E, q.k, q.splits, t, q.logits, q.bias, lane, pick, logit);
       if (lane < q.k) lds.picks[t * q.k + lane] = pick;
-      if (blockIdx.x == 0) {
+      if (blockIdx.x == 0 && blockIdx.y == 0) {
         const float w = few_weight(q.k, logit, lane);
         if (lane < q.k) {
           q.topk_idx[t * q.k + lane] = pick;
@@ -378,6 +387,15 @@ __device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds& lds
   return e >= 0;
 }
 
+// Row r, column n of the second product's left operand. It enters as the sum of two bf16 numbers, 16 bits of it: the
+// matrix cores are idle most of the time, so the layer's bf16 rounding of a is not needed here.
+__device__ __forceinline__ void few_set_a(FewLds& lds, int r, int n, float gate, float up) {
+  const float a = silu_f(gate) * up;
+  const uint16_t hi = (uint16_t)pack_bf16x2(a, 0.0f);
+  lds.a_hi[r][n] = hi;
+  lds.a_lo[r][n] = (uint16_t)pack_bf16x2(a - bf16_to_f32(hi), 0.0f);
+}
+
 // The waves' sums of 64 gate and 64 up columns -> SwiGLU -> a's columns s0...
 __device__ __forceinline__ void few_swiglu(FewLds& lds, int nrows, int s0) {
   for (int i = threadIdx.x; i < kRows * 64; i += kWaves * 64) {
@@ -390,18 +408,47 @@ __device__ __forceinline__ void few_swiglu(FewLds& lds, int nrows, int s0) {
         up += lds.red[w][r][64 + n];
       }
     }
-    // The product enters the second one as the sum of two bf16 numbers, 16 bits of it: the matrix cores are idle most
-    // of the time, so the layer's bf16 rounding of a is not needed here.
-    const float a = silu_f(gate) * up;
-    const uint16_t hi = (uint16_t)pack_bf16x2(a, 0.0f);
-    lds.a_hi[r][s0 + n] = hi;
-    lds.a_lo[r][s0 + n] = (uint16_t)pack_bf16x2(a - bf16_to_f32(hi), 0.0f);
+    few_set_a(lds, r, s0 + n, gate, up);
+  }
+}
+
+// kFirst: the waves' sums to hpart.
+__device__ __forceinline__ void few_store_h(const FewArgs& q, const FewLds& lds, int nrows, int sl) {
+  for (int i = threadIdx.x; i < nrows * 128; i += kWaves * 64) {
+    const int r = i >> 7, n = i & 127;
+    float h = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) h += lds.red[w][r][n];
+    q.hpart[(((int64_t)lds.rows[r] * q.ns + sl) * q.cuts + blockIdx.y) * 128 + n] = h;
+  }
+}
+
+// kSecond: hpart -> SwiGLU -> a.
+__device__ __forceinline__ void few_load_h(const FewArgs& q, FewLds& lds, int nrows, int sl) {
+  const int n = threadIdx.x & 63;
+#pragma unroll
+  for (int it = 0; it < kRows / kWaves; ++it) {
+    if (it * kWaves >= nrows) continue;  // rows past the last: their results are not used
+    const int r = it * kWaves + (threadIdx.x >> 6);
+    const float* h = q.hpart + ((int64_t)lds.rows[r < nrows ? r : 0] * q.ns + sl) * q.cuts * 128 + n;
+    float g[kMaxCuts], u[kMaxCuts];
+#pragma unroll
+    for (int i = 0; i < kMaxCuts; ++i) {
+      const int at = min(i, q.cuts - 1) * 128;
+      g[i] = h[at];
+      u[i] = h[at + 64];
+    }
+    float gate = 0, up = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxCuts; ++i)
+      if (i < q.cuts && r < nrows) gate += g[i], up += u[i];
+    few_set_a(lds, r, n, gate, up);
   }
 }
 
 __device__ __forceinline__ const char* bytes(const void* p) { return static_cast<const char*>(p); }
 
-template <bool WIDE, bool PICK>
+template <int PART, bool WIDE, bool PICK>
 __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) {
   __shared__ __align__(16) FewLds lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -413,24 +460,27 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
   const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
   // lanes past the last row compute on the first one; their rows of the results are not used
   const uint32_t xrow = (uint32_t)__shfl(slot, c < nrows ? c : 0) / (uint32_t)q.k;
-  // read after the first product's barrier
-  if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb;
+  // read after a barrier
+  if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb, lds.rows[lane] = slot;
 
   // The sequence of a wave's steps: n1 pairs of the first product (WIDE: a step for each 64 of the slice's 128 columns;
   // else two steps of its 64), then one step per 32 columns of the slice for each of its output blocks of 128 columns.
   // Steps past the wave's share, and past the end, load the same few words over and over: loads are never skipped, so
   // that the wait for a step counts on those behind.
   constexpr int kPair = WIDE ? 32 : 64;  // rows of emb in a pair
-  const int n1 = (emb + kWaves * kPair - 1) / (kWaves * kPair);
-  int lw = 0, ln = wave * 128, lk = 0;
+  const int kb = PART == kFirst ? blockIdx.y * q.run : 0, ke = PART == kFirst ? min(emb, kb + q.run) : emb;
+  const int n1 = PART == kSecond ? 0 : (ke - kb + kWaves * kPair - 1) / (kWaves * kPair);
+  const int nb = PART == kFirst ? emb : ((PART == kSecond ? blockIdx.y * kWaves : 0) + wave) * 128;  // the wave's blocks
+  const int nstride = (PART == kSecond ? q.cuts : 1) * kWaves * 128;
+  int lw = 0, ln = nb, lk = 0;
   const int64_t ld1 = 4 * (int64_t)mlp, ld2 = 2 * (int64_t)emb;  // bytes from row to row
   const uint32_t lane1 = 8 * g * (uint32_t)ld1 + 2 * (c < 8 ? 8 * c : mlp + 8 * (c - 8));
   const uint32_t lane2 = 8 * g * (uint32_t)ld2 + 16 * c;
   const uint32_t xlane = 2 * (xrow * (uint32_t)emb + 8 * g);
   const auto load = [&](StepBf16& st, int u) {  // u: which of the pair
-    const bool first = lw < n1;
-    const int k1 = (lw * kWaves + wave) * kPair + (WIDE ? 0 : 32 * u);
-    const bool real = first ? k1 < emb && (!WIDE || 64 * u < width) : ln < emb;
+    const bool first = PART == kFirst || (PART == kFused && lw < n1);
+    const int k1 = kb + (lw * kWaves + wave) * kPair + (WIDE ? 0 : 32 * u);
+    const bool real = first ? k1 < ke && (!WIDE || 64 * u < width) : ln < emb;
     // emb is a multiple of 64: the last block may have 64 columns, the other half then takes the first ones
     const uint32_t l2 = ln + 64 >= emb && c >= 8 ? lane2 - 128 : lane2;
     const char* p1 = bytes(q.wt.wi) + ((int64_t)e * emb + k1) * ld1 + 2 * (m0 + (WIDE ? 64 * u : 0));
@@ -439,20 +489,24 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
             bytes(q.x) + (first && real ? 2 * k1 : 0), xlane);
     const bool wrap = lk + 32 >= width;
     lk = first ? lk : wrap ? 0 : lk + 32;
-    ln = !first && wrap ? ln + kWaves * 128 : ln;
+    ln = !first && wrap ? ln + nstride : ln;
     lw = u == 1 && first ? lw + 1 : lw;
   };
 
   StepBf16 st[2];
   load(st[0], 0);
   load(st[1], 1);
+  if constexpr (PART == kSecond) {
+    __syncthreads();  // the slots
+    few_load_h(q, lds, nrows, sl);
+  }
   f32x4_t sum[WIDE ? 2 : 1][8];
 #pragma unroll
   for (int u = 0; u < (WIDE ? 2 : 1); ++u)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[u][j] = f32x4_t{0, 0, 0, 0};
   for (int w = 0; w < n1; ++w) {
-    const bool on = (w * kWaves + wave) * kPair < emb;  // emb is a multiple of 64: both steps of a pair or none
+    const bool on = kb + (w * kWaves + wave) * kPair < ke;  // emb is a multiple of 64: both steps of a pair or none
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (on) {
@@ -464,7 +518,7 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
   }
 #pragma unroll
   for (int u = 0; u < (WIDE ? 2 : 1); ++u) {
-    if (64 * u >= width) continue;
+    if (PART == kSecond || 64 * u >= width) continue;
     if (u) __syncthreads();  // the first columns' sums have been read
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -474,12 +528,14 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
       *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{sum[u][4][r], sum[u][5][r], sum[u][6][r], sum[u][7][r]};
     }
     __syncthreads();
-    few_swiglu(lds, nrows, 64 * u);
+    if constexpr (PART == kFirst) few_store_h(q, lds, nrows, sl);
+    else few_swiglu(lds, nrows, 64 * u);
   }
+  if constexpr (PART == kFirst) return;
   __syncthreads();
 
   f32x4_t acc[8];
-  for (int n0 = wave * 128; n0 < emb; n0 += kWaves * 128) {
+  for (int n0 = nb; n0 < emb; n0 += nstride) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
     for (int kk = 0; kk < width; kk += 64) {
@@ -510,7 +566,7 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
 }
 
 // The same on MXFP8 weights.
-template <bool PICK>
+template <int PART, bool PICK>
 __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs q) {
   __shared__ __align__(16) FewLds lds;
   __shared__ uint32_t scale[kWaves][2][64];
@@ -529,18 +585,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
   const bool narrow = width == 64;  // of the second product's steps
   const uint32_t xrow = (uint32_t)__shfl(slot, c < nrows ? c : 0) / (uint32_t)q.k;
-  // read after the first product's barrier
-  if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb;
+  // read after a barrier
+  if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb, lds.rows[lane] = slot;
 
   // The sequence: for each 64 columns, n1 pairs of steps (gate, up) of 128 values of emb; then output blocks of 128
   // columns, one narrow or two wide steps each, an even number in all.
-  const int n1 = (emb + kWaves * 128 - 1) / (kWaves * 128);
+  const int kb = PART == kFirst ? blockIdx.y * q.run : 0, ke = PART == kFirst ? min(emb, kb + q.run) : emb;
+  const int n1 = PART == kSecond ? 0 : (ke - kb + kWaves * 128 - 1) / (kWaves * 128);
+  const int nb = PART == kFirst ? emb : ((PART == kSecond ? blockIdx.y * kWaves : 0) + wave) * 128;  // the wave's blocks
+  const int nstride = (PART == kSecond ? q.cuts : 1) * kWaves * 128;
   const uint32_t r8 = lane >> 3, unit = (lane & 7) ^ r8;  // wide: the lane's column of each eight, and its unit
-  int ls = 0, lw = 0, ln = wave * 128;
+  int ls = 0, lw = 0, ln = nb;
   const auto load = [&](StepMx& st, int u) {  // u: which of the pair
-    const bool first = ls < width;
-    const int k1 = (lw * kWaves + wave) * 128;
-    const bool real = first ? k1 < emb : ln < emb;
+    const bool first = PART == kFirst || (PART == kFused && ls < width);
+    const int k1 = kb + (lw * kWaves + wave) * 128;
+    const bool real = first ? ls < width && k1 < ke : ln < emb;
     const int64_t ld = first ? emb : mlp;
     // wide: the first column, and the values of K that are there (emb is a multiple of 64)
     const int n = first ? m0 + ls + (u ? mlp : 0) : ln + (narrow ? 0 : 64 * u);
@@ -576,7 +635,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     const bool pair = u == 1;
     ls = first && pair && wrap ? ls + 64 : ls;
     lw = !first || !pair ? lw : wrap ? 0 : lw + 1;
-    ln = !first && (narrow || pair) ? ln + kWaves * 128 : ln;
+    ln = !first && (narrow || pair) ? ln + nstride : ln;
   };
   // wide step -> LDS; then column tile t's 16 codes (unit 4p + g) and their scale code
   u32x4_t* my = reinterpret_cast<u32x4_t*>(lds.red[wave]);
@@ -594,15 +653,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   StepMx st[2];
   load(st[0], 0);
   load(st[1], 1);
+  if constexpr (PART == kSecond) {
+    __syncthreads();  // the slots
+    few_load_h(q, lds, nrows, sl);
+    __syncthreads();
+  }
   f32x4_t acc[8];
-  for (int s0 = 0; s0 < width; s0 += 64) {
+  for (int s0 = 0; s0 < (PART == kSecond ? 0 : width); s0 += 64) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
     for (int w = 0; w < n1; ++w) {
-      const int k1 = (w * kWaves + wave) * 128;
+      const int k1 = kb + (w * kWaves + wave) * 128;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if (k1 < emb) {
+        if (k1 < ke) {
           stage(st[u]);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
@@ -629,9 +693,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
       for (int j = 0; j < 8; ++j) lds.red[wave][4 * g + r][16 * j + c] = acc[j][r];
     }
     __syncthreads();
-    few_swiglu(lds, nrows, s0);
+    if constexpr (PART == kFirst) few_store_h(q, lds, nrows, sl);
+    else few_swiglu(lds, nrows, s0);
     __syncthreads();
   }
+  if constexpr (PART == kFirst) return;
 
   const auto clear = [&]() {
 #pragma unroll
@@ -654,7 +720,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     }
   };
   if (!narrow) {
-    for (int n0 = wave * 128; n0 < emb; n0 += kWaves * 128) {
+    for (int n0 = nb; n0 < emb; n0 += nstride) {
       clear();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -677,10 +743,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
       store(n0);
     }
   } else {
-    for (int n0 = wave * 128; n0 < emb; n0 += 2 * kWaves * 128) {
+    for (int n0 = nb; n0 < emb; n0 += 2 * nstride) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if (n0 + u * kWaves * 128 < emb) {
+        if (n0 + u * nstride < emb) {
           clear();
           wave_lds_fence();
           scale[wave][0][lane] = st[u].scale[0];
@@ -696,7 +762,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
               acc[j] = mfma(al, v, mfma(ah, v, acc[j]));
             }
           }
-          store(n0 + u * kWaves * 128);
+          store(n0 + u * nstride);
         }
         load(st[u], u);
       }
@@ -755,6 +821,7 @@ __global__ __launch_bounds__(kSumWaves * 64) void few_sum_kernel(int k, int emb,
 // Slices of mlp and cuts of emb in the router, from the shape alone (the workspace's size follows).
 struct FewPlan {
   int slice, ns;       // mlp columns of a workgroup, workgroups of a tile
+  int cuts, run1;      // of emb in the first product (rows of each) and of the second one's columns; 1: both fused
   int run, splits;     // rows of emb of a router wave, router workgroups along emb
   int tiles;           // most tiles of 16 rows that the routing can give
 };
@@ -770,6 +837,19 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
   const int64_t wide = (int64_t)experts * ((mlp + 127) / 128);
   p.slice = wide >= 144 && (mx || wide <= 256 || wide >= 448) ? 128 : 64;
   p.ns = (mlp + p.slice - 1) / p.slice;
+  // Few workgroups: the products in kernels of their own, cut in up to four along emb and along the output columns. us
+  // fused and cut, by the workgroups fused: 8 (emb 7168, mlp 128) 58 / 28, 18 (emb 4096, mlp 192) 44 / 25, 64 (emb 7168,
+  // mlp 2048) 93 / 44, 96 (emb 2048, mlp 768) 33 / 29, 128 (emb 2048, mlp 1024) 36 / 30, 192 (emb 2048, mlp 768) 41 / 41
+  // and on MXFP8 weights 32 / 38. A cut leaves each of the first product's waves a pair of steps at least.
+  const int64_t filled = (S + kRows - 1) / kRows;
+  const int64_t units = (experts > filled ? experts : filled) * p.ns;
+  p.cuts = 1;
+  p.run1 = emb;
+  if (p.slice == 64 && units <= 128 && emb >= 2 * 512) {
+    const int cuts = emb / 512 < kMaxCuts ? emb / 512 : kMaxCuts;
+    p.run1 = (emb + 128 * cuts - 1) / (128 * cuts) * 128;
+    p.cuts = (emb + p.run1 - 1) / p.run1;
+  }
   const int most = experts + S / kRows;
   p.tiles = most < S ? most : S;
   // a router wave takes 64 rows of emb, more where that would cut emb into more than 16
@@ -780,22 +860,31 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-template <bool PICK>
-void launch_experts(const FewArgs& q, hipStream_t st) {
+template <int PART, bool PICK>
+void launch_part(const FewArgs& q, hipStream_t st) {
   const dim3 block(kWaves * 64);
   if (!q.wt.wi)
-    few_experts_mx_kernel<PICK><<<dim3(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks), block, 0, st>>>(q);
+    few_experts_mx_kernel<PART, PICK><<<dim3(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks, PART ? q.cuts : 1), block,
+                                        0, st>>>(q);
   else if (q.slice == 64)
-    few_experts_kernel<false, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
-  else
-    few_experts_kernel<true, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
+    few_experts_kernel<PART, false, PICK><<<dim3(q.blocks, PART ? q.cuts : 1), block, 0, st>>>(q);
+  else if constexpr (PART == kFused)
+    few_experts_kernel<kFused, true, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
+}
+
+template <bool PICK>
+void launch_experts(const FewArgs& q, hipStream_t st) {
+  if (q.cuts == 1) return launch_part<kFused, PICK>(q, st);
+  launch_part<kFirst, PICK>(q, st);
+  launch_part<kSecond, false>(q, st);
 }
 
 }  // namespace
 
 size_t few_workspace(int64_t T, int emb, int mlp, int E, int k) {
   const FewPlan p = few_plan(T, emb, mlp, E, k, false), m = few_plan(T, emb, mlp, E, k, true);
-  return up256((size_t)p.splits * T * E * 8) + up256((size_t)T * k * (p.ns > m.ns ? p.ns : m.ns) * emb * 4);
+  return up256((size_t)p.splits * T * E * 8) + up256((size_t)T * k * (p.ns > m.ns ? p.ns : m.ns) * emb * 4) +
+         up256((size_t)T * k * ((mlp + 63) / 64) * kMaxCuts * 128 * 4);
 }
 
 hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t* x, const float* wr, const float* bias,
@@ -804,6 +893,7 @@ hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t*
   const FewPlan p = few_plan(T, emb, mlp, E, k, !wt.wi);
   double* logits = static_cast<double*>(ws);
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + up256((size_t)p.splits * T * E * 8));
+  float* hpart = part + up256((size_t)T * k * p.ns * emb * 4) / 4;
   const bool pick = wr && T <= 8 && T * k <= 64;
   if (wr) {
     const dim3 grid((E + 15) / 16, p.splits), block(kLogitWaves * 64);
@@ -813,7 +903,8 @@ hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t*
     if (!pick)
       few_topk_kernel<<<dim3((unsigned)T), dim3(64), 0, stream>>>((int)T, E, k, p.splits, logits, bias, topk_idx, topk_w);
   }
-  const FewArgs q{(int)T, k, emb, mlp, E, p.slice, p.ns, p.tiles * p.ns, p.splits, x, logits, bias, topk_idx, topk_w, wt, part};
+  const FewArgs q{(int)T, k, emb, mlp, E, p.slice, p.ns, p.tiles * p.ns, p.splits, x, logits, bias, topk_idx, topk_w, wt, part,
+                  p.cuts, p.run1, hpart};
   if (pick) launch_experts<true>(q, stream);
   else launch_experts<false>(q, stream);
   few_sum_kernel<<<dim3((emb + 255) / 256, (unsigned)T), dim3(kSumWaves * 64), 0, stream>>>(

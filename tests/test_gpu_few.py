@@ -14,7 +14,9 @@ DEV = "cuda:0"
 # T, emb, mlp, E, k: one token, one expert, k = E, more than one tile of 16 rows an expert, odd 64-column tails,
 # experts past one wave, many slices
 SHAPES = [(1, 64, 64, 1, 1), (1, 2048, 768, 128, 8), (5, 1088, 448, 60, 4), (16, 128, 64, 4, 4), (17, 192, 128, 1, 1),
-          (64, 64, 320, 3, 3), (33, 192, 128, 256, 8), (64, 128, 256, 8, 2), (3, 320, 2048, 70, 64), (64, 576, 192, 160, 8)]
+          (64, 64, 320, 3, 3), (33, 192, 128, 256, 8), (64, 128, 256, 8, 2), (3, 320, 2048, 70, 64), (64, 576, 192, 160, 8),
+          # few slices and a long contraction: the products in kernels of their own, cut
+          (50, 1088, 64, 3, 2), (64, 2112, 128, 1, 1), (7, 5248, 64, 16, 3), (4, 1536, 192, 5, 2)]
 
 
 def _bf(t):
