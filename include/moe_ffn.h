@@ -593,21 +593,27 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* shape, const moe_bf16_t* dy, const float
 
 /*
  * moe_ffn_fwd_few -- the whole layer for a few tokens (a decode step), T <= 64:
- *  router, experts and combine in four kernels (two on a given routing) that read the weights of
- *  each expert that has a token once, with no permute and no copy of rows.
+ *  router, experts and combine, with no permute and no copy of rows: the
+ *  weights of each expert that has a token are read once for up to 16 of its
+ *  tokens. Three kernels (router, experts, sum of their shares) for T <= 8 and
+ *  T*k <= 64, the first left out on a given routing; one more for more tokens
+ *  (the picks), and one more where experts and slices are few (the products
+ *  apart).
  *  wr [emb, E] fp32: the layer routes x itself; bias [E] fp32 or NULL (may
  *  hold -inf to disable an expert); topk_idx [T, k] int32 and topk_w [T, k]
  *  fp32 are outputs: the k largest of the logits x . wr + bias in descending
  *  order, ties to the lower id, and their softmax. Logits are summed and
- *  compared in 64 bits (moe_route's are a chain of fp32 additions, so that
- *  picks may differ where two logits lie within its rounding). A NaN logit
- *  counts as -inf; a pick of logit -inf has weight 0.
+ *  compared in 64 bits, to 2^-44 of their size (moe_route's are a chain of
+ *  fp32 additions, so that picks may differ where two logits lie within its
+ *  rounding). A NaN logit counts as less than -inf; a pick of either has
+ *  weight 0, but a token whose logits are all NaN has NaN weights.
  *  wr NULL: topk_idx and topk_w are inputs (from moe_route, moe_route_scored
  *  or the caller), bias is NULL. A pick whose id lies outside [0, E) takes no
  *  part. An expert may be picked twice by a token here.
  *  wi [E, emb, 2*mlp], wo [E, mlp, emb] bf16; y [T, emb] bf16 =
  *  sum_j topk_w[t, j] (silu(x wi_e[:, :mlp]) * (x wi_e[:, mlp:])) wo_e,
- *  summed in fp32, the SwiGLU output kept to 16 bits, y rounded once.
+ *  summed in fp32, the SwiGLU output kept to 16 bits, y rounded once. A pick
+ *  of weight 0 takes no part.
  *  ws: at least moe_workspace_bytes_few(shape) bytes (0: unsupported shape).
  *
  * moe_ffn_fwd_few_mx -- the same on MXFP8 weights (wi_codes, wi_scales, wo_codes and

@@ -87,15 +87,17 @@ __global__ __launch_bounds__(kLogitWaves * 64) void few_logits_kernel(int T, int
   }
 }
 
-// Order-preserving 64-bit key of expert e's logit: larger logit, larger key, -0 like +0, NaN like -inf; the low 8 bits
+// Order-preserving 64-bit key of expert e's logit: larger logit, larger key, -0 like +0, NaN below -inf; the low 8 bits
 // give equal logits (to 2^-44) to the lower id. 0 is no key.
+constexpr uint64_t kNanKey = 0x100;
 __device__ __forceinline__ uint64_t pick_key(double v, int e) {
-  if (v != v) v = -__builtin_inf();
+  if (v != v) return kNanKey | (uint64_t)(255 - e);
   if (v == 0) v = 0;
   const uint64_t u = (uint64_t)__double_as_longlong(v);
   return (((u >> 63) ? ~u : (u | 0x8000000000000000ull)) & ~0xffull) | (uint64_t)(255 - e);
 }
 __device__ __forceinline__ double pick_value(uint64_t k) {
+  if (k < 2 * kNanKey) return __builtin_nan("");
   return __longlong_as_double((long long)(((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k) & ~0xffull));
 }
 // Largest value of the wave, in every lane: the rows' maxima meet in scalar registers.
@@ -153,14 +155,14 @@ __device__ __forceinline__ void few_pick(int T, int E, int k, int splits, int t,
   logit = lane < k ? pick_value(mine) : -__builtin_inf();
 }
 
-// Weight of pick `lane`: the softmax over the k picks; a disabled expert's is 0.
+// Weight of pick `lane`: the softmax over the k picks; 0 of a disabled expert (-inf or NaN), NaN where all logits are.
 __device__ __forceinline__ float few_weight(int k, double logit, int lane) {
   const double l0 = __shfl(logit, 0);
-  const double w = lane < k && logit != -__builtin_inf() ? exp(logit - l0) : 0.0;
+  const double w = lane < k && logit > -__builtin_inf() ? exp(logit - l0) : 0.0;
   double s = w;
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m);
-  return s == 0 ? 0.0f : (float)(w / s);
+  return l0 != l0 ? __builtin_nanf("") : s == 0 ? 0.0f : (float)(w / s);
 }
 
 __global__ __launch_bounds__(64) void few_topk_kernel(int T, int E, int k, int splits, const double* __restrict__ logits,
@@ -803,8 +805,9 @@ __global__ __launch_bounds__(kSumWaves * 64) void few_sum_kernel(int k, int emb,
       const int r = r0 + i * kSumWaves;
       const int j = min(__builtin_amdgcn_readlane(jl, i), k - 1);
       const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
-      // an expert id out of range has no share: its rows hold nothing
-      if (r < rows && (unsigned)__builtin_amdgcn_readlane(id, j) < (unsigned)E) {
+      // an expert id out of range has no share: its rows hold nothing; and a weight of 0 takes no part, whatever a
+      // disabled expert's weights hold
+      if (r < rows && (unsigned)__builtin_amdgcn_readlane(id, j) < (unsigned)E && wj != 0.0f) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) acc[u] = __builtin_fmaf(wj, v[i][u], acc[u]);
       }
@@ -884,7 +887,12 @@ void launch_experts(const FewArgs& q, hipStream_t st) {
 size_t few_workspace(int64_t T, int emb, int mlp, int E, int k) {
   const FewPlan p = few_plan(T, emb, mlp, E, k, false), m = few_plan(T, emb, mlp, E, k, true);
   return up256((size_t)p.splits * T * E * 8) + up256((size_t)T * k * (p.ns > m.ns ? p.ns : m.ns) * emb * 4) +
-         up256((size_t)T * k * ((mlp + 63) / 64) * kMaxCuts * 128 * 4);
+         (p.cuts > 1 || m.cuts > 1 ? up256((size_t)T * k * (mlp / 64) * kMaxCuts * 128 * 4) : 0);
+}
+
+int64_t few_blocks(int64_t T, int emb, int mlp, int E, int k) {
+  const FewPlan p = few_plan(T, emb, mlp, E, k, false), m = few_plan(T, emb, mlp, E, k, true);
+  return (int64_t)p.tiles * (p.ns > m.ns ? p.ns : m.ns);
 }
 
 hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t* x, const float* wr, const float* bias,

@@ -99,6 +99,7 @@ struct FewWeights {
   const uint8_t *wic, *wis, *woc, *wos;  // MXFP8 codes [E, N, K] and scales [E][K/64][N][4]
 };
 size_t few_workspace(int64_t T, int emb, int mlp, int E, int k);
+int64_t few_blocks(int64_t T, int emb, int mlp, int E, int k);  // workgroups (256 lanes) of the experts' kernel
 hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t* x, const float* wr, const float* bias,
                       int32_t* topk_idx, float* topk_w, const FewWeights& wt, uint16_t* y, void* ws,
                       hipStream_t stream);

@@ -1105,6 +1105,9 @@ static int check_few(const moe_shape_t* s) {
   if (int rc = check_shape(s)) return rc;
   if (s->T > moe::kFewMaxTokens)
     return fail(MOE_ERR_UNSUPPORTED, "T (%lld) > %d tokens", (long long)s->T, moe::kFewMaxTokens);
+  // a grid holds fewer than 2^32 lanes
+  if (s->T > 0 && moe::few_blocks(s->T, s->emb, s->mlp, s->E, s->k) >= 1 << 24)
+    return fail(MOE_ERR_UNSUPPORTED, "too many slices of mlp");
   return MOE_OK;
 }
 

@@ -118,10 +118,12 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int waves, float (*sh)[1
   turn ^= 1;
 }
 
+constexpr int kGridRows = 1 << 21;  // rows along a grid's x: fewer than 2^32 lanes
+
 // Forward, a workgroup a row: KC chunks of 8 elements a lane. SRC 0: x itself (moe_norm), 1: y given, 2: y = sum over
 // the token's picks of expert rows.
 template <int KC, int SRC, bool XF32>
-__global__ __launch_bounds__(1024) void block_out_kernel(int emb, BlockArgs b, const void* res, const uint16_t* __restrict__ y,
+__global__ __launch_bounds__(1024) void block_out_kernel(int64_t T, int emb, BlockArgs b, const void* res, const uint16_t* __restrict__ y,
                                                          int k, const uint16_t* __restrict__ ys,
                                                          const int32_t* __restrict__ slot_row,
                                                          const float* __restrict__ topk_w, void* out,
@@ -130,7 +132,8 @@ __global__ __launch_bounds__(1024) void block_out_kernel(int emb, BlockArgs b, c
   constexpr bool kNt = KC > 1;  // few rows (KC 1) fit the caches, where the next kernel finds them
   int turn = 0;
   const int lane = threadIdx.x, G = blockDim.x, waves = G >> 6;
-  const int64_t t = blockIdx.x, base = t * emb;
+  const int64_t t = (int64_t)blockIdx.y * kGridRows + blockIdx.x, base = t * emb;
+  if (t >= T) return;
   const int nch = emb / 8;
   const float inv = 1.0f / emb;
 
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(1024) void block_out_kernel(int emb, BlockArgs b, c
       for (int u = 0; u < 8; ++u) v[i][u] = q[i][u];
   }
   if constexpr (SRC == 2) {
-    const int64_t S = (int64_t)gridDim.x * k;
+    const int64_t S = T * k;
     const int l = threadIdx.x & 63;
     int32_t my_r = -1;
     float my_w = 0;
@@ -504,12 +507,13 @@ BwdPlan bwd_plan(int64_t T, int emb) {
 }
 
 template <int KC, bool XF32>
-void fwd(unsigned T, int emb, const BlockArgs& b, const void* res, const uint16_t* y, int k, const uint16_t* ys,
+void fwd(int64_t T, int emb, const BlockArgs& b, const void* res, const uint16_t* y, int k, const uint16_t* ys,
          const int32_t* slot_row, const float* w, void* out, uint16_t* xn, uint16_t* y_out, hipStream_t st) {
-  const dim3 grid(T), block(lanes_of(emb, KC));
-  if (ys) block_out_kernel<KC, 2, XF32><<<grid, block, 0, st>>>(emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
-  else if (y) block_out_kernel<KC, 1, XF32><<<grid, block, 0, st>>>(emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
-  else block_out_kernel<KC, 0, XF32><<<grid, block, 0, st>>>(emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
+  const dim3 grid((unsigned)(T < kGridRows ? T : kGridRows), (unsigned)((T + kGridRows - 1) / kGridRows));
+  const dim3 block(lanes_of(emb, KC));
+  if (ys) block_out_kernel<KC, 2, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
+  else if (y) block_out_kernel<KC, 1, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
+  else block_out_kernel<KC, 0, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
 }
 
 template <int KC, bool XF32>
@@ -537,15 +541,14 @@ hipError_t launch_block_out(int64_t T, int emb, const BlockArgs& b, const void* 
                             const uint16_t* ys, const int32_t* slot_row, const float* topk_w, void* out, uint16_t* xn,
                             uint16_t* y_out, hipStream_t st) {
   if (T == 0) return hipSuccess;
-  const unsigned n = (unsigned)T;
   // Few rows: a chunk a lane, the shortest way through a row. Many: two, half the waves to add up (32768 rows of 2048:
   // 95 us against 106).
   if (emb <= 8192 && T <= 256) {
-    if (b.x_f32) fwd<1, true>(n, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
-    else fwd<1, false>(n, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
+    if (b.x_f32) fwd<1, true>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
+    else fwd<1, false>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
   } else {
-    if (b.x_f32) fwd<2, true>(n, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
-    else fwd<2, false>(n, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
+    if (b.x_f32) fwd<2, true>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
+    else fwd<2, false>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
   }
   return hipGetLastError();
 }

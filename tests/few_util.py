@@ -16,18 +16,20 @@ def f64(t):
 
 
 def route(x, wr, bias, k):
-    """Picks and weights: the k largest logits, ties to the lower id, and their softmax; 0 for -inf (or NaN)."""
+    """Picks and weights: the k largest logits, ties to the lower id, and their softmax. NaN counts as less than -inf;
+    the weight of either is 0, but NaN where all logits are NaN."""
     with np.errstate(invalid="ignore"):
         l = x @ wr
         if bias is not None:
             l = l + bias
-    l = np.where(np.isnan(l), -np.inf, l)
-    idx = np.argsort(-l, axis=1, kind="stable")[:, :k]
-    top = np.take_along_axis(l, idx, 1)
+    # descending, NaN last, equal ones by id
+    idx = np.stack([np.lexsort((np.arange(len(r)), -np.where(np.isnan(r), -np.inf, r), np.isnan(r))) for r in l])[:, :k]
+    top = np.take_along_axis(np.where(np.isnan(l), -np.inf, l), idx, 1)
+    lost = np.isnan(l).all(1, keepdims=True)
     first = np.where(np.isfinite(top[:, :1]), top[:, :1], 0)
     w = np.exp(top - first)
     s = w.sum(1, keepdims=True)
-    return idx.astype(np.int32), np.where(s > 0, w / np.where(s > 0, s, 1), 0)
+    return idx.astype(np.int32), np.where(lost, np.nan, np.where(s > 0, w / np.where(s > 0, s, 1), 0))
 
 
 def few(x, wi, wo, idx, w):
@@ -38,7 +40,7 @@ def few(x, wi, wo, idx, w):
     for t in range(T):
         for j in range(idx.shape[1]):
             e = idx[t, j]
-            if not 0 <= e < wi.shape[0]:
+            if not 0 <= e < wi.shape[0] or w[t, j] == 0:
                 continue
             h = x[t] @ wi[e]
             dh = (emb + 16) * U * (np.abs(x[t]) @ np.abs(wi[e]))

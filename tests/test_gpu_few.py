@@ -122,11 +122,12 @@ def test_masked_experts_ties_and_rows_of_nan():
     bias[40] = float("nan")
     bias[100] = bias[3] = 20
     h["x"][4] = 0                  # all logits equal but for the bias
-    h["x"][7, 9] = float("nan")    # every logit NaN: the k lowest ids with weight 0
+    h["x"][7, 9] = float("nan")    # every logit NaN: the k lowest ids, weights and y NaN
     ri, rw = fu.route(fu.f64(h["x"]), fu.f64(wr), fu.f64(bias), k)
     y, idx, w = moe.ffn_fwd_few(h["x"].to(DEV), d["wi"], d["wo"], k, wr=wr.to(DEV), bias=bias.to(DEV))
     assert np.array_equal(idx.cpu().numpy(), ri)
-    assert np.allclose(fu.f64(w), rw, rtol=4 * fu.U, atol=0)
+    assert np.allclose(fu.f64(w), rw, rtol=4 * fu.U, atol=0, equal_nan=True) and np.isnan(rw[7]).all()
+    assert torch.isnan(y[7]).all()
     keep = [t for t in range(T) if t != 7]
     ref, err = fu.few(fu.f64(h["x"])[keep], fu.f64(h["wi"]), fu.f64(h["wo"]), ri[keep], fu.f64(w)[keep])
     _close(y[keep], ref, err)
@@ -195,3 +196,18 @@ def test_two_streams_and_repeated_calls_give_the_same_bits():
     torch.cuda.synchronize()
     for o in outs:
         assert all(torch.equal(a, b) for a, b in zip(o, ref))
+
+
+def test_disabled_experts_weights_may_hold_anything():
+    """With fewer enabled experts than picks, disabled ones are picked with weight 0; what their weights hold (NaN,
+    infinities) does not reach y."""
+    T, emb, mlp, E, k = 20, 192, 64, 6, 5
+    h, d = _inputs(T, emb, mlp, E, k, seed=11)
+    bias = torch.tensor([0.0, -float("inf"), 0.0, -float("inf"), 0.0, float("nan")])
+    for e, v in ((1, float("nan")), (3, float("inf")), (5, float("nan"))):
+        d["wi"][e], d["wo"][e] = v, v
+    for n in (T, 3):
+        y, idx, w = moe.ffn_fwd_few(d["x"][:n], d["wi"], d["wo"], k, wr=d["wr"], bias=bias.to(DEV))
+        ri, rw = fu.route(fu.f64(h["x"])[:n], fu.f64(h["wr"]), fu.f64(bias), k)
+        assert np.array_equal(idx.cpu().numpy(), ri) and (ri[:, 3:] == [1, 3]).all() and (rw[:, 3:] == 0).all()
+        _close(y, *fu.few(fu.f64(h["x"])[:n], fu.f64(h["wi"]), fu.f64(h["wo"]), ri, fu.f64(w)))

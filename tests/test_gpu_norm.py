@@ -271,3 +271,17 @@ def test_graph_of_forward_and_backward_replays():
         ref = step(res.clone(), y.clone())
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+
+
+def test_more_rows_than_one_grid_dimension_holds():
+    """2^21 rows lie along a grid's first dimension; the rest, and none past the last, along the second."""
+    T, emb = 2 * 2 ** 21 + 77, 8
+    x = torch.randn((T, emb), device=DEV, generator=torch.Generator(DEV).manual_seed(1)).to(BF)
+    y = torch.full((T + 3, emb), 5.0, dtype=BF, device=DEV)
+    moe.norm(x, out=y[:T])
+    v = x.double()
+    ref = v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6)
+    assert bool(((y[:T].double() - ref).abs() <= (2.0 ** -8 + 64 * fu.U) * ref.abs()).all()) and (y[T:] == 5).all()
+    r = moe.block_out(x, ys=x, slot_row=torch.arange(T, dtype=torch.int32, device=DEV),
+                      topk_w=torch.ones((T, 1), device=DEV))
+    assert torch.equal(r["out"], (x.float() + x.float()).to(BF))
