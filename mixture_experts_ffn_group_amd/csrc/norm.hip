@@ -9,6 +9,8 @@
 //
 // The tensors go through non-temporal loads and stores: a copy of 512 MiB runs at 6.1-6.3 TB/s so,
 // at 5.5 without. Weights, which every row reads, stay cached.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 #include "lanes.h"
@@ -95,14 +97,16 @@ __device__ __forceinline__ void factor8(const void* w, bool f32, float offset, i
   for (int u = 0; u < 8; ++u) v[u] += offset;
 }
 
+// A row lies in L = 16 lanes, four rows a wave (rows of up to 256 elements), or in whole waves (L = 64).
+//
 // Sums over the `waves` waves of a row, of N values at once, in an order fixed by `waves`. Every wave of the workgroup
 // calls it the same number of times; `turn` alternates the LDS rows, so that one barrier a call is enough (a wave
 // writes a row again only after the barrier of the call between).
-template <int N>
+template <int L, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], int waves, float (*sh)[16][3], int& turn) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
-  if (waves == 1) return;
+  for (int n = 0; n < N; ++n) v[n] = L == 16 ? row_sum(v[n]) : wave_sum(v[n]);
+  if (L == 16 || waves == 1) return;
   const int wave = threadIdx.x >> 6, w0 = wave / waves * waves;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -118,12 +122,12 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int waves, float (*sh)[1
   turn ^= 1;
 }
 
-constexpr int kGridRows = 1 << 21;  // rows along a grid's x: fewer than 2^32 lanes
+constexpr int kGridRows = 1 << 21;  // workgroups along a grid's x: fewer than 2^32 lanes
 
-// Forward, a workgroup a row: KC chunks of 8 elements a lane. SRC 0: x itself (moe_norm), 1: y given, 2: y = sum over
+// Forward, a workgroup a row (L = 16: sixteen rows), KC chunks of 8 elements a lane. SRC 0: x itself (moe_norm), 1: y given, 2: y = sum over
 // the token's picks of expert rows.
-template <int KC, int SRC, bool XF32>
-__global__ __launch_bounds__(1024) void block_out_kernel(int64_t T, int emb, BlockArgs b, const void* res, const uint16_t* __restrict__ y,
+template <int L, int KC, int SRC, bool XF32>
+__global__ __launch_bounds__(L == 16 ? 256 : 1024) void block_out_kernel(int64_t T, int emb, BlockArgs b, const void* res, const uint16_t* __restrict__ y,
                                                          int k, const uint16_t* __restrict__ ys,
                                                          const int32_t* __restrict__ slot_row,
                                                          const float* __restrict__ topk_w, void* out,
@@ -131,8 +135,9 @@ __global__ __launch_bounds__(1024) void block_out_kernel(int64_t T, int emb, Blo
   __shared__ float sh[2][16][3];
   constexpr bool kNt = KC > 1;  // few rows (KC 1) fit the caches, where the next kernel finds them
   int turn = 0;
-  const int lane = threadIdx.x, G = blockDim.x, waves = G >> 6;
-  const int64_t t = (int64_t)blockIdx.y * kGridRows + blockIdx.x, base = t * emb;
+  const int G = L == 16 ? 16 : blockDim.x, lane = L == 16 ? threadIdx.x & 15 : threadIdx.x, waves = G >> 6;
+  const int64_t b0 = (int64_t)blockIdx.y * kGridRows + blockIdx.x;
+  const int64_t t = L == 16 ? b0 * 16 + (threadIdx.x >> 4) : b0, base = t * emb;
   if (t >= T) return;
   const int nch = emb / 8;
   const float inv = 1.0f / emb;
@@ -163,7 +168,7 @@ __global__ __launch_bounds__(1024) void block_out_kernel(int64_t T, int emb, Blo
     const int l = threadIdx.x & 63;
     int32_t my_r = -1;
     float my_w = 0;
-    if (l < k) {
+    if (L == 64 && l < k) {
       const int32_t r = slot_row[t * k + l];
       if (r >= 0 && r < S) my_r = r, my_w = topk_w ? topk_w[t * k + l] : 1.0f;
     }
@@ -180,8 +185,17 @@ __global__ __launch_bounds__(1024) void block_out_kernel(int64_t T, int emb, Blo
       int32_t rr[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        rr[u] = j0 + u < k ? __builtin_amdgcn_readlane(my_r, (j0 + u) & 63) : -1;
-        ww[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), (j0 + u) & 63));
+        if constexpr (L == 16) {
+          rr[u] = -1;
+          ww[u] = 0;
+          if (j0 + u < k) {
+            const int32_t r = slot_row[t * k + j0 + u];
+            if (r >= 0 && r < S) rr[u] = r, ww[u] = topk_w ? topk_w[t * k + j0 + u] : 1.0f;
+          }
+        } else {
+          rr[u] = j0 + u < k ? __builtin_amdgcn_readlane(my_r, (j0 + u) & 63) : -1;
+          ww[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), (j0 + u) & 63));
+        }
 #pragma unroll
         for (int i = 0; i < KC; ++i)
           if (rr[u] >= 0)
@@ -216,7 +230,7 @@ __global__ __launch_bounds__(1024) void block_out_kernel(int64_t T, int emb, Blo
 #pragma unroll
         for (int u = 0; u < 8; ++u) s[0] = __builtin_fmaf(v[i][u], v[i][u], s[0]);
       }
-      row_sums(s, waves, sh, turn);
+      row_sums<L>(s, waves, sh, turn);
       r *= rsqrtf(s[0] * inv + b.eps);
     }
     if (b.gate_mode == kGateToken) r *= load1(b.gate, b.gate_f32, t);
@@ -249,7 +263,7 @@ __global__ __launch_bounds__(1024) void block_out_kernel(int64_t T, int emb, Blo
 #pragma unroll
     for (int u = 0; u < 8; ++u) s[0] = __builtin_fmaf(v[i][u], v[i][u], s[0]);
   }
-  row_sums(s, waves, sh, turn);
+  row_sums<L>(s, waves, sh, turn);
   const float r = rsqrtf(s[0] * inv + b.eps);
 #pragma unroll
   for (int i = 0; i < KC; ++i) {
@@ -281,8 +295,8 @@ struct BwdRow {
   Raw<false> g[KC], y[KC];
 };
 
-template <int KC, bool AHEAD, bool XF32, bool HASY, bool NEXT, bool POST, bool CHG>
-__global__ __launch_bounds__(kBwdLanes) void block_out_bwd_kernel(int64_t T, int emb, int G, BlockArgs b, const void* dout,
+template <int L, int KC, bool AHEAD, bool XF32, bool HASY, bool NEXT, bool POST, bool CHG>
+__global__ __launch_bounds__(kBwdLanes) void block_out_bwd_kernel(int64_t T, int emb, int lanes, BlockArgs b, const void* dout,
                                                                   const uint16_t* __restrict__ y, const void* out,
                                                                   const uint16_t* __restrict__ dxn, void* dres,
                                                                   uint16_t* __restrict__ dy, void* __restrict__ dgate,
@@ -291,7 +305,7 @@ __global__ __launch_bounds__(kBwdLanes) void block_out_bwd_kernel(int64_t T, int
   __shared__ float sh[2][16][3];
   __shared__ float comb[kBwdLanes * 8];
   int turn = 0;
-  const int per = blockDim.x / G, grp = threadIdx.x / G, lane = threadIdx.x - grp * G, waves = G >> 6;
+  const int G = L == 16 ? 16 : lanes, per = blockDim.x / G, grp = threadIdx.x / G, lane = threadIdx.x - grp * G, waves = G >> 6;
   const float inv = 1.0f / emb;
   float acc[kAcc > 0 ? kAcc : 1][KC][8] = {};
   // the norms' factors stay in registers where there is room for them
@@ -359,7 +373,7 @@ __global__ __launch_bounds__(kBwdLanes) void block_out_bwd_kernel(int64_t T, int
         if constexpr (POST) s[2] = __builtin_fmaf(q.y[i][u], q.y[i][u], s[2]);
       }
     }
-    if constexpr (NEXT || POST) row_sums(s, waves, sh, turn);
+    if constexpr (NEXT || POST) row_sums<L>(s, waves, sh, turn);
     const float r = NEXT ? rsqrtf(s[0] * inv + b.eps) : 0.0f, c = r * r * (s[1] * inv);
     const float ry = POST ? rsqrtf(s[2] * inv + b.eps) : 1.0f;
     const bool token = HASY && b.gate_mode == kGateToken;
@@ -423,7 +437,7 @@ __global__ __launch_bounds__(kBwdLanes) void block_out_bwd_kernel(int64_t T, int
     if constexpr (HASY) {
       float cy = 0;
       if (POST || token) {
-        row_sums(sum, waves, sh, turn);
+        row_sums<L>(sum, waves, sh, turn);
         cy = ry * ry * (sum[0] * inv);
         if (token && dgate && lane == 0 && on) static_cast<float*>(dgate)[t] = sum[0] * ry;
       }
@@ -441,25 +455,36 @@ __global__ __launch_bounds__(kBwdLanes) void block_out_bwd_kernel(int64_t T, int
     }
   }
   if (!part) return;
-  // the groups' sums, then one partial row per sum
+  // the groups' sums (of one wave's four by lane exchanges), then one partial row per sum
+  const int sets = L == 16 ? blockDim.x >> 6 : per, set = L == 16 ? threadIdx.x >> 6 : grp;
+  const bool holds = L != 16 || (threadIdx.x & 63) < 16;
 #pragma unroll
   for (int a = 0; a < kAcc; ++a) {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int n = (i * G + lane) * 8;
       if (i * G * 8 >= emb) continue;
-      if (per > 1) {
-        __syncthreads();
+      if constexpr (L == 16) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) comb[u * kBwdLanes + threadIdx.x] = acc[a][i][u];
+        for (int u = 0; u < 8; ++u) {
+          acc[a][i][u] += __shfl_xor(acc[a][i][u], 16);
+          acc[a][i][u] += __shfl_xor(acc[a][i][u], 32);
+        }
+      }
+      if (sets > 1) {
         __syncthreads();
-        if (grp == 0) {
-          for (int p = 1; p < per; ++p)
+        if (holds) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) comb[u * kBwdLanes + set * G + lane] = acc[a][i][u];
+        }
+        __syncthreads();
+        if (set == 0 && holds) {
+          for (int p = 1; p < sets; ++p)
 #pragma unroll
             for (int u = 0; u < 8; ++u) acc[a][i][u] += comb[u * kBwdLanes + p * G + lane];
         }
       }
-      if (grp == 0 && n < emb) {
+      if (set == 0 && holds && n < emb) {
         f32x4_t* d = reinterpret_cast<f32x4_t*>(part + ((int64_t)a * gridDim.x + blockIdx.x) * emb + n);
         d[0] = f32x4_t{acc[a][i][0], acc[a][i][1], acc[a][i][2], acc[a][i][3]};
         d[1] = f32x4_t{acc[a][i][4], acc[a][i][5], acc[a][i][6], acc[a][i][7]};
@@ -489,8 +514,9 @@ __global__ __launch_bounds__(1024) void colsum_kernel(int P, int emb, const floa
   if (n < emb) dst[n] = s;
 }
 
-// Lanes that hold a row at kc chunks of 8 a lane: whole waves.
-int lanes_of(int emb, int kc) { return (emb / 8 + 64 * kc - 1) / (64 * kc) * 64; }
+// Lanes that hold a row at kc chunks of 8 a lane: 16, or whole waves.
+constexpr int kSubEmb = 256;  // longest row of 16 lanes
+int lanes_of(int emb, int kc) { return kc == 2 && emb <= kSubEmb ? 16 : (emb / 8 + 64 * kc - 1) / (64 * kc) * 64; }
 
 // The backward's shape: two chunks a lane while 512 lanes hold the row so, else four.
 struct BwdPlan {
@@ -506,22 +532,23 @@ BwdPlan bwd_plan(int64_t T, int emb) {
   return p;
 }
 
-template <int KC, bool XF32>
+template <int L, int KC, bool XF32>
 void fwd(int64_t T, int emb, const BlockArgs& b, const void* res, const uint16_t* y, int k, const uint16_t* ys,
          const int32_t* slot_row, const float* w, void* out, uint16_t* xn, uint16_t* y_out, hipStream_t st) {
-  const dim3 grid((unsigned)(T < kGridRows ? T : kGridRows), (unsigned)((T + kGridRows - 1) / kGridRows));
-  const dim3 block(lanes_of(emb, KC));
-  if (ys) block_out_kernel<KC, 2, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
-  else if (y) block_out_kernel<KC, 1, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
-  else block_out_kernel<KC, 0, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
+  const int64_t n = L == 16 ? (T + 15) / 16 : T;
+  const dim3 grid((unsigned)(n < kGridRows ? n : kGridRows), (unsigned)((n + kGridRows - 1) / kGridRows));
+  const dim3 block(L == 16 ? 256 : lanes_of(emb, KC));
+  if (ys) block_out_kernel<L, KC, 2, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
+  else if (y) block_out_kernel<L, KC, 1, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
+  else block_out_kernel<L, KC, 0, XF32><<<grid, block, 0, st>>>(T, emb, b, res, y, k, ys, slot_row, w, out, xn, y_out);
 }
 
-template <int KC, bool XF32>
+template <int L, int KC, bool XF32>
 void bwd(const BwdPlan& p, int64_t T, int emb, const BlockArgs& b, bool has_y, const void* dout, const uint16_t* y,
          const void* out, const uint16_t* dxn, void* dres, uint16_t* dy, void* dgate, float* part, hipStream_t st) {
   const bool post = b.post, chg = b.gate_mode == kGateChannel;
 #define MOE_BWD(H, N, P, C)                                                                                         \
-  block_out_bwd_kernel<KC, KC == 2 && !(XF32 && P && C), XF32, H, N, P, C><<<dim3(p.grid), dim3(p.per * p.G), 0, st>>>(T, emb, p.G, b, dout, y, \
+  block_out_bwd_kernel<L, KC, KC == 2 && !(XF32 && P && C), XF32, H, N, P, C><<<dim3(p.grid), dim3(p.per * p.G), 0, st>>>(T, emb, p.G, b, dout, y, \
                                                                                                 out, dxn, dres, dy, dgate, part)
   if (!has_y) MOE_BWD(false, true, false, false);
   else if (dxn && post && chg) MOE_BWD(true, true, true, true);
@@ -542,14 +569,15 @@ hipError_t launch_block_out(int64_t T, int emb, const BlockArgs& b, const void* 
                             uint16_t* y_out, hipStream_t st) {
   if (T == 0) return hipSuccess;
   // Few rows: a chunk a lane, the shortest way through a row. Many: two, half the waves to add up (32768 rows of 2048:
-  // 95 us against 106).
-  if (emb <= 8192 && T <= 256) {
-    if (b.x_f32) fwd<1, true>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
-    else fwd<1, false>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
-  } else {
-    if (b.x_f32) fwd<2, true>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
-    else fwd<2, false>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
-  }
+  // 95 us against 106), and short rows four a wave (400000 rows of 128, norm alone: 36 us against 98).
+  const auto go = [&](auto l, auto kc) {
+    if (b.x_f32) fwd<decltype(l)::value, decltype(kc)::value, true>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
+    else fwd<decltype(l)::value, decltype(kc)::value, false>(T, emb, b, res, y, k, ys, slot_row, topk_w, out, xn, y_out, st);
+  };
+  using std::integral_constant;
+  if (emb <= 8192 && T <= 256) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (emb > kSubEmb) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
   return hipGetLastError();
 }
 
@@ -560,13 +588,14 @@ hipError_t launch_block_out_bwd(int64_t T, int emb, const BlockArgs& b, bool has
                                 float* dnext, void* dgate, float* part, hipStream_t st) {
   const BwdPlan p = bwd_plan(T, emb);
   if (T > 0) {
-    if (p.kc == 2) {
-      if (b.x_f32) bwd<2, true>(p, T, emb, b, has_y, dout, y, out, dxn, dres, dy, dgate, part, st);
-      else bwd<2, false>(p, T, emb, b, has_y, dout, y, out, dxn, dres, dy, dgate, part, st);
-    } else {
-      if (b.x_f32) bwd<4, true>(p, T, emb, b, has_y, dout, y, out, dxn, dres, dy, dgate, part, st);
-      else bwd<4, false>(p, T, emb, b, has_y, dout, y, out, dxn, dres, dy, dgate, part, st);
-    }
+    const auto go = [&](auto l, auto kc) {
+      if (b.x_f32) bwd<decltype(l)::value, decltype(kc)::value, true>(p, T, emb, b, has_y, dout, y, out, dxn, dres, dy, dgate, part, st);
+      else bwd<decltype(l)::value, decltype(kc)::value, false>(p, T, emb, b, has_y, dout, y, out, dxn, dres, dy, dgate, part, st);
+    };
+    using std::integral_constant;
+    if (p.G == 16) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    else if (p.kc == 2) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   // the order of the kernel's partial sums; of no rows (T = 0) the sums are 0

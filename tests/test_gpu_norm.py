@@ -16,7 +16,8 @@ DEV = "cuda:0"
 EPS = 1e-6
 BF, F32 = torch.bfloat16, torch.float32
 
-# rows of one chunk, of one wave's lanes, of 128, 256 and 512 lanes, full and not; row counts that leave groups empty
+# rows of one chunk, of 16 lanes, of a wave's, of 128, 256 and 512 lanes, full and not; row counts that leave groups
+# empty
 SHAPES = [(1, 8), (5, 64), (3, 520), (130, 1088), (7, 2048), (6, 2056), (9, 4096), (1027, 192), (4, 7168), (3, 8192),
           (2, 8200), (3, 16384)]
 
@@ -145,7 +146,7 @@ def test_block_out_and_its_gradient(T, emb, gate, gt, post, nxt, xt, wt):
 
 
 @pytest.mark.parametrize("T,emb,k", [(1, 64, 1), (5, 520, 3), (33, 2048, 8), (130, 192, 2), (6, 7168, 8), (3, 8200, 64),
-                                     (9, 1088, 13)])
+                                     (9, 1088, 13), (401, 128, 3), (300, 256, 11), (259, 8, 64)])
 @pytest.mark.parametrize("xt", [BF, F32])
 def test_block_out_from_expert_rows(T, emb, k, xt):
     g = _gen(12)
