@@ -21,7 +21,8 @@ namespace {
 
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kRows = 16;   // rows of a tile: the matrix instruction's side
+constexpr int kSide = 16;          // rows of the matrix instruction; a tile has 16 or 32
+constexpr int kMaxRows = 32;
 constexpr int kWaves = 4;           // waves of a workgroup of the experts' kernels
 constexpr int kFewMaxSlice = 128;  // most mlp columns of a workgroup
 
@@ -201,12 +202,14 @@ __device__ __forceinline__ bf16x8_t as_bf16(u32x4_t v) { return __builtin_bit_ca
 // product, c < 8 gate and c >= 8 up columns). Product j takes column 8c + j of every lane; its 8 values along K lie in
 // the lane's 8 rows, and one byte permute puts two of them into a register: the B operand comes straight from the
 // registers that were loaded.
+template <int R>
 struct StepBf16 {
-  u32x4_t x, v[8];
-  __device__ __forceinline__ void load(const char* p, int64_t ld, uint32_t lane, const char* xp, uint32_t xlane) {
+  u32x4_t x[R], v[8];
+  __device__ __forceinline__ void load(const char* p, int64_t ld, uint32_t lane, const char* xp, const uint32_t (&xlane)[R]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = ldw16(p + i * ld + lane);
-    x = ld16(xp + xlane);
+#pragma unroll
+    for (int m = 0; m < R; ++m) x[m] = ld16(xp + xlane[m]);
   }
   __device__ __forceinline__ bf16x8_t col(int j) const {
     const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
@@ -226,8 +229,9 @@ struct StepBf16 {
 // subnormal weights have, or above 246 leaves bf16's range).
 // Slices of 64 mlp columns give the second product rows of 64 bytes: 128 columns by 64 values of K then, in the
 // operand's own order (v[j]: column 16j + c, codes 16g..), through plain loads.
+template <int R>
 struct StepMx {
-  u32x4_t x[4], v[8];
+  u32x4_t x[R][4], v[8];
   uint32_t scale[2];
 };
 
@@ -243,10 +247,11 @@ __device__ __forceinline__ bf16x8_t mx_values(u32x4_t codes, int h, uint32_t cod
   return as_bf16(r);
 }
 
-// Finds tile `tile`: up to 16 slots (t*k + j) of one expert, in slot order. Lane r < 16 gets row r's slot.
-
+// Finds tile `tile`: up to ROWS slots (t*k + j) of one expert, in slot order. Lane r < ROWS gets row r's slot.
+//
 // Up to 64 slots, slot l's expert in lane l: every wave by itself, in registers. A slot whose rank among its expert's
-// is a multiple of 16 starts a tile.
+// is a multiple of ROWS starts a tile.
+template <int ROWS>
 __device__ __forceinline__ void find_tile64(int S, int E, int tile, int e, int lane, int& te, int& tn,
                                             int& slot) {
   const bool valid = lane < S && (unsigned)e < (unsigned)E;
@@ -255,18 +260,19 @@ __device__ __forceinline__ void find_tile64(int S, int E, int tile, int e, int l
     if ((unsigned)ej >= (unsigned)E) continue;
     const uint64_t m = __ballot(valid && e == ej);
     const int rank = popc64(m & ((1ull << j) - 1));
-    if (rank % kRows || tile--) continue;
+    if (rank % ROWS || tile--) continue;
     const int r = popc64(m & ((1ull << lane) - 1)) - rank;
-    const bool in = valid && e == ej && r >= 0 && r < kRows;
+    const bool in = valid && e == ej && r >= 0 && r < ROWS;
     // lanes outside send to lane 63, which is no row's
     slot = __builtin_amdgcn_ds_permute((in ? r : 63) * 4, lane);
     te = ej;
-    tn = min(kRows, popc64(m) - rank);
+    tn = min(ROWS, popc64(m) - rank);
     break;
   }
 }
 
 // Any number of slots, through LDS; tiles go by expert. Called by the whole workgroup.
+template <int ROWS>
 __device__ __forceinline__ void find_tile(int S, int E, int tile, const int32_t* __restrict__ idx, int* cnt, int* found,
                                           int* rows, int& te, int& tn, int& slot) {
   const int tid = threadIdx.x, lane = tid & 63;
@@ -281,7 +287,7 @@ __device__ __forceinline__ void find_tile(int S, int E, int tile, const int32_t*
   if (tid < 64) {
     int base = 0;
     for (int q = 0; q < E; q += 64) {
-      const int n = (cnt[q + lane] + kRows - 1) / kRows;
+      const int n = (cnt[q + lane] + ROWS - 1) / ROWS;
       int inc = n;
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) {
@@ -296,20 +302,20 @@ __device__ __forceinline__ void find_tile(int S, int E, int tile, const int32_t*
   __syncthreads();
   const int e = found[0];
   if (e < 0) return;
-  const int r0 = found[1] * kRows;
+  const int r0 = found[1] * ROWS;
   if (tid < 64) {
     int base = 0;
     for (int q = 0; q < S; q += 64) {
       const bool mine = q + lane < S && idx[q + lane] == e;
       const uint64_t m = __ballot(mine);
       const int r = base + popc64(m & ((1ull << lane) - 1)) - r0;
-      if (mine && r >= 0 && r < kRows) rows[r] = q + lane;
+      if (mine && r >= 0 && r < ROWS) rows[r] = q + lane;
       base += popc64(m);
     }
   }
   __syncthreads();
   te = e;
-  tn = min(kRows, cnt[e] - r0);
+  tn = min(ROWS, cnt[e] - r0);
   slot = rows[lane < tn ? lane : 0];
 }
 
@@ -343,21 +349,22 @@ struct FewArgs {
 enum { kFused = 0, kFirst = 1, kSecond = 2 };
 constexpr int kMaxCuts = 4;
 
+template <int ROWS>
 struct FewLds {
   union {
-    float red[kWaves][kRows][128];  // first product: each wave's sums; MXFP8: before and after, the wave's step
+    float red[kWaves][kSide][128];  // first product: each wave's sums; MXFP8: before and after, the wave's step
     struct {                    // before both: the search for the tile
       int cnt[kMaxExperts], found[2], picks[64];
     };
   };
-  uint16_t a_hi[kRows][kFewMaxSlice + 8], a_lo[kRows][kFewMaxSlice + 8];
-  int rows[kRows];
-  int64_t share[kRows];  // where each row's share starts in part
+  uint16_t a_hi[ROWS][kFewMaxSlice + 8], a_lo[ROWS][kFewMaxSlice + 8];
+  int rows[kMaxRows];
+  int64_t share[kMaxRows];  // where each row's share starts in part
 };
 
 // Which rows, of which expert. False: the routing has no such tile.
-template <bool PICK>
-__device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds& lds, int lane, int wave, int& e, int& nrows,
+template <bool PICK, int ROWS>
+__device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds<ROWS>& lds, int lane, int wave, int& e, int& nrows,
                                          int& slot) {
   e = -1;
   nrows = slot = 0;
@@ -377,11 +384,11 @@ __device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds& lds
       }
     }
     __syncthreads();
-    find_tile64(S, q.E, tile, lane < S ? lds.picks[lane] : -1, lane, e, nrows, slot);
+    find_tile64<ROWS>(S, q.E, tile, lane < S ? lds.picks[lane] : -1, lane, e, nrows, slot);
   } else if (S <= 64) {
-    find_tile64(S, q.E, tile, lane < S ? q.topk_idx[lane] : -1, lane, e, nrows, slot);
+    find_tile64<ROWS>(S, q.E, tile, lane < S ? q.topk_idx[lane] : -1, lane, e, nrows, slot);
   } else {
-    find_tile(S, q.E, tile, q.topk_idx, lds.cnt, lds.found, lds.rows, e, nrows, slot);
+    find_tile<ROWS>(S, q.E, tile, q.topk_idx, lds.cnt, lds.found, lds.rows, e, nrows, slot);
   }
   __syncthreads();  // the search is over, its LDS free
   e = __builtin_amdgcn_readfirstlane(e);
@@ -391,45 +398,50 @@ __device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds& lds
 
 // Row r, column n of the second product's left operand. It enters as the sum of two bf16 numbers, 16 bits of it: the
 // matrix cores are idle most of the time, so the layer's bf16 rounding of a is not needed here.
-__device__ __forceinline__ void few_set_a(FewLds& lds, int r, int n, float gate, float up) {
+template <int ROWS>
+__device__ __forceinline__ void few_set_a(FewLds<ROWS>& lds, int r, int n, float gate, float up) {
   const float a = silu_f(gate) * up;
   const uint16_t hi = (uint16_t)pack_bf16x2(a, 0.0f);
   lds.a_hi[r][n] = hi;
-  lds.a_lo[r][n] = (uint16_t)pack_bf16x2(a - bf16_to_f32(hi), 0.0f);
+  // past bf16's range the second number is 0: inf - inf would make the row NaN
+  lds.a_lo[r][n] = (hi & 0x7f80) == 0x7f80 ? 0 : (uint16_t)pack_bf16x2(a - bf16_to_f32(hi), 0.0f);
 }
 
-// The waves' sums of 64 gate and 64 up columns -> SwiGLU -> a's columns s0...
-__device__ __forceinline__ void few_swiglu(FewLds& lds, int nrows, int s0) {
-  for (int i = threadIdx.x; i < kRows * 64; i += kWaves * 64) {
+// The waves' sums of 64 gate and 64 up columns of rows r0.. -> SwiGLU -> a's columns s0...
+template <int ROWS>
+__device__ __forceinline__ void few_swiglu(FewLds<ROWS>& lds, int nrows, int r0, int s0) {
+  for (int i = threadIdx.x; i < kSide * 64; i += kWaves * 64) {
     const int r = i >> 6, n = i & 63;
     float gate = 0, up = 0;
-    if (r < nrows) {
+    if (r0 + r < nrows) {
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         gate += lds.red[w][r][n];
         up += lds.red[w][r][64 + n];
       }
     }
-    few_set_a(lds, r, s0 + n, gate, up);
+    few_set_a(lds, r0 + r, s0 + n, gate, up);
   }
 }
 
 // kFirst: the waves' sums to hpart.
-__device__ __forceinline__ void few_store_h(const FewArgs& q, const FewLds& lds, int nrows, int sl) {
-  for (int i = threadIdx.x; i < nrows * 128; i += kWaves * 64) {
+template <int ROWS>
+__device__ __forceinline__ void few_store_h(const FewArgs& q, const FewLds<ROWS>& lds, int nrows, int r0, int sl) {
+  for (int i = threadIdx.x; i < min(kSide, nrows - r0) * 128; i += kWaves * 64) {
     const int r = i >> 7, n = i & 127;
     float h = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) h += lds.red[w][r][n];
-    q.hpart[(((int64_t)lds.rows[r] * q.ns + sl) * q.cuts + blockIdx.y) * 128 + n] = h;
+    q.hpart[(((int64_t)lds.rows[r0 + r] * q.ns + sl) * q.cuts + blockIdx.y) * 128 + n] = h;
   }
 }
 
 // kSecond: hpart -> SwiGLU -> a.
-__device__ __forceinline__ void few_load_h(const FewArgs& q, FewLds& lds, int nrows, int sl) {
+template <int ROWS>
+__device__ __forceinline__ void few_load_h(const FewArgs& q, FewLds<ROWS>& lds, int nrows, int sl) {
   const int n = threadIdx.x & 63;
 #pragma unroll
-  for (int it = 0; it < kRows / kWaves; ++it) {
+  for (int it = 0; it < ROWS / kWaves; ++it) {
     if (it * kWaves >= nrows) continue;  // rows past the last: their results are not used
     const int r = it * kWaves + (threadIdx.x >> 6);
     const float* h = q.hpart + ((int64_t)lds.rows[r < nrows ? r : 0] * q.ns + sl) * q.cuts * 128 + n;
@@ -450,18 +462,22 @@ __device__ __forceinline__ void few_load_h(const FewArgs& q, FewLds& lds, int nr
 
 __device__ __forceinline__ const char* bytes(const void* p) { return static_cast<const char*>(p); }
 
-template <int PART, bool WIDE, bool PICK>
-__global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) {
-  __shared__ __align__(16) FewLds lds;
+template <int PART, bool WIDE, bool PICK, int R>
+__global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kernel(FewArgs q) {
+  constexpr int kRows = R * kSide;
+  __shared__ __align__(16) FewLds<kRows> lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int emb = q.emb, mlp = q.mlp;
   const int tile = blockIdx.x / q.ns, sl = blockIdx.x - tile * q.ns;
   int e, nrows, slot;
-  if (!few_tile<PICK>(q, tile, lds, lane, wave, e, nrows, slot)) return;
+  if (!few_tile<PICK, kRows>(q, tile, lds, lane, wave, e, nrows, slot)) return;
   const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
   // lanes past the last row compute on the first one; their rows of the results are not used
-  const uint32_t xrow = (uint32_t)__shfl(slot, c < nrows ? c : 0) / (uint32_t)q.k;
+  uint32_t xlane[R];
+#pragma unroll
+  for (int m = 0; m < R; ++m)
+    xlane[m] = 2 * ((uint32_t)__shfl(slot, m * kSide + c < nrows ? m * kSide + c : 0) / (uint32_t)q.k * (uint32_t)emb + 8 * g);
   // read after a barrier
   if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb, lds.rows[lane] = slot;
 
@@ -478,8 +494,7 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
   const int64_t ld1 = 4 * (int64_t)mlp, ld2 = 2 * (int64_t)emb;  // bytes from row to row
   const uint32_t lane1 = 8 * g * (uint32_t)ld1 + 2 * (c < 8 ? 8 * c : mlp + 8 * (c - 8));
   const uint32_t lane2 = 8 * g * (uint32_t)ld2 + 16 * c;
-  const uint32_t xlane = 2 * (xrow * (uint32_t)emb + 8 * g);
-  const auto load = [&](StepBf16& st, int u) {  // u: which of the pair
+  const auto load = [&](StepBf16<R>& st, int u) {  // u: which of the pair
     const bool first = PART == kFirst || (PART == kFused && lw < n1);
     const int k1 = kb + (lw * kWaves + wave) * kPair + (WIDE ? 0 : 32 * u);
     const bool real = first ? k1 < ke && (!WIDE || 64 * u < width) : ln < emb;
@@ -495,60 +510,77 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
     lw = u == 1 && first ? lw + 1 : lw;
   };
 
-  StepBf16 st[2];
+  StepBf16<R> st[2];
   load(st[0], 0);
   load(st[1], 1);
   if constexpr (PART == kSecond) {
     __syncthreads();  // the slots
     few_load_h(q, lds, nrows, sl);
   }
-  f32x4_t sum[WIDE ? 2 : 1][8];
+  f32x4_t sum[WIDE ? 2 : 1][R][8];
 #pragma unroll
   for (int u = 0; u < (WIDE ? 2 : 1); ++u)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[u][j] = f32x4_t{0, 0, 0, 0};
+    for (int m = 0; m < R; ++m)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[u][m][j] = f32x4_t{0, 0, 0, 0};
   for (int w = 0; w < n1; ++w) {
     const bool on = kb + (w * kWaves + wave) * kPair < ke;  // emb is a multiple of 64: both steps of a pair or none
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (on) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[WIDE ? u : 0][j] = mfma(as_bf16(st[u].x), st[u].col(j), sum[WIDE ? u : 0][j]);
+        for (int j = 0; j < 8; ++j) {
+          const bf16x8_t b = st[u].col(j);
+#pragma unroll
+          for (int m = 0; m < R; ++m) sum[WIDE ? u : 0][m][j] = mfma(as_bf16(st[u].x[m]), b, sum[WIDE ? u : 0][m][j]);
+        }
       }
       load(st[u], u);
     }
   }
 #pragma unroll
   for (int u = 0; u < (WIDE ? 2 : 1); ++u) {
-    if (PART == kSecond || 64 * u >= width) continue;
-    if (u) __syncthreads();  // the first columns' sums have been read
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (4 * g + r >= nrows) continue;
-      float* d = &lds.red[wave][4 * g + r][8 * c];
-      *reinterpret_cast<f32x4_t*>(d) = f32x4_t{sum[u][0][r], sum[u][1][r], sum[u][2][r], sum[u][3][r]};
-      *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{sum[u][4][r], sum[u][5][r], sum[u][6][r], sum[u][7][r]};
+    for (int m = 0; m < R; ++m) {
+      if (PART == kSecond || 64 * u >= width) continue;
+      if (u || m) __syncthreads();  // the sums before have been read
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (m * kSide + 4 * g + r >= nrows) continue;
+        const f32x4_t* v = sum[u][m];
+        float* d = &lds.red[wave][4 * g + r][8 * c];
+        *reinterpret_cast<f32x4_t*>(d) = f32x4_t{v[0][r], v[1][r], v[2][r], v[3][r]};
+        *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{v[4][r], v[5][r], v[6][r], v[7][r]};
+      }
+      __syncthreads();
+      if constexpr (PART == kFirst) few_store_h(q, lds, nrows, m * kSide, sl);
+      else few_swiglu(lds, nrows, m * kSide, 64 * u);
     }
-    __syncthreads();
-    if constexpr (PART == kFirst) few_store_h(q, lds, nrows, sl);
-    else few_swiglu(lds, nrows, 64 * u);
   }
   if constexpr (PART == kFirst) return;
   __syncthreads();
 
-  f32x4_t acc[8];
+  f32x4_t acc[R][8];
   for (int n0 = nb; n0 < emb; n0 += nstride) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
+    for (int m = 0; m < R; ++m)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[m][j] = f32x4_t{0, 0, 0, 0};
     for (int kk = 0; kk < width; kk += 64) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bf16x8_t ah = as_bf16(ld16(&lds.a_hi[c][kk + 32 * u + 8 * g]));
-        const bf16x8_t al = as_bf16(ld16(&lds.a_lo[c][kk + 32 * u + 8 * g]));
+        bf16x8_t ah[R], al[R];
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+          ah[m] = as_bf16(ld16(&lds.a_hi[m * kSide + c][kk + 32 * u + 8 * g]));
+          al[m] = as_bf16(ld16(&lds.a_lo[m * kSide + c][kk + 32 * u + 8 * g]));
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const bf16x8_t b = st[u].col(j);
-          acc[j] = mfma(al, b, mfma(ah, b, acc[j]));
+#pragma unroll
+          for (int m = 0; m < R; ++m) acc[m][j] = mfma(al[m], b, mfma(ah[m], b, acc[m][j]));
         }
         load(st[u], u);
       }
@@ -557,20 +589,25 @@ __global__ __launch_bounds__(kWaves * 64, 3) void few_experts_kernel(FewArgs q) 
     const int n = n0 + 8 * c;
     if (n >= emb) continue;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * g + r;
-      if (row >= nrows) continue;
-      float* d = q.part + lds.share[row] + n;
-      *reinterpret_cast<f32x4_t*>(d) = f32x4_t{acc[0][r], acc[1][r], acc[2][r], acc[3][r]};
-      *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{acc[4][r], acc[5][r], acc[6][r], acc[7][r]};
+    for (int m = 0; m < R; ++m) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = m * kSide + 4 * g + r;
+        if (row >= nrows) continue;
+        const f32x4_t* v = acc[m];
+        float* d = q.part + lds.share[row] + n;
+        *reinterpret_cast<f32x4_t*>(d) = f32x4_t{v[0][r], v[1][r], v[2][r], v[3][r]};
+        *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{v[4][r], v[5][r], v[6][r], v[7][r]};
+      }
     }
   }
 }
 
 // The same on MXFP8 weights.
-template <int PART, bool PICK>
+template <int PART, bool PICK, int R>
 __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs q) {
-  __shared__ __align__(16) FewLds lds;
+  constexpr int kRows = R * kSide;
+  __shared__ __align__(16) FewLds<kRows> lds;
   __shared__ uint32_t scale[kWaves][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -583,10 +620,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   }
   const int tile = b / q.ns, sl = (b - tile * q.ns + (q.slice == 64 ? 0 : tile)) % q.ns;
   int e, nrows, slot;
-  if (!few_tile<PICK>(q, tile, lds, lane, wave, e, nrows, slot)) return;
+  if (!few_tile<PICK, kRows>(q, tile, lds, lane, wave, e, nrows, slot)) return;
   const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
   const bool narrow = width == 64;  // of the second product's steps
-  const uint32_t xrow = (uint32_t)__shfl(slot, c < nrows ? c : 0) / (uint32_t)q.k;
+  uint32_t xlane[R];
+#pragma unroll
+  for (int m = 0; m < R; ++m)
+    xlane[m] = 2 * ((uint32_t)__shfl(slot, m * kSide + c < nrows ? m * kSide + c : 0) / (uint32_t)q.k * (uint32_t)emb + 16 * g);
   // read after a barrier
   if (wave == 0 && lane < kRows) lds.share[lane] = ((int64_t)slot * q.ns + sl) * emb, lds.rows[lane] = slot;
 
@@ -598,7 +638,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   const int nstride = (PART == kSecond ? q.cuts : 1) * kWaves * 128;
   const uint32_t r8 = lane >> 3, unit = (lane & 7) ^ r8;  // wide: the lane's column of each eight, and its unit
   int ls = 0, lw = 0, ln = nb;
-  const auto load = [&](StepMx& st, int u) {  // u: which of the pair
+  const auto load = [&](StepMx<R>& st, int u) {  // u: which of the pair
     const bool first = PART == kFirst || (PART == kFused && ls < width);
     const int k1 = kb + (lw * kWaves + wave) * 128;
     const bool real = first ? ls < width && k1 < ke : ln < emb;
@@ -626,12 +666,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     }
     st.scale[0] = *reinterpret_cast<const uint32_t*>(s + 4 * lane);
     st.scale[1] = *reinterpret_cast<const uint32_t*>(s + plane + 4 * lane);
-    const char* xp = bytes(q.x) + 2 * (xrow * (uint32_t)emb + 16 * g) + (first && real ? 2 * k1 : 0);
+    const char* xp = bytes(q.x) + (first && real ? 2 * k1 : 0);
     const int xh = half || !real || !first ? 0 : 128;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      st.x[h] = ld16(xp + 16 * h);
-      st.x[2 + h] = ld16(xp + xh + 16 * h);
+    for (int m = 0; m < R; ++m) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        st.x[m][h] = ld16(xp + xlane[m] + 16 * h);
+        st.x[m][2 + h] = ld16(xp + xh + xlane[m] + 16 * h);
+      }
     }
     const bool wrap = lw + 1 == n1;
     const bool pair = u == 1;
@@ -641,7 +684,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   };
   // wide step -> LDS; then column tile t's 16 codes (unit 4p + g) and their scale code
   u32x4_t* my = reinterpret_cast<u32x4_t*>(lds.red[wave]);
-  const auto stage = [&](const StepMx& st) {
+  const auto stage = [&](const StepMx<R>& st) {
     wave_lds_fence();
 #pragma unroll
     for (int j = 0; j < 8; ++j) my[64 * j + lane] = st.v[j];
@@ -652,7 +695,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   const auto codes = [&](int t, int p) { return my[(16 * t + c) * 8 + ((4 * p + g) ^ (c & 7))]; };
   const auto code_of = [&](uint32_t d) { return (g & 2) ? d >> 8 : d; };
 
-  StepMx st[2];
+  StepMx<R> st[2];
   load(st[0], 0);
   load(st[1], 1);
   if constexpr (PART == kSecond) {
@@ -660,10 +703,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     few_load_h(q, lds, nrows, sl);
     __syncthreads();
   }
-  f32x4_t acc[8];
-  for (int s0 = 0; s0 < (PART == kSecond ? 0 : width); s0 += 64) {
+  f32x4_t acc[R][8];
+  const auto clear = [&]() {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
+    for (int m = 0; m < R; ++m)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[m][j] = f32x4_t{0, 0, 0, 0};
+  };
+  for (int s0 = 0; s0 < (PART == kSecond ? 0 : width); s0 += 64) {
+    clear();
     for (int w = 0; w < n1; ++w) {
       const int k1 = kb + (w * kWaves + wave) * 128;
 #pragma unroll
@@ -678,8 +726,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
               const u32x4_t v = codes(t, p);
               const uint32_t s = code_of(scale[wave][p][16 * t + c]);
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                acc[4 * u + t] = mfma(as_bf16(st[u].x[2 * p + h]), mx_values(v, h, s), acc[4 * u + t]);
+              for (int h = 0; h < 2; ++h) {
+                const bf16x8_t b = mx_values(v, h, s);
+#pragma unroll
+                for (int m = 0; m < R; ++m) acc[m][4 * u + t] = mfma(as_bf16(st[u].x[m][2 * p + h]), b, acc[m][4 * u + t]);
+              }
             }
           }
         }
@@ -689,36 +740,41 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     // the wave's own LDS from here on holds its sums, until all have read them
     wave_lds_fence();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (4 * g + r >= nrows) continue;
+    for (int m = 0; m < R; ++m) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) lds.red[wave][4 * g + r][16 * j + c] = acc[j][r];
+      for (int r = 0; r < 4; ++r) {
+        if (m * kSide + 4 * g + r >= nrows) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) lds.red[wave][4 * g + r][16 * j + c] = acc[m][j][r];
+      }
+      __syncthreads();
+      if constexpr (PART == kFirst) few_store_h(q, lds, nrows, m * kSide, sl);
+      else few_swiglu(lds, nrows, m * kSide, s0);
+      __syncthreads();
     }
-    __syncthreads();
-    if constexpr (PART == kFirst) few_store_h(q, lds, nrows, sl);
-    else few_swiglu(lds, nrows, s0);
-    __syncthreads();
   }
   if constexpr (PART == kFirst) return;
 
-  const auto clear = [&]() {
+  const auto a_of = [&](int k, bf16x8_t (&hi)[R], bf16x8_t (&lo)[R]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
-  };
-  const auto a_of = [&](int k, bf16x8_t& hi, bf16x8_t& lo) {
-    hi = as_bf16(ld16(&lds.a_hi[c][k]));
-    lo = as_bf16(ld16(&lds.a_lo[c][k]));
+    for (int m = 0; m < R; ++m) {
+      hi[m] = as_bf16(ld16(&lds.a_hi[m * kSide + c][k]));
+      lo[m] = as_bf16(ld16(&lds.a_lo[m * kSide + c][k]));
+    }
   };
   const auto store = [&](int n0) {
     wave_lds_fence();  // `share` is read again, not kept in registers
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * g + r;
-      if (row >= nrows) continue;
-      float* d = q.part + lds.share[row] + n0 + c;
+    for (int m = 0; m < R; ++m) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (n0 + 16 * j < emb) d[16 * j] = acc[j][r];
+      for (int r = 0; r < 4; ++r) {
+        const int row = m * kSide + 4 * g + r;
+        if (row >= nrows) continue;
+        float* d = q.part + lds.share[row] + n0 + c;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n0 + 16 * j < emb) d[16 * j] = acc[m][j][r];
+      }
     }
   };
   if (!narrow) {
@@ -731,12 +787,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
         for (int p = 0; p < 2; ++p) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            bf16x8_t ah, al;
+            bf16x8_t ah[R], al[R];
             a_of(64 * p + 16 * g + 8 * h, ah, al);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const bf16x8_t v = mx_values(codes(t, p), h, code_of(scale[wave][p][16 * t + c]));
-              acc[4 * u + t] = mfma(al, v, mfma(ah, v, acc[4 * u + t]));
+#pragma unroll
+              for (int m = 0; m < R; ++m) acc[m][4 * u + t] = mfma(al[m], v, mfma(ah[m], v, acc[m][4 * u + t]));
             }
           }
         }
@@ -756,12 +813,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
           wave_lds_fence();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            bf16x8_t ah, al;
+            bf16x8_t ah[R], al[R];
             a_of(16 * g + 8 * h, ah, al);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const bf16x8_t v = mx_values(st[u].v[j], h, code_of(scale[wave][j >> 2][16 * (j & 3) + c]));
-              acc[j] = mfma(al, v, mfma(ah, v, acc[j]));
+#pragma unroll
+              for (int m = 0; m < R; ++m) acc[m][j] = mfma(al[m], v, mfma(ah[m], v, acc[m][j]));
             }
           }
           store(n0 + u * nstride);
@@ -826,12 +884,17 @@ struct FewPlan {
   int slice, ns;       // mlp columns of a workgroup, workgroups of a tile
   int cuts, run1;      // of emb in the first product (rows of each) and of the second one's columns; 1: both fused
   int run, splits;     // rows of emb of a router wave, router workgroups along emb
-  int tiles;           // most tiles of 16 rows that the routing can give
+  int rows, tiles;     // rows of a tile, most tiles that the routing can give
 };
 
 FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
   FewPlan p;
   const int S = (int)T * k, experts = S < E ? S : E;
+  // Rows of a tile: an expert with more reads its weights again for the next tile, but tiles of 32 leave half the
+  // workgroups where 16 would have done. us, 16 against 32 rows, by the mean rows of an expert (emb 4096, mlp 14336, top-2
+  // of 8): 8: 580 / 582, 12: 652 / 611, 16: 895 / 644; MXFP8 350 / 354, 397 / 379, 540 / 420; one expert (emb 2048, mlp
+  // 8192), 32 tokens: 64 / 67 and MXFP8 53 / 67, 48 tokens: 97 / 74 and 80 / 63.
+  p.rows = T > 2 * kSide && S >= 12 * E ? 2 * kSide : kSide;
   // Slices of 128 columns are read in longer runs and leave half the shares, slices of 64 give twice the workgroups, and
   // a compute unit reads 46 GB/s at most. us at emb 2048, mlp 768, top-8 of 128, slices of 64 against 128, by the
   // workgroups that 128 gives: 96: 44 / 56, 144: 67 / 61, 192: 70 / 64, 288: 99 / 108, 384: 105 / 112 (a second
@@ -844,7 +907,7 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
   // fused and cut, by the workgroups fused: 8 (emb 7168, mlp 128) 58 / 28, 18 (emb 4096, mlp 192) 44 / 25, 64 (emb 7168,
   // mlp 2048) 93 / 44, 96 (emb 2048, mlp 768) 33 / 29, 128 (emb 2048, mlp 1024) 36 / 30, 192 (emb 2048, mlp 768) 41 / 41
   // and on MXFP8 weights 32 / 38. A cut leaves each of the first product's waves a pair of steps at least.
-  const int64_t filled = (S + kRows - 1) / kRows;
+  const int64_t filled = (S + p.rows - 1) / p.rows;
   const int64_t units = (experts > filled ? experts : filled) * p.ns;
   p.cuts = 1;
   p.run1 = emb;
@@ -853,7 +916,7 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
     p.run1 = (emb + 128 * cuts - 1) / (128 * cuts) * 128;
     p.cuts = (emb + p.run1 - 1) / p.run1;
   }
-  const int most = experts + S / kRows;
+  const int most = experts + S / p.rows;
   p.tiles = most < S ? most : S;
   // a router wave takes 64 rows of emb, more where that would cut emb into more than 16
   p.run = (emb + kLogitWaves * 16 * 64 - 1) / (kLogitWaves * 16 * 64) * 64;
@@ -863,23 +926,22 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-template <int PART, bool PICK>
+template <int PART, bool PICK, int R>
 void launch_part(const FewArgs& q, hipStream_t st) {
-  const dim3 block(kWaves * 64);
+  const dim3 block(kWaves * 64), grid(q.blocks, PART ? q.cuts : 1);
   if (!q.wt.wi)
-    few_experts_mx_kernel<PART, PICK><<<dim3(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks, PART ? q.cuts : 1), block,
-                                        0, st>>>(q);
+    few_experts_mx_kernel<PART, PICK, R><<<dim3(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks, grid.y), block, 0, st>>>(q);
   else if (q.slice == 64)
-    few_experts_kernel<PART, false, PICK><<<dim3(q.blocks, PART ? q.cuts : 1), block, 0, st>>>(q);
+    few_experts_kernel<PART, false, PICK, R><<<grid, block, 0, st>>>(q);
   else if constexpr (PART == kFused)
-    few_experts_kernel<kFused, true, PICK><<<dim3(q.blocks), block, 0, st>>>(q);
+    few_experts_kernel<kFused, true, PICK, R><<<grid, block, 0, st>>>(q);
 }
 
-template <bool PICK>
+template <bool PICK, int R>
 void launch_experts(const FewArgs& q, hipStream_t st) {
-  if (q.cuts == 1) return launch_part<kFused, PICK>(q, st);
-  launch_part<kFirst, PICK>(q, st);
-  launch_part<kSecond, false>(q, st);
+  if (q.cuts == 1) return launch_part<kFused, PICK, R>(q, st);
+  launch_part<kFirst, PICK, R>(q, st);
+  launch_part<kSecond, false, R>(q, st);
 }
 
 }  // namespace
@@ -913,8 +975,9 @@ hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t*
   }
   const FewArgs q{(int)T, k, emb, mlp, E, p.slice, p.ns, p.tiles * p.ns, p.splits, x, logits, bias, topk_idx, topk_w, wt, part,
                   p.cuts, p.run1, hpart};
-  if (pick) launch_experts<true>(q, stream);
-  else launch_experts<false>(q, stream);
+  if (pick) launch_experts<true, 1>(q, stream);
+  else if (p.rows == kSide) launch_experts<false, 1>(q, stream);
+  else launch_experts<false, 2>(q, stream);
   few_sum_kernel<<<dim3((emb + 255) / 256, (unsigned)T), dim3(kSumWaves * 64), 0, stream>>>(
       k, emb, E, p.ns, part, topk_idx, topk_w, y);
   return hipGetLastError();

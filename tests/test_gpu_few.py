@@ -16,7 +16,9 @@ DEV = "cuda:0"
 SHAPES = [(1, 64, 64, 1, 1), (1, 2048, 768, 128, 8), (5, 1088, 448, 60, 4), (16, 128, 64, 4, 4), (17, 192, 128, 1, 1),
           (64, 64, 320, 3, 3), (33, 192, 128, 256, 8), (64, 128, 256, 8, 2), (3, 320, 2048, 70, 64), (64, 576, 192, 160, 8),
           # few slices and a long contraction: the products in kernels of their own, cut
-          (50, 1088, 64, 3, 2), (64, 2112, 128, 1, 1), (7, 5248, 64, 16, 3), (4, 1536, 192, 5, 2)]
+          (50, 1088, 64, 3, 2), (64, 2112, 128, 1, 1), (7, 5248, 64, 16, 3), (4, 1536, 192, 5, 2),
+          # tiles of 32 rows, half-filled ones too, in slices of 128 and of 64 columns
+          (40, 192, 2368, 8, 8), (49, 1024, 320, 3, 1), (64, 320, 192, 4, 1)]
 
 
 def _bf(t):
@@ -211,3 +213,68 @@ def test_disabled_experts_weights_may_hold_anything():
         ri, rw = fu.route(fu.f64(h["x"])[:n], fu.f64(h["wr"]), fu.f64(bias), k)
         assert np.array_equal(idx.cpu().numpy(), ri) and (ri[:, 3:] == [1, 3]).all() and (rw[:, 3:] == 0).all()
         _close(y, *fu.few(fu.f64(h["x"])[:n], fu.f64(h["wi"]), fu.f64(h["wo"]), ri, fu.f64(w)))
+
+
+def test_swiglu_past_bf16_is_infinite_not_nan():
+    """silu(g) * u past bf16's range: with positive down weights the output is +inf, as from a rounded to bf16."""
+    emb = mlp = 64
+    x = torch.ones((2, emb), dtype=torch.bfloat16, device=DEV)
+    wi = torch.full((1, emb, 2 * mlp), 2.0 ** 58, dtype=torch.bfloat16, device=DEV)  # g = u = 2^64
+    wo = torch.ones((1, mlp, emb), dtype=torch.bfloat16, device=DEV)
+    idx, w = torch.zeros((2, 1), dtype=torch.int32, device=DEV), torch.ones((2, 1), device=DEV)
+    x[1] = 2.0 ** -58  # g = u = 64: finite beside it
+    y = moe.ffn_fwd_few(x, wi, wo, topk_idx=idx, topk_w=w)[0]
+    assert torch.equal(y[0], torch.full_like(y[0], float("inf")))
+    assert torch.equal(y[1], torch.full_like(y[1], 64.0 * 64 * mlp))
+
+
+def test_experts_of_zero_weights_give_zeros():
+    h, d = _inputs(5, 192, 128, 6, 2, seed=9)
+    d["wi"][2:4] = 0
+    d["wo"][4] = 0
+    idx = torch.tensor([[2, 3], [3, 4], [4, 2], [2, 2], [0, 4]], dtype=torch.int32, device=DEV)
+    w = torch.ones((5, 2), device=DEV)
+    for y in (moe.ffn_fwd_few(d["x"], d["wi"], d["wo"], topk_idx=idx, topk_w=w)[0],
+              moe.ffn_fwd_few_mx(d["x"], moe.mx_quantize_expert_weights(d["wi"], d["wo"]), topk_idx=idx, topk_w=w)[0]):
+        assert not y[:4].any() and y[4].any() and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_largest_expert_past_32_bit_offsets(mx):
+    """emb 16384, mlp 65472, the second of two experts: its weights start past 2^32 bytes (MXFP8: past 2^31)."""
+    T, emb, mlp = 3, 16384, 65472
+    g = torch.Generator(device=DEV).manual_seed(5)
+    wi = torch.empty((2, emb, 2 * mlp), dtype=torch.bfloat16, device=DEV).normal_(0, emb ** -0.5, generator=g)
+    wo = torch.empty((2, mlp, emb), dtype=torch.bfloat16, device=DEV).normal_(0, mlp ** -0.5, generator=g)
+    x = torch.empty((T, emb), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    idx, w = torch.ones((T, 1), dtype=torch.int32, device=DEV), torch.tensor([[0.5], [1.0], [0.25]], device=DEV)
+    if mx:
+        wq = moe.mx_quantize_expert_weights(wi, wo)
+        y = moe.ffn_fwd_few_mx(x, wq, topk_idx=idx, topk_w=w)[0]
+        s = {n: torch.exp2(wq[n + "_scales"][1, ..., :2].double() - 127).transpose(0, 1) for n in ("wi", "wo")}
+
+        def values(n, lo, hi, k0, k1):  # [N rows, K] of the expert: rows lo..hi, K k0..k1
+            c = wq[n + "_codes"][1, lo:hi, k0:k1].view(torch.float8_e4m3fn).double()
+            sc = s[n][lo:hi, k0 // 64:k1 // 64].reshape(hi - lo, -1)
+            return c * torch.repeat_interleave(sc, 32, dim=1)
+        cols = lambda lo, hi: values("wi", lo, hi, 0, emb).T
+        rows = lambda lo, hi: values("wo", 0, emb, lo, hi).T
+    else:
+        y = moe.ffn_fwd_few(x, wi, wo, topk_idx=idx, topk_w=w)[0]
+        cols = lambda lo, hi: wi[1, :, lo:hi].double()
+        rows = lambda lo, hi: wo[1, lo:hi].double()
+    ref, err = torch.zeros((T, emb), dtype=torch.float64, device=DEV), torch.zeros((T, emb), dtype=torch.float64, device=DEV)
+    xd = x.double()
+    for m in range(0, mlp, 3968):  # 16.5 chunks of whole 64s
+        n = min(m + 3968, mlp)
+        gate, up, down = cols(m, n), cols(mlp + m, mlp + n), rows(m, n)
+        gv, uv = xd @ gate, xd @ up
+        dg, du = ((emb + 16) * fu.U * (xd.abs() @ v.abs()) for v in (gate, up))
+        sv = torch.nn.functional.silu(gv)
+        a = sv * uv
+        da = 1.1 * dg * uv.abs() + sv.abs() * du + 1.1 * dg * du + a.abs() * (2.0 ** -16 + 2.0 ** -19)
+        ref += a @ down
+        err += da @ down.abs() + (mlp + 16) * fu.U * ((a.abs() + da) @ down.abs())
+        err += (mlp // 64 + 17) * fu.U * (a.abs() @ down.abs())
+    ref, err = ref * w.double(), err * w.double()
+    _close(y, ref.cpu().numpy(), (err + fu.H * (ref.abs() + err)).cpu().numpy())
