@@ -12,6 +12,8 @@
 // few_topk (one wave a token), few_experts (a workgroup per expert, 16 of its rows,
 // and a slice of mlp columns: gate/up, SwiGLU, and the slice's share of the down
 // product) and few_sum (a token's shares, weighted).
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 #include "lanes.h"
@@ -202,14 +204,11 @@ __device__ __forceinline__ bf16x8_t as_bf16(u32x4_t v) { return __builtin_bit_ca
 // product, c < 8 gate and c >= 8 up columns). Product j takes column 8c + j of every lane; its 8 values along K lie in
 // the lane's 8 rows, and one byte permute puts two of them into a register: the B operand comes straight from the
 // registers that were loaded.
-template <int R>
 struct StepBf16 {
-  u32x4_t x[R], v[8];
-  __device__ __forceinline__ void load(const char* p, int64_t ld, uint32_t lane, const char* xp, const uint32_t (&xlane)[R]) {
+  u32x4_t v[8];
+  __device__ __forceinline__ void load(const char* p, int64_t ld, uint32_t lane) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = ldw16(p + i * ld + lane);
-#pragma unroll
-    for (int m = 0; m < R; ++m) x[m] = ld16(xp + xlane[m]);
   }
   __device__ __forceinline__ bf16x8_t col(int j) const {
     const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
@@ -229,9 +228,8 @@ struct StepBf16 {
 // subnormal weights have, or above 246 leaves bf16's range).
 // Slices of 64 mlp columns give the second product rows of 64 bytes: 128 columns by 64 values of K then, in the
 // operand's own order (v[j]: column 16j + c, codes 16g..), through plain loads.
-template <int R>
 struct StepMx {
-  u32x4_t x[R][4], v[8];
+  u32x4_t v[8];
   uint32_t scale[2];
 };
 
@@ -494,7 +492,7 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
   const int64_t ld1 = 4 * (int64_t)mlp, ld2 = 2 * (int64_t)emb;  // bytes from row to row
   const uint32_t lane1 = 8 * g * (uint32_t)ld1 + 2 * (c < 8 ? 8 * c : mlp + 8 * (c - 8));
   const uint32_t lane2 = 8 * g * (uint32_t)ld2 + 16 * c;
-  const auto load = [&](StepBf16<R>& st, int u) {  // u: which of the pair
+  const auto load = [&](StepBf16& st, int u, auto x) {  // u: which of the pair; x: nullptr where it is not needed
     const bool first = PART == kFirst || (PART == kFused && lw < n1);
     const int k1 = kb + (lw * kWaves + wave) * kPair + (WIDE ? 0 : 32 * u);
     const bool real = first ? k1 < ke && (!WIDE || 64 * u < width) : ln < emb;
@@ -502,17 +500,24 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
     const uint32_t l2 = ln + 64 >= emb && c >= 8 ? lane2 - 128 : lane2;
     const char* p1 = bytes(q.wt.wi) + ((int64_t)e * emb + k1) * ld1 + 2 * (m0 + (WIDE ? 64 * u : 0));
     const char* p2 = bytes(q.wt.wo) + ((int64_t)e * mlp + m0 + lk) * ld2 + 2 * ln;
-    st.load(real ? first ? p1 : p2 : bytes(q.x), real ? first ? ld1 : ld2 : 0, real ? first ? lane1 : l2 : 0,
-            bytes(q.x) + (first && real ? 2 * k1 : 0), xlane);
+    st.load(real ? first ? p1 : p2 : bytes(q.x), real ? first ? ld1 : ld2 : 0, real ? first ? lane1 : l2 : 0);
+    if constexpr (!std::is_same_v<decltype(x), std::nullptr_t>) {
+      const char* xp = bytes(q.x) + (first && real ? 2 * k1 : 0);
+#pragma unroll
+      for (int m = 0; m < R; ++m) x[m] = ld16(xp + xlane[m]);
+    }
     const bool wrap = lk + 32 >= width;
     lk = first ? lk : wrap ? 0 : lk + 32;
     ln = !first && wrap ? ln + nstride : ln;
     lw = u == 1 && first ? lw + 1 : lw;
   };
 
-  StepBf16<R> st[2];
-  load(st[0], 0);
-  load(st[1], 1);
+  // x of a pair's first step, which WIDE's second one shares, and of the second one
+  StepBf16 st[2];
+  u32x4_t xs[2][R];
+  load(st[0], 0, &xs[0][0]);
+  if constexpr (WIDE) load(st[1], 1, nullptr);
+  else load(st[1], 1, &xs[1][0]);
   if constexpr (PART == kSecond) {
     __syncthreads();  // the slots
     few_load_h(q, lds, nrows, sl);
@@ -526,17 +531,21 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
       for (int j = 0; j < 8; ++j) sum[u][m][j] = f32x4_t{0, 0, 0, 0};
   for (int w = 0; w < n1; ++w) {
     const bool on = kb + (w * kWaves + wave) * kPair < ke;  // emb is a multiple of 64: both steps of a pair or none
+    u32x4_t x[R];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int m = 0; m < R; ++m) x[m] = WIDE && u ? x[m] : xs[u][m];
       if (on) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const bf16x8_t b = st[u].col(j);
 #pragma unroll
-          for (int m = 0; m < R; ++m) sum[WIDE ? u : 0][m][j] = mfma(as_bf16(st[u].x[m]), b, sum[WIDE ? u : 0][m][j]);
+          for (int m = 0; m < R; ++m) sum[WIDE ? u : 0][m][j] = mfma(as_bf16(x[m]), b, sum[WIDE ? u : 0][m][j]);
         }
       }
-      load(st[u], u);
+      if (WIDE && u) load(st[u], u, nullptr);
+      else load(st[u], u, &xs[u][0]);
     }
   }
 #pragma unroll
@@ -582,7 +591,7 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
 #pragma unroll
           for (int m = 0; m < R; ++m) acc[m][j] = mfma(al[m], b, mfma(ah[m], b, acc[m][j]));
         }
-        load(st[u], u);
+        load(st[u], u, nullptr);
       }
     }
     wave_lds_fence();  // `share` is read again, not kept in registers
@@ -638,7 +647,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   const int nstride = (PART == kSecond ? q.cuts : 1) * kWaves * 128;
   const uint32_t r8 = lane >> 3, unit = (lane & 7) ^ r8;  // wide: the lane's column of each eight, and its unit
   int ls = 0, lw = 0, ln = nb;
-  const auto load = [&](StepMx<R>& st, int u) {  // u: which of the pair
+  const auto load = [&](StepMx& st, int u, auto x) {  // u: which of the pair; x: nullptr where it is not needed
     const bool first = PART == kFirst || (PART == kFused && ls < width);
     const int k1 = kb + (lw * kWaves + wave) * 128;
     const bool real = first ? ls < width && k1 < ke : ln < emb;
@@ -666,14 +675,16 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     }
     st.scale[0] = *reinterpret_cast<const uint32_t*>(s + 4 * lane);
     st.scale[1] = *reinterpret_cast<const uint32_t*>(s + plane + 4 * lane);
-    const char* xp = bytes(q.x) + (first && real ? 2 * k1 : 0);
-    const int xh = half || !real || !first ? 0 : 128;
+    if constexpr (!std::is_same_v<decltype(x), std::nullptr_t>) {
+      const char* xp = bytes(q.x) + (first && real ? 2 * k1 : 0);
+      const int xh = half || !real || !first ? 0 : 128;
 #pragma unroll
-    for (int m = 0; m < R; ++m) {
+      for (int m = 0; m < R; ++m) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        st.x[m][h] = ld16(xp + xlane[m] + 16 * h);
-        st.x[m][2 + h] = ld16(xp + xh + xlane[m] + 16 * h);
+        for (int h = 0; h < 2; ++h) {
+          x[m][h] = ld16(xp + xlane[m] + 16 * h);
+          x[m][2 + h] = ld16(xp + xh + xlane[m] + 16 * h);
+        }
       }
     }
     const bool wrap = lw + 1 == n1;
@@ -684,7 +695,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   };
   // wide step -> LDS; then column tile t's 16 codes (unit 4p + g) and their scale code
   u32x4_t* my = reinterpret_cast<u32x4_t*>(lds.red[wave]);
-  const auto stage = [&](const StepMx<R>& st) {
+  const auto stage = [&](const StepMx& st) {
     wave_lds_fence();
 #pragma unroll
     for (int j = 0; j < 8; ++j) my[64 * j + lane] = st.v[j];
@@ -695,9 +706,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   const auto codes = [&](int t, int p) { return my[(16 * t + c) * 8 + ((4 * p + g) ^ (c & 7))]; };
   const auto code_of = [&](uint32_t d) { return (g & 2) ? d >> 8 : d; };
 
-  StepMx<R> st[2];
-  load(st[0], 0);
-  load(st[1], 1);
+  StepMx st[2];
+  u32x4_t xs[R][4];  // both of a pair multiply the same x
+  load(st[0], 0, &xs[0]);
+  load(st[1], 1, nullptr);
   if constexpr (PART == kSecond) {
     __syncthreads();  // the slots
     few_load_h(q, lds, nrows, sl);
@@ -714,6 +726,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     clear();
     for (int w = 0; w < n1; ++w) {
       const int k1 = kb + (w * kWaves + wave) * 128;
+      u32x4_t x[R][4];
+#pragma unroll
+      for (int m = 0; m < R; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[m][i] = xs[m][i];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (k1 < ke) {
@@ -729,12 +746,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
               for (int h = 0; h < 2; ++h) {
                 const bf16x8_t b = mx_values(v, h, s);
 #pragma unroll
-                for (int m = 0; m < R; ++m) acc[m][4 * u + t] = mfma(as_bf16(st[u].x[m][2 * p + h]), b, acc[m][4 * u + t]);
+                for (int m = 0; m < R; ++m) acc[m][4 * u + t] = mfma(as_bf16(x[m][2 * p + h]), b, acc[m][4 * u + t]);
               }
             }
           }
         }
-        load(st[u], u);
+        if (u) load(st[u], u, nullptr);
+        else load(st[u], u, &xs[0]);
       }
     }
     // the wave's own LDS from here on holds its sums, until all have read them
@@ -797,7 +815,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
             }
           }
         }
-        load(st[u], u);
+        load(st[u], u, nullptr);
       }
       store(n0);
     }
@@ -824,7 +842,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
           }
           store(n0 + u * nstride);
         }
-        load(st[u], u);
+        load(st[u], u, nullptr);
       }
     }
   }
