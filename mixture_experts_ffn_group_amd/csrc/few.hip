@@ -219,15 +219,16 @@ struct StepBf16 {
   }
 };
 
-// MXFP8, K-contiguous [N, K], 64 columns by 128 values of K: load j covers columns 8j..8j+7, 16 codes a lane. In that
-// order the lanes of a column hold its K side by side, where the matrix instruction wants columns side by side: the
-// step goes through the wave's own 8 KB of LDS, from where lane (g, c) reads codes 16(4p + g).. of column 16t + c.
-// Within a column the 16-byte units are stored at u ^ (column & 7), so that both the writes and the reads spread over
-// the banks; the swizzle is in the address the lane loads from. `scale` holds the dwords of the 64 columns for the
-// step's two 64-blocks. Codes convert to bf16 exactly (3 bits of mantissa; a scale code below 3, which only blocks of
-// subnormal weights have, or above 246 leaves bf16's range).
+// MXFP8, K-contiguous [N, K], 64 columns by 128 values of K. Product t takes column 4c + t of every lane, so that a lane
+// ends up with four neighbouring results. Load j covers columns (j & 3) + 32 (j >> 2) + 4 r8, r8 = lane / 8, 16 codes a
+// lane: the lanes of a column hold its K side by side, where the matrix instruction wants columns side by side. The step
+// goes through the wave's own 8 KB of LDS, row 16t + c for column 4c + t, from where lane (g, c) reads codes 16(4p + g)...
+// Within a row the 16-byte units are stored at u ^ (row & 7), so that both the writes and the reads spread over the banks;
+// the swizzle is in the address the lane loads from. `scale` holds the dwords of the 64 columns for the step's two
+// 64-blocks. Codes convert to bf16 exactly (3 bits of mantissa; a scale code below 3, which only blocks of subnormal
+// weights have, or above 246 leaves bf16's range).
 // Slices of 64 mlp columns give the second product rows of 64 bytes: 128 columns by 64 values of K then, in the
-// operand's own order (v[j]: column 16j + c, codes 16g..), through plain loads.
+// operand's own order (v[j]: column 64 (j >> 2) + 4c + (j & 3), codes 16g..), through plain loads.
 struct StepMx {
   u32x4_t v[8];
   uint32_t scale[2];
@@ -645,7 +646,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   const int n1 = PART == kSecond ? 0 : (ke - kb + kWaves * 128 - 1) / (kWaves * 128);
   const int nb = PART == kFirst ? emb : ((PART == kSecond ? blockIdx.y * kWaves : 0) + wave) * 128;  // the wave's blocks
   const int nstride = (PART == kSecond ? q.cuts : 1) * kWaves * 128;
-  const uint32_t r8 = lane >> 3, unit = (lane & 7) ^ r8;  // wide: the lane's column of each eight, and its unit
+  const uint32_t r8 = lane >> 3, unit = (lane & 7) ^ r8;  // wide: the lane's column of a load, and its unit
   int ls = 0, lw = 0, ln = nb;
   const auto load = [&](StepMx& st, int u, auto x) {  // u: which of the pair; x: nullptr where it is not needed
     const bool first = PART == kFirst || (PART == kFused && ls < width);
@@ -662,10 +663,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     const char* s = (first ? bytes(q.wt.wis) : bytes(q.wt.wos)) +
                     (((int64_t)e * (ld / 64) + (first ? k1 : m0) / 64) * planes + (there ? n : ln)) * 4;
     const bool direct = !first && narrow;
-    uint32_t lo = direct ? c * (uint32_t)mlp + 16 * g : r8 * (uint32_t)ld + 16 * (half ? unit & 3 : unit);
-    int64_t step = direct ? 16 * ld : 8 * ld;
+    uint32_t lo = direct ? 4 * c * (uint32_t)mlp + 16 * g : 4 * r8 * (uint32_t)ld + 16 * (half ? unit & 3 : unit);
+    int64_t step = ld;
     // columns 64..127 of a narrow step may not be there
-    int64_t upper = direct && ln + 64 >= emb ? 0 : 4 * step;
+    int64_t upper = !direct ? 32 * ld : ln + 64 >= emb ? 0 : 64 * ld;
     int64_t plane = direct ? (ln + 64 >= emb ? 0 : 256) : half ? 0 : 4 * planes;
     if (!real) p = bytes(q.wt.wic), s = bytes(q.wt.wis), step = upper = plane = 0, lo = 0;
 #pragma unroll
@@ -693,12 +694,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
     lw = !first || !pair ? lw : wrap ? 0 : lw + 1;
     ln = !first && (narrow || pair) ? ln + nstride : ln;
   };
-  // wide step -> LDS; then column tile t's 16 codes (unit 4p + g) and their scale code
+  // wide step -> LDS; then 16 codes (unit 4p + g) of product t's column, and their scale code
   u32x4_t* my = reinterpret_cast<u32x4_t*>(lds.red[wave]);
   const auto stage = [&](const StepMx& st) {
     wave_lds_fence();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) my[64 * j + lane] = st.v[j];
+    for (int j = 0; j < 8; ++j) my[128 * (j & 3) + 64 * (j >> 2) + lane] = st.v[j];
     scale[wave][0][lane] = st.scale[0];
     scale[wave][1][lane] = st.scale[1];
     wave_lds_fence();
@@ -741,7 +742,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const u32x4_t v = codes(t, p);
-              const uint32_t s = code_of(scale[wave][p][16 * t + c]);
+              const uint32_t s = code_of(scale[wave][p][4 * c + t]);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const bf16x8_t b = mx_values(v, h, s);
@@ -762,8 +763,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (m * kSide + 4 * g + r >= nrows) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) lds.red[wave][4 * g + r][16 * j + c] = acc[m][j][r];
+        const f32x4_t* v = acc[m];
+        float* d = &lds.red[wave][4 * g + r][4 * c];
+        *reinterpret_cast<f32x4_t*>(d) = f32x4_t{v[0][r], v[1][r], v[2][r], v[3][r]};
+        *reinterpret_cast<f32x4_t*>(d + 64) = f32x4_t{v[4][r], v[5][r], v[6][r], v[7][r]};
       }
       __syncthreads();
       if constexpr (PART == kFirst) few_store_h(q, lds, nrows, m * kSide, sl);
@@ -788,10 +791,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
       for (int r = 0; r < 4; ++r) {
         const int row = m * kSide + 4 * g + r;
         if (row >= nrows) continue;
-        float* d = q.part + lds.share[row] + n0 + c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (n0 + 16 * j < emb) d[16 * j] = acc[m][j][r];
+        const f32x4_t* v = acc[m];
+        float* d = q.part + lds.share[row] + n0 + 4 * c;
+        *reinterpret_cast<f32x4_t*>(d) = f32x4_t{v[0][r], v[1][r], v[2][r], v[3][r]};
+        if (n0 + 64 < emb) *reinterpret_cast<f32x4_t*>(d + 64) = f32x4_t{v[4][r], v[5][r], v[6][r], v[7][r]};
       }
     }
   };
@@ -809,7 +812,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
             a_of(64 * p + 16 * g + 8 * h, ah, al);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const bf16x8_t v = mx_values(codes(t, p), h, code_of(scale[wave][p][16 * t + c]));
+              const bf16x8_t v = mx_values(codes(t, p), h, code_of(scale[wave][p][4 * c + t]));
 #pragma unroll
               for (int m = 0; m < R; ++m) acc[m][4 * u + t] = mfma(al[m], v, mfma(ah[m], v, acc[m][4 * u + t]));
             }
@@ -835,7 +838,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
             a_of(16 * g + 8 * h, ah, al);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const bf16x8_t v = mx_values(st[u].v[j], h, code_of(scale[wave][j >> 2][16 * (j & 3) + c]));
+              const bf16x8_t v = mx_values(st[u].v[j], h, code_of(scale[wave][j >> 2][4 * c + (j & 3)]));
 #pragma unroll
               for (int m = 0; m < R; ++m) acc[m][j] = mfma(al[m], v, mfma(ah[m], v, acc[m][j]));
             }
