@@ -124,8 +124,8 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int waves, float (*sh)[1
 
 constexpr int kGridRows = 1 << 21;  // workgroups along a grid's x: fewer than 2^32 lanes
 
-// Forward, a workgroup a row (L = 16: sixteen rows), KC chunks of 8 elements a lane. SRC 0: x itself (moe_norm), 1: y given, 2: y = sum over
-// the token's picks of expert rows.
+// Forward, a workgroup a row (L = 16: sixteen rows), KC chunks of 8 elements a lane. SRC 0: x itself (moe_norm), 1: y
+// given, 2: y = sum over the token's picks of expert rows.
 template <int L, int KC, int SRC, bool XF32>
 __global__ __launch_bounds__(L == 16 ? 256 : 1024) void block_out_kernel(int64_t T, int emb, BlockArgs b, const void* res, const uint16_t* __restrict__ y,
                                                          int k, const uint16_t* __restrict__ ys,

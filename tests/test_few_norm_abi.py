@@ -31,6 +31,7 @@ FEW = dict(x=P, wr=P, bias=None, idx=P, w=P, wi=P, wo=P, y=P, ws=P, n=1 << 40)
     (dict(mlp=32), {}, UNSUP),
     (dict(E=257), {}, UNSUP),
     (dict(k=9), {}, SHAPE),
+    (dict(T=64, emb=64, mlp=1 << 23, E=256, k=64), {}, UNSUP),  # more workgroups than a grid holds
     ({}, dict(x=None), NULL),
     ({}, dict(x=ODD), ALIGN),
     ({}, dict(wr=ODD), ALIGN),
