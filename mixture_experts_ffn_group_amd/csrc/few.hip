@@ -343,7 +343,7 @@ struct FewArgs {
   float* part;
   // the products in kernels of their own: cuts of emb (rows of each) and of the output columns; hpart: the first one's
   // sums [slot][slice][cut][64 gate, 64 up]
-  int cuts, run;
+  int cuts, run, cuts2;
   float* hpart;
 };
 
@@ -360,7 +360,7 @@ struct FewArgs {
 // PICK (T <= 8, T*k <= 64): every workgroup first picks the experts from the logits, a wave a token, instead of
 // waiting for another kernel to do it; workgroup 0 writes the routing.
 enum { kFused = 0, kFirst = 1, kSecond = 2 };
-constexpr int kMaxCuts = 4;
+constexpr int kMaxCuts = 8;
 
 template <int ROWS>
 struct FewLds {
@@ -502,7 +502,7 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
   const int kb = PART == kFirst ? blockIdx.y * q.run : 0, ke = PART == kFirst ? min(emb, kb + q.run) : emb;
   const int n1 = PART == kSecond ? 0 : (ke - kb + kWaves * kPair - 1) / (kWaves * kPair);
   const int nb = PART == kFirst ? emb : ((PART == kSecond ? blockIdx.y * kWaves : 0) + wave) * 128;  // the wave's blocks
-  const int nstride = (PART == kSecond ? q.cuts : 1) * kWaves * 128;
+  const int nstride = (PART == kSecond ? q.cuts2 : 1) * kWaves * 128;
   int lw = 0, ln = nb, lk = 0;
   const int64_t ld1 = 4 * (int64_t)mlp, ld2 = 2 * (int64_t)emb;  // bytes from row to row
   const uint32_t lane1 = 8 * g * (uint32_t)ld1 + 2 * (c < 8 ? 8 * c : mlp + 8 * (c - 8));
@@ -659,7 +659,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   const int kb = PART == kFirst ? blockIdx.y * q.run : 0, ke = PART == kFirst ? min(emb, kb + q.run) : emb;
   const int n1 = PART == kSecond ? 0 : (ke - kb + kWaves * 128 - 1) / (kWaves * 128);
   const int nb = PART == kFirst ? emb : ((PART == kSecond ? blockIdx.y * kWaves : 0) + wave) * 128;  // the wave's blocks
-  const int nstride = (PART == kSecond ? q.cuts : 1) * kWaves * 128;
+  const int nstride = (PART == kSecond ? q.cuts2 : 1) * kWaves * 128;
   const uint32_t r8 = lane >> 3, unit = (lane & 7) ^ r8;  // wide: the lane's column of a load, and its unit
   int ls = 0, lw = 0, ln = nb;
   const auto load = [&](StepMx& st, int u, auto x) {  // u: which of the pair; x: nullptr where it is not needed
@@ -917,7 +917,8 @@ __global__ __launch_bounds__(kSumWaves * 64) void few_sum_kernel(int k, int emb,
 // Slices of mlp and cuts of emb in the router, from the shape alone (the workspace's size follows).
 struct FewPlan {
   int slice, ns;       // mlp columns of a workgroup, workgroups of a tile
-  int cuts, run1;      // of emb in the first product (rows of each) and of the second one's columns; 1: both fused
+  int cuts, run1;      // of emb in the first product (rows of each); 1: both fused
+  int cuts2;           // of the second one's columns
   int run, splits;     // rows of emb of a router wave, router workgroups along emb
   int rows, tiles;     // rows of a tile, most tiles that the routing can give
 };
@@ -938,21 +939,25 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
   const int64_t wide = (int64_t)experts * ((mlp + 127) / 128);
   p.slice = wide >= 144 && (mx || wide <= 256 || wide >= 448) ? 128 : 64;
   p.ns = (mlp + p.slice - 1) / p.slice;
-  // Few workgroups: the products in kernels of their own, cut in up to four along emb and along the output columns. us
-  // fused and cut, by the workgroups fused: 8 (emb 7168, mlp 128) 58 / 28, 18 (emb 4096, mlp 192) 44 / 25, 64 (emb 7168,
-  // mlp 2048) 93 / 44, 96 (emb 2048, mlp 768) 33 / 29, 128 (emb 2048, mlp 1024) 36 / 30, 192 (emb 2048, mlp 768) 41 / 41
-  // and on MXFP8 weights 32 / 38. A cut leaves each of the first product's waves a pair of steps at least.
+  // Few workgroups: the products in kernels of their own, cut along emb (in up to four, up to eight where that leaves few
+  // workgroups still) and along the output columns. us fused and cut in four, by the workgroups fused: 8 (emb 7168, mlp
+  // 128) 58 / 28, 18 (emb 4096, mlp 192) 44 / 25, 64 (emb 7168, mlp 2048) 93 / 44, 96 (emb 2048, mlp 768) 33 / 29, 128
+  // (emb 2048, mlp 1024) 36 / 30, 192 (emb 2048, mlp 768) 41 / 41 and on MXFP8 weights 32 / 38. In four and in eight: 16
+  // (emb 4096, mlp 128) 24.1 / 22.1, 32 (emb 2048, mlp 256) 20.9 / 19.7, 64 (emb 7168, mlp 512) 47 / 47, 96 (emb 4096, mlp
+  // 1536) 42.5 / 40.1, 128 (emb 2048, mlp 1024) 29.2 / 31.5. A cut leaves each of the first product's waves a pair of
+  // steps at least: MXFP8 at emb 2048 loses by eight (96: 26.1 / 27.4).
   const int64_t filled = (S + p.rows - 1) / p.rows;
   const int64_t units = (experts > filled ? experts : filled) * p.ns;
-  p.cuts = 1;
+  p.cuts = p.cuts2 = 1;
   p.run1 = emb;
   if (p.slice == 64 && units <= 128 && emb >= 2 * 512) {
-    const int cuts = emb / 512 < kMaxCuts ? emb / 512 : kMaxCuts;
+    const int most = units <= 96 ? kMaxCuts : 4, pairs = emb / (kWaves * (mx ? 128 : 64));
+    const int cuts = pairs < most ? pairs : most;
+    p.cuts2 = emb / (kWaves * 128) < 4 ? emb / (kWaves * 128) : 4;
     p.run1 = (emb + 128 * cuts - 1) / (128 * cuts) * 128;
     p.cuts = (emb + p.run1 - 1) / p.run1;
   }
-  const int most = experts + S / p.rows;
-  p.tiles = most < S ? most : S;
+  p.tiles = experts + S / p.rows < S ? experts + S / p.rows : S;
   // a router wave takes 64 rows of emb, more where that would cut emb into more than 16
   p.run = (emb + kLogitWaves * 16 * 64 - 1) / (kLogitWaves * 16 * 64) * 64;
   p.splits = (emb + kLogitWaves * p.run - 1) / (kLogitWaves * p.run);
@@ -963,7 +968,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 template <int PART, bool PICK, int R>
 void launch_part(const FewArgs& q, hipStream_t st) {
-  const dim3 block(kWaves * 64), grid(q.blocks, PART ? q.cuts : 1);
+  const dim3 block(kWaves * 64), grid(q.blocks, PART == kFirst ? q.cuts : PART == kSecond ? q.cuts2 : 1);
   if (!q.wt.wi)
     few_experts_mx_kernel<PART, PICK, R><<<dim3(q.slice == 64 ? (q.blocks + 15) / 16 * 16 : q.blocks, grid.y), block, 0, st>>>(q);
   else if (q.slice == 64)
@@ -1009,7 +1014,7 @@ hipError_t launch_few(int64_t T, int emb, int mlp, int E, int k, const uint16_t*
       few_topk_kernel<<<dim3((unsigned)T), dim3(64), 0, stream>>>((int)T, E, k, p.splits, logits, bias, topk_idx, topk_w);
   }
   const FewArgs q{(int)T, k, emb, mlp, E, p.slice, p.ns, p.tiles * p.ns, p.splits, x, logits, bias, topk_idx, topk_w, wt, part,
-                  p.cuts, p.run1, hpart};
+                  p.cuts, p.run1, p.cuts2, hpart};
   if (pick) launch_experts<true, 1>(q, stream);
   else if (p.rows == kSide) launch_experts<false, 1>(q, stream);
   else launch_experts<false, 2>(q, stream);
