@@ -18,13 +18,13 @@
 // atomics, whose order changes results.
 //
 // Measured, us, kernels alone (weight bytes per second): one token, top-8 of 128, emb
-// 2048, mlp 768: 4.6 + 14.3 + 8.0 + 4.4, launch and latency of four kernels; 4 tokens
-// with 8 picks each, emb 7168, mlp 2048: experts 405 (6.5 TB/s), sum 5; 64 tokens,
-// top-8 of 128, emb 2048, mlp 768: 7 + 5 + 200 (6.0 TB/s) + 6; 19 tokens with 8 picks
-// each on MXFP8, emb 7168, mlp 2048: 6 + 5 + 470 (5.9 TB/s) + 13. What holds the long ones
-// below a read's 7.2 TB/s: the shares (S * mlp / 128 * emb * 8 bytes written and read
-// again: 64 experts of emb 7168, mlp 2048 take 930 us with one row each, 1073 with
-// eight), and workgroups that do not come out even over the compute units (6.1 TB/s
+// 2048, mlp 768: 3.2 + 13.7 + 8.2 + 4.0, launch and latency of four kernels; 4 tokens
+// with 8 picks each, emb 7168, mlp 2048: experts 409 (6.5 TB/s), sum 5; 64 tokens,
+// top-8 of 128, emb 2048, mlp 768: 7 + 5 + 202 (5.9 TB/s) + 6; 19 tokens with 8 picks
+// each on MXFP8, emb 7168, mlp 2048: 6 + 5 + 474 (5.8 TB/s) + 13. What holds the long
+// ones below a read's 7.2 TB/s: the shares (S * mlp / 128 * emb * 4 bytes, written and
+// read again: 64 experts of emb 7168, mlp 2048 take 934 us with one row each, 1071 with
+// eight), and workgroups that do not come out even over the compute units (6.2 TB/s
 // with 512 of them, 5.5 with 384).
 #include <type_traits>
 
