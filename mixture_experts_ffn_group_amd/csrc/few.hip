@@ -18,14 +18,14 @@
 // atomics, whose order changes results.
 //
 // Measured, us, kernels alone (weight bytes per second): one token, top-8 of 128, emb
-// 2048, mlp 768: 3.2 + 13.7 + 8.2 + 4.0, launch and latency of four kernels; 4 tokens
+// 2048, mlp 768: 3.4 + 13.6 + 8.2 + 4.1, launch and latency of four kernels; 4 tokens
 // with 8 picks each, emb 7168, mlp 2048: experts 409 (6.5 TB/s), sum 5; 64 tokens,
-// top-8 of 128, emb 2048, mlp 768: 7 + 5 + 202 (5.9 TB/s) + 6; 19 tokens with 8 picks
+// top-8 of 128, emb 2048, mlp 768: 7 + 5 + 203 (5.9 TB/s) + 6; 19 tokens with 8 picks
 // each on MXFP8, emb 7168, mlp 2048: 6 + 5 + 474 (5.8 TB/s) + 13. What holds the long
 // ones below a read's 7.2 TB/s: the shares (S * mlp / 128 * emb * 4 bytes, written and
-// read again: 64 experts of emb 7168, mlp 2048 take 934 us with one row each, 1071 with
+// read again: 64 experts of emb 7168, mlp 2048 take 932 us with one row each, 1076 with
 // eight), and workgroups that do not come out even over the compute units (6.2 TB/s
-// with 512 of them, 5.5 with 384).
+// with 512 of them, 5.8 with 640).
 #include <type_traits>
 
 #include "common.h"
@@ -931,26 +931,28 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
   // of 8): 8: 580 / 582, 12: 652 / 611, 16: 895 / 644; MXFP8 350 / 354, 397 / 379, 540 / 420; one expert (emb 2048, mlp
   // 8192), 32 tokens: 64 / 67 and MXFP8 53 / 67, 48 tokens: 97 / 74 and 80 / 63.
   p.rows = T > 2 * kSide && S >= 12 * E ? 2 * kSide : kSide;
-  // Slices of 128 columns are read in longer runs and leave half the shares, slices of 64 give twice the workgroups, and
-  // a compute unit reads 46 GB/s at most. us at emb 2048, mlp 768, top-8 of 128, slices of 64 against 128, by the
-  // workgroups that 128 gives: 96: 44 / 56, 144: 67 / 61, 192: 70 / 64, 288: 99 / 108, 384: 105 / 112 (a second
-  // workgroup for some compute units), 576: 136 / 121; on MXFP8 weights, whose rows of wo are only 64 bytes long in slices of
-  // 64: 96: 37 / 48, 144: 50 / 50, 288: 81 / 72, 576: 96 / 82.
+  // Slices of 128 columns are read in longer runs and leave half the shares, slices of 64 give twice the workgroups, of
+  // which three fit a compute unit, 768 in all. us, slices of 64 against 128, by the workgroups that 128 gives: (emb 2048,
+  // mlp 768) 96: 44 / 56, 144: 67 / 61, 204: 62 / 58, 258: 87 / 95 (a second one for some compute units), 354: 99 / 104;
+  // (emb 7168, mlp 2048) 256: 250 / 226, 272: 320 / 333, 352: 362 / 355, 384: 383 / 368, 400: 450 / 371 (64 gives more
+  // than fit), 448: 474 / 403; on MXFP8 weights, whose rows of wo are only 64 bytes long in slices of 64: 96: 37 / 48, 144:
+  // 50 / 50, 288: 81 / 72, 576: 96 / 82.
   const int64_t wide = (int64_t)experts * ((mlp + 127) / 128);
-  p.slice = wide >= 144 && (mx || wide <= 256 || wide >= 448) ? 128 : 64;
+  p.slice = wide >= 144 && (mx || wide <= 256 || wide >= 384) ? 128 : 64;
   p.ns = (mlp + p.slice - 1) / p.slice;
   // Few workgroups: the products in kernels of their own, cut along emb (in up to four, up to eight where that leaves few
   // workgroups still) and along the output columns. us fused and cut in four, by the workgroups fused: 8 (emb 7168, mlp
   // 128) 58 / 28, 18 (emb 4096, mlp 192) 44 / 25, 64 (emb 7168, mlp 2048) 93 / 44, 96 (emb 2048, mlp 768) 33 / 29, 128
-  // (emb 2048, mlp 1024) 36 / 30, 192 (emb 2048, mlp 768) 41 / 41 and on MXFP8 weights 32 / 38. In four and in eight: 16
-  // (emb 4096, mlp 128) 24.1 / 22.1, 32 (emb 2048, mlp 256) 20.9 / 19.7, 64 (emb 7168, mlp 512) 47 / 47, 96 (emb 4096, mlp
-  // 1536) 42.5 / 40.1, 128 (emb 2048, mlp 1024) 29.2 / 31.5. A cut leaves each of the first product's waves a pair of
-  // steps at least: MXFP8 at emb 2048 loses by eight (96: 26.1 / 27.4).
+  // (emb 2048, mlp 1024) 36 / 30, 144 (emb 2048, mlp 1152) 34.5 / 34.6, 160 (emb 7168, mlp 1280) 99 / 90, 192 (emb 2048,
+  // mlp 768) 40 / 40 and (emb 4096, mlp 1536) 68 / 62; on MXFP8 weights the last four 28.7 / 32.1, 68 / 67, 31 / 37, 47 /
+  // 48. In four and in eight: 16 (emb 4096, mlp 128) 24.1 / 22.1, 32 (emb 2048, mlp 256) 20.9 / 19.7, 64 (emb 7168, mlp
+  // 512) 47 / 47, 96 (emb 4096, mlp 1536) 42.5 / 40.1, 128 (emb 2048, mlp 1024) 29.2 / 31.5. A cut leaves each of the
+  // first product's waves a pair of steps at least: MXFP8 at emb 2048 loses by eight (96: 26.1 / 27.4).
   const int64_t filled = (S + p.rows - 1) / p.rows;
   const int64_t units = (experts > filled ? experts : filled) * p.ns;
   p.cuts = p.cuts2 = 1;
   p.run1 = emb;
-  if (p.slice == 64 && units <= 128 && emb >= 2 * 512) {
+  if (p.slice == 64 && units <= (!mx && emb >= 4096 ? 192 : 128) && emb >= 2 * 512) {
     const int most = units <= 96 ? kMaxCuts : 4, pairs = emb / (kWaves * (mx ? 128 : 64));
     const int cuts = pairs < most ? pairs : most;
     p.cuts2 = emb / (kWaves * 128) < 4 ? emb / (kWaves * 128) : 4;

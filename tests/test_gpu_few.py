@@ -18,7 +18,9 @@ SHAPES = [(1, 64, 64, 1, 1), (1, 2048, 768, 128, 8), (5, 1088, 448, 60, 4), (16,
           # few slices and a long contraction: the products in kernels of their own, cut
           (50, 1088, 64, 3, 2), (64, 2112, 128, 1, 1), (7, 5248, 64, 16, 3), (4, 1536, 192, 5, 2),
           # tiles of 32 rows, half-filled ones too, in slices of 128 and of 64 columns
-          (40, 192, 2368, 8, 8), (49, 1024, 320, 3, 1), (64, 320, 192, 4, 1), (64, 64, 128, 70, 64)]
+          (40, 192, 2368, 8, 8), (49, 1024, 320, 3, 1), (64, 320, 192, 4, 1), (64, 64, 128, 70, 64),
+          # 192 workgroups at emb 4096 (bf16: cut), 390 of 128
+          (3, 4096, 1024, 16, 4), (40, 64, 704, 65, 2)]
 
 
 def _bf(t):
