@@ -45,7 +45,7 @@ constexpr int kFewMaxSlice = 128;  // most mlp columns of a workgroup
 // ---------------------------------------------------------------- router
 
 // logits[split][t][e] = sum over the split's rows of x[t, i] wr[i, e]. The products (8 + 24 bits) are exact in
-// fp64 and the sums are off by 2^-53 a step, so picks are those of exact arithmetic but for ties to 2^-40.
+// fp64 and the sums are off by 2^-53 a step, so picks are those of exact arithmetic but for ties to 2^-44.
 // A wave takes 16 experts and 64 rows of emb at a time, all of whose loads are in flight at once (the kernel is one
 // memory latency long). v_mfma_f64_16x16x4 has A[i = lane%16][k = lane/16], B[k = lane/16][j = lane%16] and
 // D[i = 4r + lane/16][j = lane%16]; step i of the 16 takes row 16 (lane/16) + i of the 64.
