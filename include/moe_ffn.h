@@ -612,8 +612,8 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* shape, const moe_bf16_t* dy, const float
  *  part. An expert may be picked twice by a token here.
  *  wi [E, emb, 2*mlp], wo [E, mlp, emb] bf16; y [T, emb] bf16 =
  *  sum_j topk_w[t, j] (silu(x wi_e[:, :mlp]) * (x wi_e[:, mlp:])) wo_e,
- *  summed in fp32, the SwiGLU output kept to 16 bits, y rounded once. A pick
- *  of weight 0 takes no part.
+ *  summed in fp32, the SwiGLU output in fp32, y rounded once. A pick of
+ *  weight 0 takes no part.
  *  ws: at least moe_workspace_bytes_few(shape) bytes (0: unsupported shape).
  *
  * moe_ffn_fwd_few_mx -- the same on MXFP8 weights (wi_codes, wi_scales, wo_codes and

@@ -41,6 +41,7 @@ constexpr int kSide = 16;          // rows of the matrix instruction; a tile has
 constexpr int kMaxRows = 32;
 constexpr int kWaves = 4;          // waves of a workgroup of the experts' kernels
 constexpr int kFewMaxSlice = 128;  // most mlp columns of a workgroup
+constexpr int kParts = 3;          // bf16 numbers that the SwiGLU output is the sum of
 
 // ---------------------------------------------------------------- router
 
@@ -362,23 +363,26 @@ struct FewArgs {
 enum { kFused = 0, kFirst = 1, kSecond = 2 };
 constexpr int kMaxCuts = 8;
 
-template <int ROWS>
+// Each part holds what it uses, so that three workgroups of a cut product fit a compute unit on tiles of 32 rows too.
+template <int PART, int ROWS, bool MX>
 struct FewLds {
+  static constexpr int kRows = ROWS;
   union {
-    float red[kWaves][kSide][128];  // first product: each wave's sums; MXFP8: before and after, the wave's step
+    // first product: each wave's sums; MXFP8: before and after, the wave's step
+    float red[PART == kSecond && !MX ? 1 : kWaves][kSide][128];
     struct {                    // before both: the search for the tile
       int cnt[kMaxExperts], found[2], picks[64];
     };
   };
-  uint16_t a_hi[ROWS][kFewMaxSlice + 8], a_lo[ROWS][kFewMaxSlice + 8];
+  uint16_t a[PART == kFirst ? 1 : kParts][ROWS][PART == kFirst ? 8 : kFewMaxSlice + 8];
   int rows[kMaxRows];
   int64_t share[kMaxRows];  // where each row's share starts in part
 };
 
 // Which rows, of which expert. False: the routing has no such tile.
-template <bool PICK, int ROWS>
-__device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds<ROWS>& lds, int lane, int wave, int& e, int& nrows,
-                                         int& slot) {
+template <bool PICK, class Lds>
+__device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, Lds& lds, int lane, int wave, int& e, int& nrows, int& slot) {
+  constexpr int ROWS = Lds::kRows;
   e = -1;
   nrows = slot = 0;
   const int S = q.T * q.k;
@@ -409,20 +413,30 @@ __device__ __forceinline__ bool few_tile(const FewArgs& q, int tile, FewLds<ROWS
   return e >= 0;
 }
 
-// Row r, column n of the second product's left operand. It enters as the sum of two bf16 numbers, 16 bits of it: the
-// matrix cores are idle most of the time, so the layer's bf16 rounding of a is not needed here.
-template <int ROWS>
-__device__ __forceinline__ void few_set_a(FewLds<ROWS>& lds, int r, int n, float gate, float up) {
-  const float a = silu_f(gate) * up;
-  const uint16_t hi = (uint16_t)pack_bf16x2(a, 0.0f);
-  lds.a_hi[r][n] = hi;
-  // past bf16's range the second number is 0: inf - inf would make the row NaN
-  lds.a_lo[r][n] = (hi & 0x7f80) == 0x7f80 ? 0 : (uint16_t)pack_bf16x2(a - bf16_to_f32(hi), 0.0f);
+// silu(g) = g * sigmoid(g) to a few steps of fp32, with no exponential past fp32's range.
+__device__ __forceinline__ float few_silu(float g) {
+  const float e = expf(-__builtin_fabsf(g));
+  return (g < 0 ? g * e : g) / (1.0f + e);
+}
+
+// Row r, column n of the second product's left operand. It enters as the sum of three bf16 numbers, which is all of
+// fp32's 24 bits: the matrix cores are idle most of the time, so nothing is rounded here. (Two of them, 16 bits, left y on
+// the other side of a rounding in one of a thousand elements: 1.3e-4 between y and an fp32 layer's, relative.)
+template <class Lds>
+__device__ __forceinline__ void few_set_a(Lds& lds, int r, int n, float gate, float up) {
+  float a = few_silu(gate) * up;
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    const uint16_t v = (uint16_t)pack_bf16x2(a, 0.0f);
+    lds.a[p][r][n] = v;
+    // past bf16's range the others are 0: inf - inf would make the row NaN
+    a = (v & 0x7f80) == 0x7f80 ? 0.0f : a - bf16_to_f32(v);
+  }
 }
 
 // The waves' sums of 64 gate and 64 up columns of rows r0.. -> SwiGLU -> a's columns s0...
-template <int ROWS>
-__device__ __forceinline__ void few_swiglu(FewLds<ROWS>& lds, int nrows, int r0, int s0) {
+template <class Lds>
+__device__ __forceinline__ void few_swiglu(Lds& lds, int nrows, int r0, int s0) {
   for (int i = threadIdx.x; i < kSide * 64; i += kWaves * 64) {
     const int r = i >> 6, n = i & 63;
     float gate = 0, up = 0;
@@ -438,8 +452,8 @@ __device__ __forceinline__ void few_swiglu(FewLds<ROWS>& lds, int nrows, int r0,
 }
 
 // kFirst: the waves' sums to hpart.
-template <int ROWS>
-__device__ __forceinline__ void few_store_h(const FewArgs& q, const FewLds<ROWS>& lds, int nrows, int r0, int sl) {
+template <class Lds>
+__device__ __forceinline__ void few_store_h(const FewArgs& q, const Lds& lds, int nrows, int r0, int sl) {
   for (int i = threadIdx.x; i < min(kSide, nrows - r0) * 128; i += kWaves * 64) {
     const int r = i >> 7, n = i & 127;
     float h = 0;
@@ -450,11 +464,11 @@ __device__ __forceinline__ void few_store_h(const FewArgs& q, const FewLds<ROWS>
 }
 
 // kSecond: hpart -> SwiGLU -> a.
-template <int ROWS>
-__device__ __forceinline__ void few_load_h(const FewArgs& q, FewLds<ROWS>& lds, int nrows, int sl) {
+template <class Lds>
+__device__ __forceinline__ void few_load_h(const FewArgs& q, Lds& lds, int nrows, int sl) {
   const int n = threadIdx.x & 63;
 #pragma unroll
-  for (int it = 0; it < ROWS / kWaves; ++it) {
+  for (int it = 0; it < Lds::kRows / kWaves; ++it) {
     if (it * kWaves >= nrows) continue;  // rows past the last: their results are not used
     const int r = it * kWaves + (threadIdx.x >> 6);
     const float* h = q.hpart + ((int64_t)lds.rows[r < nrows ? r : 0] * q.ns + sl) * q.cuts * 128 + n;
@@ -475,16 +489,18 @@ __device__ __forceinline__ void few_load_h(const FewArgs& q, FewLds<ROWS>& lds, 
 
 __device__ __forceinline__ const char* bytes(const void* p) { return static_cast<const char*>(p); }
 
+// The second product alone runs three workgroups a compute unit on tiles of 32 rows too, though three registers of the 172
+// it would take are then kept in memory: 64 tokens, top-1 of 4, emb 4096, mlp 2048: 74.5 us against 79.5 with two.
 template <int PART, bool WIDE, bool PICK, int R>
-__global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kernel(FewArgs q) {
+__global__ __launch_bounds__(kWaves * 64, R == 1 || PART == kSecond ? 3 : 2) void few_experts_kernel(FewArgs q) {
   constexpr int kRows = R * kSide;
-  __shared__ __align__(16) FewLds<kRows> lds;
+  __shared__ __align__(16) FewLds<PART, kRows, false> lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int emb = q.emb, mlp = q.mlp;
   const int tile = blockIdx.x / q.ns, sl = blockIdx.x - tile * q.ns;
   int e, nrows, slot;
-  if (!few_tile<PICK, kRows>(q, tile, lds, lane, wave, e, nrows, slot)) return;
+  if (!few_tile<PICK>(q, tile, lds, lane, wave, e, nrows, slot)) return;
   const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
   // lanes past the last row compute on the first one; their rows of the results are not used
   uint32_t xlane[R];
@@ -564,10 +580,10 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
     }
   }
 #pragma unroll
-  for (int u = 0; u < (WIDE ? 2 : 1); ++u) {
+  for (int u = 0; u < (PART == kSecond ? 0 : WIDE ? 2 : 1); ++u) {
 #pragma unroll
     for (int m = 0; m < R; ++m) {
-      if (PART == kSecond || 64 * u >= width) continue;
+      if (64 * u >= width) continue;
       if (u || m) __syncthreads();  // the sums before have been read
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -594,17 +610,18 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
     for (int kk = 0; kk < width; kk += 64) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        bf16x8_t ah[R], al[R];
+        bf16x8_t a[R][kParts];
 #pragma unroll
-        for (int m = 0; m < R; ++m) {
-          ah[m] = as_bf16(ld16(&lds.a_hi[m * kSide + c][kk + 32 * u + 8 * g]));
-          al[m] = as_bf16(ld16(&lds.a_lo[m * kSide + c][kk + 32 * u + 8 * g]));
-        }
+        for (int m = 0; m < R; ++m)
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) a[m][p] = as_bf16(ld16(&lds.a[p][m * kSide + c][kk + 32 * u + 8 * g]));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const bf16x8_t b = st[u].col(j);
 #pragma unroll
-          for (int m = 0; m < R; ++m) acc[m][j] = mfma(al[m], b, mfma(ah[m], b, acc[m][j]));
+          for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int m = 0; m < R; ++m) acc[m][j] = mfma(a[m][p], b, acc[m][j]);
         }
         load(st[u], u, nullptr);
       }
@@ -631,7 +648,7 @@ __global__ __launch_bounds__(kWaves * 64, R == 1 ? 3 : 2) void few_experts_kerne
 template <int PART, bool PICK, int R>
 __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs q) {
   constexpr int kRows = R * kSide;
-  __shared__ __align__(16) FewLds<kRows> lds;
+  __shared__ __align__(16) FewLds<PART, kRows, true> lds;
   __shared__ uint32_t scale[kWaves][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -644,7 +661,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   }
   const int tile = b / q.ns, sl = (b - tile * q.ns + (q.slice == 64 ? 0 : tile)) % q.ns;
   int e, nrows, slot;
-  if (!few_tile<PICK, kRows>(q, tile, lds, lane, wave, e, nrows, slot)) return;
+  if (!few_tile<PICK>(q, tile, lds, lane, wave, e, nrows, slot)) return;
   const int m0 = sl * q.slice, width = min(q.slice, mlp - m0);
   const bool narrow = width == 64;  // of the second product's steps
   uint32_t xlane[R];
@@ -790,12 +807,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
   }
   if constexpr (PART == kFirst) return;
 
-  const auto a_of = [&](int k, bf16x8_t (&hi)[R], bf16x8_t (&lo)[R]) {
+  // acc[.][j] += a times v
+  const auto multiply = [&](const bf16x8_t (&a)[R][kParts], bf16x8_t v, int j) {
 #pragma unroll
-    for (int m = 0; m < R; ++m) {
-      hi[m] = as_bf16(ld16(&lds.a_hi[m * kSide + c][k]));
-      lo[m] = as_bf16(ld16(&lds.a_lo[m * kSide + c][k]));
-    }
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int m = 0; m < R; ++m) acc[m][j] = mfma(a[m][p], v, acc[m][j]);
+  };
+  const auto a_of = [&](int k, bf16x8_t (&a)[R][kParts]) {
+#pragma unroll
+    for (int m = 0; m < R; ++m)
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) a[m][p] = as_bf16(ld16(&lds.a[p][m * kSide + c][k]));
   };
   const auto store = [&](int n0) {
     wave_lds_fence();  // `share` is read again, not kept in registers
@@ -822,13 +845,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
         for (int p = 0; p < 2; ++p) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            bf16x8_t ah[R], al[R];
-            a_of(64 * p + 16 * g + 8 * h, ah, al);
+            bf16x8_t a[R][kParts];
+            a_of(64 * p + 16 * g + 8 * h, a);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const bf16x8_t v = mx_values(codes(t, p), h, code_of(scale[wave][p][4 * c + t]));
-#pragma unroll
-              for (int m = 0; m < R; ++m) acc[m][4 * u + t] = mfma(al[m], v, mfma(ah[m], v, acc[m][4 * u + t]));
+              multiply(a, mx_values(codes(t, p), h, code_of(scale[wave][p][4 * c + t])), 4 * u + t);
             }
           }
         }
@@ -848,13 +869,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_experts_mx_kernel(FewArgs 
           wave_lds_fence();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            bf16x8_t ah[R], al[R];
-            a_of(16 * g + 8 * h, ah, al);
+            bf16x8_t a[R][kParts];
+            a_of(16 * g + 8 * h, a);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const bf16x8_t v = mx_values(st[u].v[j], h, code_of(scale[wave][j >> 2][4 * c + (j & 3)]));
-#pragma unroll
-              for (int m = 0; m < R; ++m) acc[m][j] = mfma(al[m], v, mfma(ah[m], v, acc[m][j]));
+              multiply(a, mx_values(st[u].v[j], h, code_of(scale[wave][j >> 2][4 * c + (j & 3)])), j);
             }
           }
           store(n0 + u * nstride);
