@@ -603,9 +603,8 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* shape, const moe_bf16_t* dy, const float
  *  hold -inf to disable an expert); topk_idx [T, k] int32 and topk_w [T, k]
  *  fp32 are outputs: the k largest of the logits x . wr + bias in descending
  *  order, ties to the lower id, and their softmax. Logits are summed and
- *  compared in 64 bits, to 2^-44 of their size (moe_route's are a chain of
- *  fp32 additions, so that picks may differ where two logits lie within its
- *  rounding). A NaN logit counts as less than -inf; a pick of either has
+ *  compared in 64 bits (moe_route's are a chain of fp32 additions, so that
+ *  picks may differ where two logits lie within its rounding). A NaN logit counts as less than -inf; a pick of either has
  *  weight 0, but a token whose logits are all NaN has NaN weights.
  *  wr NULL: topk_idx and topk_w are inputs (from moe_route, moe_route_scored
  *  or the caller), bias is NULL. A pick whose id lies outside [0, E) takes no

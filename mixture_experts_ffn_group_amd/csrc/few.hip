@@ -46,7 +46,8 @@ constexpr int kParts = 3;          // bf16 numbers that the SwiGLU output is the
 // ---------------------------------------------------------------- router
 
 // logits[split][t][e] = sum over the split's rows of x[t, i] wr[i, e]. The products (8 + 24 bits) are exact in
-// fp64 and the sums are off by 2^-53 a step, so picks are those of exact arithmetic but for ties to 2^-44.
+// fp64 and the sums are off by 2^-53 a step, so picks are those of exact arithmetic but where logits lie
+// within that.
 // A wave takes 16 experts and 64 rows of emb at a time, all of whose loads are in flight at once (the kernel is one
 // memory latency long). v_mfma_f64_16x16x4 has A[i = lane%16][k = lane/16], B[k = lane/16][j = lane%16] and
 // D[i = 4r + lane/16][j = lane%16]; step i of the 16 takes row 16 (lane/16) + i of the 64.
@@ -105,18 +106,31 @@ __global__ __launch_bounds__(kLogitWaves * 64) void few_logits_kernel(int T, int
   }
 }
 
-// Order-preserving 64-bit key of expert e's logit: larger logit, larger key, -0 like +0, NaN below -inf; the low 8 bits
-// give equal logits (to 2^-44) to the lower id. 0 is no key.
-constexpr uint64_t kNanKey = 0x100;
-__device__ __forceinline__ uint64_t pick_key(double v, int e) {
-  if (v != v) return kNanKey | (uint64_t)(255 - e);
+// Order-preserving key of a logit, all 64 bits of it: larger logit, larger key, -0 like +0, NaN below -inf. 0 is no key.
+constexpr uint64_t kNanKey = 1;
+__device__ __forceinline__ uint64_t pick_key(double v) {
+  if (v != v) return kNanKey;
   if (v == 0) v = 0;
   const uint64_t u = (uint64_t)__double_as_longlong(v);
-  return (((u >> 63) ? ~u : (u | 0x8000000000000000ull)) & ~0xffull) | (uint64_t)(255 - e);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 __device__ __forceinline__ double pick_value(uint64_t k) {
-  if (k < 2 * kNanKey) return __builtin_nan("");
-  return __longlong_as_double((long long)(((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k) & ~0xffull));
+  if (k <= kNanKey) return __builtin_nan("");
+  return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+}
+// The lane's four keys in descending order; equal ones stay in theirs, by id (neighbours change places only).
+__device__ __forceinline__ void sort_picks(uint64_t (&key)[4], int (&id)[4]) {
+#pragma unroll
+  for (int last = 3; last > 0; --last) {
+#pragma unroll
+    for (int a = 0; a < last; ++a) {
+      const bool sw = key[a + 1] > key[a];
+      const uint64_t hi = sw ? key[a + 1] : key[a], lo = sw ? key[a] : key[a + 1];
+      const int first = sw ? id[a + 1] : id[a], second = sw ? id[a] : id[a + 1];
+      key[a] = hi, key[a + 1] = lo;
+      id[a] = first, id[a + 1] = second;
+    }
+  }
 }
 // Largest value of the wave, in every lane: the rows' maxima meet in scalar registers.
 __device__ __forceinline__ uint32_t wave_max_fused(uint32_t v) {
@@ -149,27 +163,37 @@ __device__ __forceinline__ void few_pick(int T, int E, int k, int splits, int t,
     }
   }
   uint64_t key[4];
+  int id[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = e < E ? pick_key(bias ? sum[i] + (double)bias[e] : sum[i], e) : 0;
+    id[i] = lane + 64 * i;
+    key[i] = id[i] < E ? pick_key(bias ? sum[i] + (double)bias[id[i]] : sum[i]) : 0;
   }
-  sort_desc(key);
+  if (E > 64) sort_picks(key, id);
   uint64_t mine = 0;
+  pick = 0;
   for (int j = 0; j < k; ++j) {
     const uint32_t hi = (uint32_t)(key[0] >> 32), lo = (uint32_t)key[0];
     const uint32_t mh = wave_max_fused(hi);
     uint64_t m = __ballot(hi == mh);
-    if (m & (m - 1)) {  // several lanes, seldom: the low halves differ, if only in the id
+    if (m & (m - 1)) {  // several lanes, seldom
       const uint32_t ml = wave_max_fused(hi == mh ? lo : 0u);
-      m = __ballot(hi == mh && lo == ml);
+      const bool top = hi == mh && lo == ml;
+      m = __ballot(top);
+      if (m & (m - 1)) {  // equal logits: the lowest id
+        const uint32_t low = wave_max_fused(top ? 256u - (uint32_t)id[0] : 0u);
+        m = __ballot(top && 256u - (uint32_t)id[0] == low);
+      }
     }
     const int l = __builtin_ctzll(m);
     const uint32_t ml = (uint32_t)__builtin_amdgcn_readlane((int)lo, l);
-    if (lane == l) key[0] = key[1], key[1] = key[2], key[2] = key[3], key[3] = 0;
-    if (lane == j) mine = (uint64_t)mh << 32 | ml;
+    const int e = __builtin_amdgcn_readlane(id[0], l);
+    if (lane == l) {
+      key[0] = key[1], key[1] = key[2], key[2] = key[3], key[3] = 0;
+      id[0] = id[1], id[1] = id[2], id[2] = id[3];
+    }
+    if (lane == j) mine = (uint64_t)mh << 32 | ml, pick = e;
   }
-  pick = lane < k ? 255 - (int)(mine & 0xff) : 0;
   logit = lane < k ? pick_value(mine) : -__builtin_inf();
 }
 

@@ -49,3 +49,25 @@ def test_swiglu_output_enters_the_down_product_in_24_bits(T, emb, mlp, mx):
     ref = (h[:, :mlp] * h[:, mlp:]) @ wo[0]  # exact in 64 bits
     assert np.array_equal(ref, ref.astype(np.float32)) and (ref != 0).any()
     assert np.array_equal(fu.f64(y), ref)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 64, 8), (8, 200, 8), (20, 256, 13), (64, 70, 64)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_logits_are_compared_in_all_64_bits(T, E, k, bias):
+    """Logits +-1 + d 2^-50, d = 0..7, are exact in 64 bits: the larger d is picked first, equal ones by id."""
+    gen = torch.Generator().manual_seed(T)
+    emb, mlp = 64, 64
+    x, wr = torch.zeros((T, emb)), torch.zeros((emb, E))
+    x[:, 0] = torch.randint(0, 2, (T,), generator=gen).float() * 2 - 1
+    x[:, 1] = 1
+    d = torch.randint(0, 8, (E,), generator=gen).float() * 2.0 ** -50
+    wr[0], b = 1, None
+    if bias:
+        b = d
+    else:
+        wr[1] = d
+    ri, _ = fu.route(fu.f64(x), fu.f64(wr), fu.f64(b), k)
+    wi, wo = torch.zeros((E, emb, 2 * mlp)).bfloat16().to(DEV), torch.zeros((E, mlp, emb)).bfloat16().to(DEV)
+    y, idx, w = moe.ffn_fwd_few(x.bfloat16().to(DEV), wi, wo, k, wr=wr.to(DEV), bias=None if b is None else b.to(DEV))
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert np.abs(fu.f64(w) - 1 / k).max() <= 2 * fu.U / k and not y.any()
