@@ -26,6 +26,8 @@
 // read again: 64 experts of emb 7168, mlp 2048 take 932 us with one row each, 1076 with
 // eight), and workgroups that do not come out even over the compute units (6.2 TB/s
 // with 512 of them, 5.8 with 640).
+#include <math.h>
+
 #include <type_traits>
 
 #include "common.h"
@@ -975,13 +977,20 @@ FewPlan few_plan(int64_t T, int emb, int mlp, int E, int k, bool mx) {
   // 8192), 32 tokens: 64 / 67 and MXFP8 53 / 67, 48 tokens: 97 / 74 and 80 / 63.
   p.rows = T > 2 * kSide && S >= 12 * E ? 2 * kSide : kSide;
   // Slices of 128 columns are read in longer runs and leave half the shares, slices of 64 give twice the workgroups, of
-  // which three fit a compute unit, 768 in all. us, slices of 64 against 128, by the workgroups that 128 gives: (emb 2048,
-  // mlp 768) 96: 44 / 56, 144: 67 / 61, 204: 62 / 58, 258: 87 / 95 (a second one for some compute units), 354: 99 / 104;
-  // (emb 7168, mlp 2048) 256: 250 / 226, 272: 320 / 333, 352: 362 / 355, 384: 383 / 368, 400: 450 / 371 (64 gives more
-  // than fit), 448: 474 / 403; on MXFP8 weights, whose rows of wo are only 64 bytes long in slices of 64: 96: 37 / 48, 144:
-  // 50 / 50, 288: 81 / 72, 576: 96 / 82.
-  const int64_t wide = (int64_t)experts * ((mlp + 127) / 128);
-  p.slice = wide >= 144 && (mx || wide <= 256 || wide >= 384) ? 128 : 64;
+  // which three fit a compute unit, 768 in all. What counts are the workgroups with work: of the experts that T tokens of k
+  // picks are expected to reach (they are not known here, and min(S, E) is more: 8 tokens of top-8 of 128 reach about 52).
+  // us, slices of 64 against 128, by the workgroups that 128 gives these experts. emb 2048, mlp 768 or 1408: 174: 65 / 59,
+  // 212: 73 / 70, 229: 72 / 71, 247: 84.6 / 86.0 (the picks scatter: past 256 some compute units get a second one), 273: 91
+  // / 98, 279: 96 / 105, 309: 101 / 108, 314: 103 / 112, 351: 108 / 110, 365: 110 / 113, 384: 117 / 112 (64 gives more than
+  // fit), 414: 125 / 116, 494: 145 / 133. emb 4096 and more, where a longer run counts for more: 240: 252 / 218, 279: 192 /
+  // 203, 310: 203 / 207, 321: 265 / 260, 338: 357 / 352, 355: 282 / 274, 424: 424 / 384. On MXFP8 weights, whose rows of wo
+  // are only 64 bytes long in slices of 64, by the most workgroups that 128 can give: 96: 37 / 48, 144: 50 / 50, 288: 81 /
+  // 72, 576: 96 / 82.
+  const int n128 = (mlp + 127) / 128;
+  const int64_t wide = (int64_t)experts * n128;
+  const double reached = E * (1 - pow(1 - (double)k / E, (double)T)) * n128;
+  const bool one = reached <= (emb >= 4096 ? 256 : 244), past = reached >= (emb >= 4096 ? 320 : 376);
+  p.slice = wide >= 144 && (mx || one || past) ? 128 : 64;
   p.ns = (mlp + p.slice - 1) / p.slice;
   // Few workgroups: the products in kernels of their own, cut along emb (in up to four, up to eight where that leaves few
   // workgroups still) and along the output columns. us fused and cut in four, by the workgroups fused: 8 (emb 7168, mlp
