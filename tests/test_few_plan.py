@@ -6,7 +6,7 @@ import mixture_experts_ffn_group_amd as moe
 
 def _slices(T, emb, mlp, E, k):
     run = -(-emb // 4096) * 64  # rows of emb of a router wave; four waves a workgroup
-    logits = -(-emb // (4 * run)) * T * E * 8
+    logits = -(-(-(-emb // (4 * run)) * T * E * 8) // 256) * 256
     return (moe.workspace_bytes_few(T, emb, mlp, E, k) - logits) / (T * k * emb * 4)
 
 
