@@ -594,18 +594,19 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* shape, const moe_bf16_t* dy, const float
 /*
  * moe_ffn_fwd_few -- the whole layer for a few tokens (a decode step), T <= 64:
  *  router, experts and combine, with no permute and no copy of rows: the
- *  weights of each expert that has a token are read once for up to 16 of its
- *  tokens. Three kernels (router, experts, sum of their shares) for T <= 8 and
- *  T*k <= 64, the first left out on a given routing; one more for more tokens
- *  (the picks), and one more where experts and slices are few (the products
- *  apart).
+ *  weights of each expert that has a token are read once for 16 of its tokens
+ *  (32 where experts have many). Three kernels (router, experts, sum of their
+ *  shares) for T <= 8 and T*k <= 64, the first left out on a given routing; one
+ *  more for more tokens (the picks), and one more where experts and slices are
+ *  few (the products apart).
  *  wr [emb, E] fp32: the layer routes x itself; bias [E] fp32 or NULL (may
  *  hold -inf to disable an expert); topk_idx [T, k] int32 and topk_w [T, k]
  *  fp32 are outputs: the k largest of the logits x . wr + bias in descending
  *  order, ties to the lower id, and their softmax. Logits are summed and
  *  compared in 64 bits (moe_route's are a chain of fp32 additions, so that
- *  picks may differ where two logits lie within its rounding). A NaN logit counts as less than -inf; a pick of either has
- *  weight 0, but a token whose logits are all NaN has NaN weights.
+ *  picks may differ where two logits lie within its rounding). A NaN logit
+ *  counts as less than -inf; a pick of either has weight 0, but a token whose
+ *  logits are all NaN has NaN weights.
  *  wr NULL: topk_idx and topk_w are inputs (from moe_route, moe_route_scored
  *  or the caller), bias is NULL. A pick whose id lies outside [0, E) takes no
  *  part. An expert may be picked twice by a token here.
@@ -619,7 +620,10 @@ int moe_ffn_bwd_ckpt(const moe_shape_t* shape, const moe_bf16_t* dy, const float
  *  wo_scales as in moe_ffn_fwd_mx). x and the SwiGLU output are not
  *  quantized, the weights enter at the values their codes stand for, and sums
  *  are fp32, so the result differs from moe_ffn_fwd_mx's by that one's
- *  activation quantization. Scale codes above 246 (weights past 2^119) are unspecified.
+ *  activation quantization. Weights of scale codes 0 to 2 (blocks whose largest
+ *  weight is below 2^-116) enter rounded to multiples of 2^-133, the smallest
+ *  bf16 number; scale codes above 246 (block maxima of 2^128 and more) are
+ *  unspecified.
  */
 size_t moe_workspace_bytes_few(const moe_shape_t* shape);
 int moe_ffn_fwd_few(const moe_shape_t* shape, const moe_bf16_t* x, const float* wr, const float* bias,

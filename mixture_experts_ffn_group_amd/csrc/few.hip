@@ -2,7 +2,7 @@
 // combine without the permute and the 256-row tiles of the grouped GEMMs.
 //
 // With T <= 64 tokens the layer is a stream over the weights of the experts that
-// have a token: 6 * emb * mlp bytes each in bf16, 3.1 in MXFP8, for 2 to 2 * T
+// have a token: 6 * emb * mlp bytes each in bf16, 3.2 in MXFP8, for 2 to 2 * T
 // multiply-adds an element. So the kernels are built around the weight loads: 16
 // bytes a lane and whole 128-byte lines, read once for all (up to 16 or 32) rows of
 // the expert, two steps of 8 KB a wave in flight at all times. bf16 goes from its
@@ -48,8 +48,7 @@ constexpr int kParts = 3;          // bf16 numbers that the SwiGLU output is the
 // ---------------------------------------------------------------- router
 
 // logits[split][t][e] = sum over the split's rows of x[t, i] wr[i, e]. The products (8 + 24 bits) are exact in
-// fp64 and the sums are off by 2^-53 a step, so picks are those of exact arithmetic but where logits lie
-// within that.
+// fp64 and the sums are off by 2^-53 a step, so picks are those of exact arithmetic but where logits lie within that.
 // A wave takes 16 experts and 64 rows of emb at a time, all of whose loads are in flight at once (the kernel is one
 // memory latency long). v_mfma_f64_16x16x4 has A[i = lane%16][k = lane/16], B[k = lane/16][j = lane%16] and
 // D[i = 4r + lane/16][j = lane%16]; step i of the 16 takes row 16 (lane/16) + i of the 64.
@@ -266,8 +265,8 @@ struct StepBf16 {
 // goes through the wave's own 8 KB of LDS, row 16t + c for column 4c + t, from where lane (g, c) reads codes 16(4p + g)...
 // Within a row the 16-byte units are stored at u ^ (row & 7), so that both the writes and the reads spread over the banks;
 // the swizzle is in the address the lane loads from. `scale` holds the dwords of the 64 columns for the step's two
-// 64-blocks. Codes convert to bf16 exactly (3 bits of mantissa; a scale code below 3, which only blocks of subnormal
-// weights have, or above 246 leaves bf16's range).
+// 64-blocks. Codes convert to bf16 exactly (3 bits of mantissa), but to multiples of 2^-133 below scale code 3, which only
+// blocks of weights below 2^-116 have; a scale code above 246 leaves bf16's range.
 // Slices of 64 mlp columns give the second product rows of 64 bytes: 128 columns by 64 values of K then, in the
 // operand's own order (v[j]: column 64 (j >> 2) + 4c + (j & 3), codes 16g..), through plain loads.
 struct StepMx {

@@ -5,6 +5,7 @@ import torch
 
 import few_util as fu
 import mixture_experts_ffn_group_amd as moe
+import oracle
 from test_gpu_few import _mx_values
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +72,25 @@ def test_logits_are_compared_in_all_64_bits(T, E, k, bias):
     y, idx, w = moe.ffn_fwd_few(x.bfloat16().to(DEV), wi, wo, k, wr=wr.to(DEV), bias=None if b is None else b.to(DEV))
     assert np.array_equal(idx.cpu().numpy(), ri)
     assert np.abs(fu.f64(w) - 1 / k).max() <= 2 * fu.U / k and not y.any()
+
+
+@pytest.mark.parametrize("code", [0, 1, 2, 3, 7, 12, 127, 246])
+def test_mx_weights_of_every_scale(code):
+    """All positive codes on one scale, one to a column: exact, but rounded to multiples of 2^-133 (half a step off at
+    most) where the scale is below 2^-124. y = 64 x w, x a power of two: nothing else is rounded."""
+    emb = mlp = 128
+    wi = torch.zeros((1, emb, 2 * mlp))
+    wi[0, 32, :mlp] = 64  # the gate, in a block of its own: silu(64) = 64
+    wq = moe.mx_quantize_expert_weights(wi.bfloat16().to(DEV), torch.eye(emb)[None].bfloat16().to(DEV))
+    wq["wi_codes"][0, mlp:, 0] = (torch.arange(mlp) % 127).to(torch.uint8).to(DEV)  # 127 is a NaN
+    wq["wi_scales"][0, 0, mlp:, 0] = code
+    x = torch.zeros((1, emb))
+    x[0, 0], x[0, 32] = 2.0 ** (100 if code < 64 else -100), 1
+    idx, w = torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.ones((1, 1), device=DEV)
+    y = fu.f64(moe.ffn_fwd_few_mx(x.bfloat16().to(DEV), wq, topk_idx=idx, topk_w=w)[0])[0]
+    v = np.array([oracle.e4m3_value(c % 127) for c in range(mlp)]) * 2.0 ** (code - 127)
+    got = y / (64 * float(x[0, 0]))
+    if code < 3:
+        assert np.abs(got - v).max() == 2.0 ** -134 and np.array_equal(got, np.round(v * 2.0 ** 133) * 2.0 ** -133)
+    else:
+        assert np.array_equal(got, v) and got[126] > 0
