@@ -18,12 +18,12 @@
 // atomics, whose order changes results.
 //
 // Measured, us, kernels alone (weight bytes per second): one token, top-8 of 128, emb
-// 2048, mlp 768: 3.4 + 13.6 + 8.2 + 4.1, launch and latency of four kernels; 4 tokens
-// with 8 picks each, emb 7168, mlp 2048: experts 409 (6.5 TB/s), sum 5; 64 tokens,
+// 2048, mlp 768: 3.5 + 13.8 + 8.4 + 4.2, launch and latency of four kernels; 4 tokens
+// with 8 picks each, emb 7168, mlp 2048: experts 412 (6.5 TB/s), sum 5; 64 tokens,
 // top-8 of 128, emb 2048, mlp 768: 7 + 5 + 203 (5.9 TB/s) + 6; 19 tokens with 8 picks
-// each on MXFP8, emb 7168, mlp 2048: 6 + 5 + 474 (5.8 TB/s) + 13. What holds the long
+// each on MXFP8, emb 7168, mlp 2048: 6 + 5 + 477 (5.8 TB/s) + 13. What holds the long
 // ones below a read's 7.2 TB/s: the shares (S * mlp / 128 * emb * 4 bytes, written and
-// read again: 64 experts of emb 7168, mlp 2048 take 932 us with one row each, 1076 with
+// read again: 64 experts of emb 7168, mlp 2048 take 929 us with one row each, 1074 with
 // eight), and workgroups that do not come out even over the compute units (6.2 TB/s
 // with 512 of them, 5.8 with 640).
 #include <math.h>
