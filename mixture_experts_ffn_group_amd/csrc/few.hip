@@ -445,8 +445,9 @@ __device__ __forceinline__ float few_silu(float g) {
 }
 
 // Row r, column n of the second product's left operand. It enters as the sum of three bf16 numbers, which is all of
-// fp32's 24 bits: the matrix cores are idle most of the time, so nothing is rounded here. (Two of them, 16 bits, left y on
-// the other side of a rounding in one of a thousand elements: 1.3e-4 between y and an fp32 layer's, relative.)
+// fp32's 24 bits: the matrix cores are idle most of the time, so nothing is rounded here. (Elements of y that are not the
+// rounded 64-bit result, 64 tokens of emb 2048, mlp 768, top-8 of 128: 41 of 131072; fp32 operations one after another:
+// 66; with two numbers, 16 bits: 340.)
 template <class Lds>
 __device__ __forceinline__ void few_set_a(Lds& lds, int r, int n, float gate, float up) {
   float a = few_silu(gate) * up;
